@@ -8,8 +8,10 @@ PyTorch is used for device memory (outputs the caller does not pass are
 allocated with torch) and streams.
 """
 import ctypes
+import functools
 import os
 
+import numpy as np
 import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -25,11 +27,17 @@ MAXSIM_ERR_HIP = 6
 MAXSIM_ERR_SCRATCH = 7
 MAXSIM_F16 = 0
 MAXSIM_BF16 = 1
+MAXSIM_F32 = 2
+MAXSIM_I8 = 3
+MAXSIM_E4M3 = 4
+QBLOCK = 128  # values that share a scale
 
-# name -> (restype, argtypes); must match include/maxsim.h
+# name -> (restype, argtypes); must match include/maxsim.h and include/maxsim_encoder.h
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
+_F32 = ctypes.c_float
+_F64 = ctypes.c_double
 SIGNATURES = {
     "maxsim_fwd": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P]),
     "maxsim_fwd_varlen": (ctypes.c_int, [_P, _P, _P, _I32, _I32, _I32, _I64, _I32, _I32, _I32, _P, _P, _P]),
@@ -60,6 +68,16 @@ SIGNATURES = {
     "maxsim_two_stage_topk": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _I32, _I32, _I32, _I32, _I64, _I32, _I32,
                                              _I32, _I32, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "maxsim_status_string": (ctypes.c_char_p, [ctypes.c_int]),
+    "maxsim_rmsnorm_fwd": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I32, _I32, _I32, _I32, _F32, _I32, _P, _I64, _P,
+                                          _P, _I64, _P, _P]),
+    "maxsim_rmsnorm_bwd_workspace_bytes": (ctypes.c_size_t, [_I32, _I32]),
+    "maxsim_rmsnorm_bwd": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _I32, _P, _I64, _I32, _I32, _I32, _P, _I64, _P,
+                                          _P, ctypes.c_size_t, _P]),
+    "maxsim_quant_fp8": (ctypes.c_int, [_P, _I64, _I32, _I32, _I32, _I32, _P, _I64, _P, _P, _I64, _P, _P]),
+    "maxsim_gemm_fp8_workspace_bytes": (ctypes.c_size_t, [_I32, _I32, _I32]),
+    "maxsim_gemm_fp8": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _P, _I32, _I32, _I32, _I32, _I32, _P, _I64, _P,
+                                       ctypes.c_size_t, _P]),
+    "maxsim_adamw": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _F64, _F64, _F64, _F64, _F64, _I32, _P, _P]),
 }
 
 
@@ -610,3 +628,439 @@ def maxsim_two_stage_topk(Q8, q_scale, D8, d_scale, Q16, D16, cu_seqlens, max_Ld
                                      workspace.numel(), _stream(Q8, stream))
     _check(st, "maxsim_two_stage_topk")
     return cand, cand8, top_idx, top_score
+
+
+# ---------------------------------------------------------------- the embedding head and its training step
+# (include/maxsim_encoder.h)
+
+_CODES = {torch.float16: MAXSIM_F16, torch.bfloat16: MAXSIM_BF16, torch.float32: MAXSIM_F32, torch.int8: MAXSIM_I8,
+          torch.float8_e4m3fn: MAXSIM_E4M3}
+
+
+def _on_its_device(f):
+    """Runs f on the device of its first argument, and on `stream` where one is given: what f allocates then belongs
+    to the stream that uses it."""
+
+    @functools.wraps(f)
+    def call(first, *args, stream=None, **kw):
+        dev = first.device
+        if dev.type != "cuda":
+            raise ValueError("%s: the tensors must be on the device" % f.__name__)
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError("%s: the stream is on %s, the tensors on %s" % (f.__name__, stream.device, dev))
+            with torch.cuda.stream(stream):
+                return f(first, *args, **kw)
+        if dev.index != torch._C._cuda_getDevice():
+            with torch.cuda.device(dev):
+                return f(first, *args, **kw)
+        return f(first, *args, **kw)
+
+    return call
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _code(dtype, allowed, name):
+    c = _CODES.get(dtype, -1)
+    if c not in allowed:
+        raise TypeError("%s may not be %s" % (name, dtype))
+    return c
+
+
+_FLOATS = (MAXSIM_F16, MAXSIM_BF16, MAXSIM_F32)
+
+
+def _rows(t, name, shape, dtype, dev):
+    """The pitch of t as rows of its last dimension; t has `shape` and `dtype` and lies on `dev`."""
+    if t.device != dev:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    width = shape[-1]
+    if t.is_contiguous():
+        return width
+    # rows one pitch apart through all leading dimensions, neighbours within a row
+    pitch, rows = None, 1
+    for d in range(len(shape) - 2, -1, -1):
+        if shape[d] == 1:
+            continue
+        if pitch is None:
+            pitch = t.stride(d)
+        elif t.stride(d) != pitch * rows:
+            raise ValueError("%s: the rows must be one pitch apart" % name)
+        rows *= shape[d]
+    if t.stride(-1) != 1 and width > 1:
+        raise ValueError("%s: the values of a row must be neighbours" % name)
+    if pitch is None:
+        return width
+    if pitch < width:
+        raise ValueError("%s: the rows overlap" % name)
+    return pitch
+
+
+def _flat(t, name, n, dtype, dev):
+    """t holds n values of `dtype` back to back on `dev`."""
+    if t.device != dev:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must hold %d contiguous values" % (name, n))
+
+
+def _empty_e4m3(shape, dev):
+    """[..., width] e4m3 with rows a multiple of 16 bytes apart, as the product reads them."""
+    width = shape[-1]
+    pad = -width % 16
+    if pad == 0:
+        return torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
+    return torch.empty(tuple(shape[:-1]) + (width + pad,), dtype=torch.float8_e4m3fn, device=dev)[..., :width]
+
+
+def _row_count(shape):
+    n = 1
+    for s in shape[:-1]:
+        n *= s
+    return n
+
+
+def _gain(weight, H, dtype, dev):
+    if weight is None:
+        return None, MAXSIM_F32
+    if weight.dtype != dtype and weight.dtype != torch.float32:
+        raise TypeError("weight must be %s or float32, got %s" % (dtype, weight.dtype))
+    _flat(weight, "weight", H, weight.dtype, dev)
+    return weight.data_ptr(), _CODES[weight.dtype]
+
+
+@_on_its_device
+def maxsim_rmsnorm_fwd(x, weight=None, eps=1e-6, residual=None, out_dtype=None, with_rstd=False, y=None, scale=None,
+                       sum=None, rstd=None):
+    """RMS norm of the rows of x [..., H] (fp16, bf16, fp32), of x + residual where one is given.
+
+    out_dtype: x's (the default), float16, bfloat16, float32, int8 (a scale for each row: the operand of
+    maxsim_fwd_i8) or float8_e4m3fn (a scale for each 128 columns: the operand of maxsim_gemm_fp8).
+    Returns (y, scale or None, sum or None, rstd or None); sum = x + residual in x's type, rstd [...] fp32.
+    """
+    dev, shape = x.device, x.shape
+    H, R = shape[-1], _row_count(shape)
+    code = _code(x.dtype, _FLOATS, "x")
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    out = _code(out_dtype, (0, 1, 2, 3, 4), "out_dtype")
+    ldx = _rows(x, "x", shape, x.dtype, dev)
+    w, w_code = _gain(weight, H, x.dtype, dev)
+    ldr = lds = H
+    if residual is not None:
+        ldr = _rows(residual, "residual", shape, x.dtype, dev)
+        if sum is None:
+            sum = torch.empty(shape, dtype=x.dtype, device=dev)
+    if sum is not None:
+        lds = _rows(sum, "sum", shape, x.dtype, dev)
+    if y is None:
+        y = _empty_e4m3(shape, dev) if out == MAXSIM_E4M3 else torch.empty(shape, dtype=out_dtype, device=dev)
+    ldy = _rows(y, "y", shape, out_dtype, dev)
+    if out >= MAXSIM_I8:
+        want = shape[:-1] + (-(-H // QBLOCK),) if out == MAXSIM_E4M3 else shape[:-1]
+        if scale is None:
+            scale = torch.empty(want, dtype=torch.float32, device=dev)
+        else:
+            _flat(scale, "scale", R * (want[-1] if out == MAXSIM_E4M3 else 1), torch.float32, dev)
+    elif scale is not None:
+        raise ValueError("scale goes with an 8-bit output")
+    if rstd is not None:
+        _flat(rstd, "rstd", R, torch.float32, dev)
+    elif with_rstd:
+        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
+    st = _lib.maxsim_rmsnorm_fwd(x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, w, w_code,
+                                 R, H, code, eps, out, y.data_ptr(), ldy, None if scale is None else scale.data_ptr(),
+                                 None if sum is None else sum.data_ptr(), lds,
+                                 None if rstd is None else rstd.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "maxsim_rmsnorm_fwd")
+    return y, scale, sum, rstd
+
+
+def maxsim_rmsnorm_bwd_workspace_bytes(R, H):
+    return int(lib().maxsim_rmsnorm_bwd_workspace_bytes(R, H))
+
+
+@_on_its_device
+def maxsim_rmsnorm_bwd(dy, h, rstd, weight=None, dsum=None, with_dweight=True, dx=None, dweight=None, workspace=None):
+    """Backward of the norm.  dy [..., H] is the gradient of y, h the forward's sum (x without a residual), rstd its
+    rstd, dsum the gradient that arrives at sum itself.  Returns (dx, dweight [H] fp32 or None); dx is the gradient
+    of x and of residual alike."""
+    dev, shape = h.device, h.shape
+    H, R = shape[-1], _row_count(shape)
+    code = _code(h.dtype, _FLOATS, "h")
+    ldh = _rows(h, "h", shape, h.dtype, dev)
+    lddy = _rows(dy, "dy", shape, h.dtype, dev)
+    _flat(rstd, "rstd", R, torch.float32, dev)
+    w, w_code = _gain(weight, H, h.dtype, dev)
+    ldds = H if dsum is None else _rows(dsum, "dsum", shape, h.dtype, dev)
+    if dx is None:
+        dx = torch.empty(shape, dtype=h.dtype, device=dev)
+    lddx = _rows(dx, "dx", shape, h.dtype, dev)
+    nbytes = 0
+    if dweight is None and with_dweight:
+        dweight = torch.empty(H, dtype=torch.float32, device=dev)
+    elif dweight is not None:
+        _flat(dweight, "dweight", H, torch.float32, dev)
+    if dweight is not None:
+        if workspace is None:
+            workspace = torch.empty(max(16, _lib.maxsim_rmsnorm_bwd_workspace_bytes(R, H)), dtype=torch.uint8,
+                                    device=dev)
+        _need(workspace, "workspace", device=dev)
+        nbytes = workspace.numel() * workspace.element_size()
+    st = _lib.maxsim_rmsnorm_bwd(dy.data_ptr(), lddy, h.data_ptr(), ldh, rstd.data_ptr(), w, w_code,
+                                 None if dsum is None else dsum.data_ptr(), ldds, R, H, code, dx.data_ptr(), lddx,
+                                 None if dweight is None else dweight.data_ptr(),
+                                 None if workspace is None else workspace.data_ptr(), nbytes, _raw_stream(dev))
+    if st:
+        _check(st, "maxsim_rmsnorm_bwd")
+    return dx, dweight
+
+
+@_on_its_device
+def maxsim_quant_fp8(x, block_rows=1, rows=True, transposed=False):
+    """x [R, C] (fp16, bf16, fp32) in e4m3 with a scale for each 128 columns of a row (block_rows 1) or each
+    128 x 128 values (block_rows 128), for maxsim_gemm_fp8.  Returns (q [R, C], scale, qt [C, R], scale_t): qt is x
+    transposed, with a scale for each 128 of x's rows; rows / transposed say which of the two are made (else None)."""
+    if x.dim() != 2:
+        raise ValueError("x must be [R, C]")
+    dev = x.device
+    R, C = x.shape
+    code = _code(x.dtype, _FLOATS, "x")
+    ldx = _rows(x, "x", x.shape, x.dtype, dev)
+    if not rows and not transposed:
+        raise ValueError("neither rows nor transposed: nothing to make")
+    rb, cb = -(-R // QBLOCK), -(-C // QBLOCK)
+    q = scale = qt = scale_t = None
+    if rows:
+        q = _empty_e4m3((R, C), dev)
+        scale = torch.empty((R if block_rows == 1 else rb, cb), dtype=torch.float32, device=dev)
+    if transposed:
+        qt = _empty_e4m3((C, R), dev)
+        scale_t = torch.empty((C if block_rows == 1 else cb, rb), dtype=torch.float32, device=dev)
+    st = _lib.maxsim_quant_fp8(x.data_ptr(), ldx, R, C, code, block_rows,
+                               None if q is None else q.data_ptr(), -(-C // 16) * 16,
+                               None if scale is None else scale.data_ptr(),
+                               None if qt is None else qt.data_ptr(), -(-R // 16) * 16,
+                               None if scale_t is None else scale_t.data_ptr(), _raw_stream(dev))
+    if st:
+        _check(st, "maxsim_quant_fp8")
+    return q, scale, qt, scale_t
+
+
+def _operand(t, name, dev):
+    """The pitch of an e4m3 operand [rows, K]; every row is readable up to K rounded up to 16."""
+    rows, K = t.shape
+    ld = _rows(t, name, t.shape, torch.float8_e4m3fn, dev)
+    k16 = -(-K // 16) * 16
+    if ld < k16 and rows <= 1:
+        ld = k16
+    if K != k16 and rows > 0 and t.storage_offset() + (rows - 1) * ld + k16 > t.untyped_storage().nbytes():
+        raise ValueError("%s: rows of %d bytes must be readable up to %d" % (name, K, k16))
+    return ld
+
+
+def maxsim_gemm_fp8_workspace_bytes(M, N, K):
+    return int(lib().maxsim_gemm_fp8_workspace_bytes(M, N, K))
+
+
+@_on_its_device
+def maxsim_gemm_fp8(A, a_scale, B, b_scale, out_dtype=torch.bfloat16, out=None, workspace=None):
+    """A B^T of e4m3 A [M, K] and B [N, K] with a_scale [M, ceil(K/128)] and b_scale [N, ceil(K/128)] or
+    [ceil(N/128), ceil(K/128)] (a scale for 128 rows of B); fp32 sums, rounded once to out_dtype."""
+    dev = A.device
+    if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
+        raise ValueError("A [M, K] and B [N, K] must share K")
+    M, K = A.shape
+    N = B.shape[0]
+    lda, ldb = _operand(A, "A", dev), _operand(B, "B", dev)
+    kb = -(-K // QBLOCK)
+    _flat(a_scale, "a_scale", M * kb, torch.float32, dev)
+    block_rows = 1 if b_scale.shape[0] == N else QBLOCK
+    _flat(b_scale, "b_scale", -(-N // block_rows) * kb, torch.float32, dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    code = _code(out.dtype, _FLOATS, "out_dtype")
+    ldc = _rows(out, "out", (M, N), out.dtype, dev)
+    nbytes = _lib.maxsim_gemm_fp8_workspace_bytes(M, N, K)
+    if workspace is not None:
+        _need(workspace, "workspace", device=dev)
+        nbytes = workspace.numel() * workspace.element_size()
+    elif nbytes:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    st = _lib.maxsim_gemm_fp8(A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(), ldb, b_scale.data_ptr(), block_rows,
+                              M, N, K, code, out.data_ptr(), ldc, None if workspace is None else workspace.data_ptr(),
+                              nbytes, _raw_stream(dev))
+    if st:
+        _check(st, "maxsim_gemm_fp8")
+    return out
+
+
+_TENSOR = np.dtype([("param", np.uint64), ("grad", np.uint64), ("master", np.uint64), ("m", np.uint64),
+                    ("v", np.uint64), ("m_scale", np.uint64), ("v_scale", np.uint64), ("n", np.int64)])
+
+
+class AdamWTensors:
+    """The tensors that maxsim_adamw steps over: parameters (all fp16, bf16 or fp32), moments m and v, and for 16-bit
+    parameters fp32 masters that they are rounded from (optional).  Moments are fp32, or float8_e4m3fn with m_scales
+    and v_scales (fp32, one for each 128 values; v is then held as its square root).  zeros() makes them."""
+
+    def __init__(self, params, m, v, m_scales=None, v_scales=None, masters=None):
+        params = list(params)
+        if not params:
+            raise ValueError("no parameters")
+        self.device = dev = params[0].device
+        self.params, self.m, self.v = params, list(m), list(v)
+        self.m_scales = None if m_scales is None else list(m_scales)
+        self.v_scales = None if v_scales is None else list(v_scales)
+        self.masters = None if masters is None else list(masters)
+        self.param_code = _code(params[0].dtype, _FLOATS, "params")
+        self.state_code = _code(self.m[0].dtype if self.m else None, (MAXSIM_F32, MAXSIM_E4M3), "m")
+        if (self.state_code == MAXSIM_E4M3) != (m_scales is not None) or (m_scales is None) != (v_scales is None):
+            raise ValueError("m_scales and v_scales go with 8-bit moments")
+        if masters is not None and self.param_code == MAXSIM_F32:
+            raise ValueError("masters go with 16-bit parameters")
+        self.sizes = [p.numel() for p in params]
+        state = self.m[0].dtype
+        table = np.zeros(len(params), _TENSOR)
+        table["n"] = self.sizes
+
+        def put(field, tensors, dtype, per=1):
+            if len(tensors) != len(params):
+                raise ValueError("%s: %d tensors for %d parameters" % (field, len(tensors), len(params)))
+            for i, t in enumerate(tensors):
+                _flat(t, "%s[%d]" % (field, i), -(-self.sizes[i] // per), dtype, dev)
+                table[field][i] = t.data_ptr()
+
+        put("param", params, params[0].dtype)
+        put("m", self.m, state)
+        put("v", self.v, state)
+        if m_scales is not None:
+            put("m_scale", self.m_scales, torch.float32, QBLOCK)
+            put("v_scale", self.v_scales, torch.float32, QBLOCK)
+        if masters is not None:
+            put("master", self.masters, torch.float32)
+        self._table = table
+
+    @classmethod
+    def zeros(cls, params, state_dtype=torch.float32, masters=True):
+        """Moments at 0 for these parameters, and fp32 masters of 16-bit ones."""
+        params = list(params)
+        moments = lambda: [torch.zeros(p.numel(), dtype=torch.float32, device=p.device).to(state_dtype)  # noqa: E731
+                           for p in params]
+        scales = lambda: [torch.zeros(-(-p.numel() // QBLOCK), device=p.device) for p in params]  # noqa: E731
+        eight = state_dtype == torch.float8_e4m3fn
+        held = [p.detach().float() for p in params] if masters and params[0].dtype != torch.float32 else None
+        return cls([p.detach() for p in params], moments(), moments(), scales() if eight else None,
+                   scales() if eight else None, held)
+
+
+@_on_its_device
+def maxsim_adamw(tensors, grads, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, step_dev=None):
+    """One AdamW step of an AdamWTensors with these gradients (one tensor a parameter, all fp16, bf16 or fp32), in
+    place.  step: the number of this step, from 1 on; or step_dev, a device int32 that holds it, for a step that is
+    captured and replayed."""
+    dev = tensors.device
+    if len(grads) != len(tensors.sizes):
+        raise ValueError("%d gradients for %d parameters" % (len(grads), len(tensors.sizes)))
+    dtype = grads[0].dtype
+    code = _code(dtype, _FLOATS, "grads")
+    for g, n in zip(grads, tensors.sizes):
+        if g.dtype != dtype or g.numel() != n or g.device != dev or not g.is_contiguous():
+            raise ValueError("gradients must be contiguous, of one type, on %s and of their parameters' sizes" % dev)
+    if step_dev is not None:
+        _flat(step_dev, "step_dev", 1, torch.int32, dev)
+    table = tensors._table.copy()
+    table["grad"] = [g.data_ptr() for g in grads]
+    st = _lib.maxsim_adamw(table.ctypes.data, len(grads), tensors.param_code, code, tensors.state_code, lr, beta1,
+                           beta2, eps, weight_decay, step, None if step_dev is None else step_dev.data_ptr(),
+                           _raw_stream(dev))
+    if st:
+        _check(st, "maxsim_adamw")
+
+
+class RMSNormFunction(torch.autograd.Function):
+    """RMS norm of x (+ residual) as an autograd op; with a residual the sum is an output too."""
+
+    @staticmethod
+    def forward(ctx, x, weight, residual, eps):
+        y, _, h, rstd = maxsim_rmsnorm_fwd(x, weight, eps, residual=residual, with_rstd=True)
+        ctx.save_for_backward(x if residual is None else h, weight, rstd)
+        return y if residual is None else (y, h)
+
+    @staticmethod
+    def backward(ctx, dy, dsum=None):
+        h, weight, rstd = ctx.saved_tensors
+        dx, dw = maxsim_rmsnorm_bwd(dy.contiguous(), h, rstd, weight,
+                                    dsum=None if dsum is None else dsum.contiguous(),
+                                    with_dweight=weight is not None and ctx.needs_input_grad[1])
+        return (dx if ctx.needs_input_grad[0] else None, None if dw is None else dw.to(weight.dtype),
+                dx if ctx.needs_input_grad[2] else None, None)
+
+
+def rms_norm(x, weight=None, residual=None, eps=1e-6):
+    """x / sqrt(mean(x^2) + eps) * weight over the last dimension, with autograd support.  With a residual of x's shape: the norm
+    of x + residual, and the sum itself, (y, sum)."""
+    return RMSNormFunction.apply(x, weight, residual, eps)
+
+
+class LinearFP8Function(torch.autograd.Function):
+    """x W^T with both operands in 8 bits, as an autograd op: x and dy with a scale for each 128 along the sum they
+    take part in, W for each 128 x 128.  Of x only its 8-bit transpose is kept for dW."""
+
+    @staticmethod
+    def forward(ctx, x, weight):
+        rows = x.reshape(-1, x.shape[-1])
+        need_x, need_w = ctx.needs_input_grad
+        q, s, qt, st = maxsim_quant_fp8(rows, transposed=need_w)
+        w, ws, wt, wst = maxsim_quant_fp8(weight, block_rows=QBLOCK, transposed=need_x)
+        ctx.save_for_backward(qt, st, wt, wst)
+        ctx.x_shape, ctx.x_dtype, ctx.w_dtype = x.shape, x.dtype, weight.dtype
+        return maxsim_gemm_fp8(q, s, w, ws, out_dtype=x.dtype).reshape(x.shape[:-1] + (weight.shape[0],))
+
+    @staticmethod
+    def backward(ctx, dy):
+        qt, st, wt, wst = ctx.saved_tensors
+        need_x, need_w = ctx.needs_input_grad
+        g, gs, gt, gst = maxsim_quant_fp8(dy.reshape(-1, dy.shape[-1]).contiguous(), rows=need_x, transposed=need_w)
+        dx = dw = None
+        if need_x:
+            dx = maxsim_gemm_fp8(g, gs, wt, wst, out_dtype=ctx.x_dtype).reshape(ctx.x_shape)
+        if need_w:
+            dw = maxsim_gemm_fp8(gt, gst, qt, st, out_dtype=torch.float32).to(ctx.w_dtype)
+        return dx, dw
+
+
+def linear_fp8(x, weight):
+    """x [..., K] times weight [N, K] transposed, in 8-bit floating point with a scale for each block of 128, with
+    autograd support (x, weight: fp16, bf16 or fp32; the result has x's type)."""
+    if weight.dim() != 2 or x.shape[-1] != weight.shape[1]:
+        raise ValueError("x [..., K] and weight [N, K] must share K")
+    return LinearFP8Function.apply(x, weight)
+
+
+def encode_tokens(hidden, gain, proj, proj_scale, residual=None, out_dtype=torch.int8, eps=1e-6):
+    """Token rows for the MaxSim entry points from an encoder's last hidden rows [..., H]: their RMS norm (of
+    hidden + residual where one is given) in 8 bits, the projection to 128 columns, and rows of length 1 --
+    (rows int8 [..., 128], scale [...]) for maxsim_fwd_i8, or (rows fp16 / bf16, None) for the other forwards.
+    proj [128, H] and proj_scale: maxsim_quant_fp8(weight, block_rows=128)."""
+    if proj.shape[0] != QBLOCK:
+        raise ValueError("proj must have 128 rows, got %d" % proj.shape[0])
+    q, s, _, _ = maxsim_rmsnorm_fwd(hidden, gain, eps, residual=residual, out_dtype=torch.float8_e4m3fn)
+    H = hidden.shape[-1]
+    # rows of one pitch: the leading dimensions collapse without a copy
+    flat = q.as_strided((_row_count(q.shape), H), (-(-H // 16) * 16, 1))
+    rows = maxsim_gemm_fp8(flat, s, proj, proj_scale, out_dtype=torch.float32)
+    # rows of length 1: the norm with the gain 1 / sqrt(128)
+    gain1 = torch.full((QBLOCK,), QBLOCK ** -0.5, dtype=torch.float32, device=rows.device)
+    rows, scale, _, _ = maxsim_rmsnorm_fwd(rows, gain1, 1e-12, out_dtype=out_dtype)
+    shape = hidden.shape[:-1]
+    return rows.reshape(shape + (QBLOCK,)), None if scale is None else scale.reshape(shape)

@@ -2,30 +2,34 @@
 
 Usage: python -m late_interaction_retrieval_amd.build
 """
+from concurrent.futures import ThreadPoolExecutor
 import os
 import subprocess
 import sys
+import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmaxsim.so")
-SOURCES = ["fwd.hip", "bwd.hip", "topk.hip", "ooc.hip", "chamfer.hip", "noalloc.hip", "capi.cpp"]
+SOURCES = ["fwd.hip", "bwd.hip", "topk.hip", "ooc.hip", "chamfer.hip", "noalloc.hip", "capi.cpp",
+           "rmsnorm.hip", "quant.hip", "gemm_fp8.hip", "adamw.hip", "capi_encoder.cpp"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # fp32 products and sums are separate IEEE operations unless fmaf is asked for
     "-ffp-contract=off",
-    # inputs are finite: max needs no NaN canonicalisation (infinities are kept)
-    "-fno-honor-nans",
     # no packed fp32 VALU ops
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wno-unused-command-line-argument",
 ]
+# inputs are finite: max needs no NaN canonicalisation (infinities are kept)
+FINITE_FLAGS = ["-fno-honor-nans"]
+# these pass NaN and infinity through as their formulas give them
+SOURCE_FLAGS = {s: [] for s in ("rmsnorm.hip", "quant.hip", "gemm_fp8.hip", "adamw.hip")}
 
 
 def hipcc():
@@ -33,11 +37,7 @@ def hipcc():
     return os.path.join(rocm, "bin", "hipcc")
 
 
-def _compile(sources, lib, verbose, extra):
-    tmp = lib + ".tmp%d" % os.getpid()
-    cmd = [hipcc()] + HIPCC_FLAGS + list(extra) + [
-        "-I", os.path.join(ROOT, "include"), "-I", CSRC,
-    ] + [os.path.join(CSRC, s) for s in sources] + ["-o", tmp]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -47,6 +47,21 @@ def _compile(sources, lib, verbose, extra):
         raise RuntimeError("hipcc failed:\n" + out)
     if verbose and out.strip():
         print(out)
+
+
+def _compile(sources, lib, verbose, extra):
+    """Each source to an object (several at a time), then one link."""
+    tmp = lib + ".tmp%d" % os.getpid()
+    with tempfile.TemporaryDirectory(prefix="maxsim_build_") as objs:
+        def one(s):
+            obj = os.path.join(objs, s + ".o")
+            _run([hipcc()] + HIPCC_FLAGS + SOURCE_FLAGS.get(s, FINITE_FLAGS) + list(extra) +
+                 ["-I", os.path.join(ROOT, "include"), "-I", CSRC, "-c", os.path.join(CSRC, s), "-o", obj], verbose)
+            return obj
+
+        with ThreadPoolExecutor(max_workers=4) as pool:
+            done = list(pool.map(one, sources))
+        _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC"] + done + ["-o", tmp], verbose)
     os.replace(tmp, lib)
     return lib
 

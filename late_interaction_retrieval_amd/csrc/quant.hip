@@ -1,0 +1,134 @@
+// quant.hip -- rows in 8-bit floating point with a scale for each 128 values,
+// as rows, transposed, or both from one read, for gfx950 (MI355X).
+//
+// A workgroup takes one tile of 128 x 128 values, whose row blocks, column
+// blocks and square block all lie inside it, so each kind of scale is a maximum
+// over registers of the tile and x is read once.  A thread holds 8 x 8
+// neighbouring values: a row block's maximum goes over 16 lanes by DPP, a
+// column block's over the thread's 8 rows, the lane groups and, through LDS,
+// the 4 waves.  HBM-bound: 2 (bf16) + 1 + 1 bytes a value.
+#include "encoder_dev.h"
+
+namespace maxsim {
+namespace {
+
+template <typename TT, bool SQUARE>
+__global__ __launch_bounds__(256) void quant_kernel(QuantArgs p) {
+    typedef typename TT::type T;
+    __shared__ uint32_t col_top[4][kQBlock];     // per wave: column maxima (or, square, one word)
+    __shared__ u32x2 bytes_t[kQBlock][16 + 1];   // the transposed tile: row = column of x, 8 bytes a word
+    const int tid = threadIdx.x, wave = tid >> 6;
+    const int lane_c = tid & 15, lane_r = tid >> 4;  // 8 columns x 8 rows of the tile
+    const int64_t row_blocks = (p.C + kQBlock - 1) / kQBlock;  // scales of a row of q
+    const int64_t col_blocks = (p.R + kQBlock - 1) / kQBlock;  // scales of a row of qt
+    const int bc = blockIdx.x % (uint32_t)row_blocks, br = blockIdx.x / (uint32_t)row_blocks;
+    const int c0 = bc * kQBlock, r0 = br * kQBlock;
+    const int c = c0 + lane_c * kVec, r = r0 + lane_r * kVec;
+    float x[kVec][kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+        if (r + j < p.R) {
+            const auto v = load8<T>((const T*)p.x + (int64_t)(r + j) * p.ldx, c, p.C);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) x[j][i] = (float)v[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) x[j][i] = 0.f;
+        }
+    }
+    Scale whole;
+    if constexpr (SQUARE) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) top = umax(top, mag(x[j][i]));
+        top = max64(top);
+        if ((tid & 63) == 0) col_top[wave][0] = top;
+        __syncthreads();
+        top = umax(umax(col_top[0][0], col_top[1][0]), umax(col_top[2][0], col_top[3][0]));
+        whole = block_scale(top, 448.f);
+        if (tid == 0) {
+            if (p.q != nullptr) p.scale[br * row_blocks + bc] = whole.s;
+            if (p.qt != nullptr) p.scale_t[bc * col_blocks + br] = whole.s;
+        }
+    }
+    if (p.q != nullptr) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            Scale k;
+            if constexpr (SQUARE) {
+                k = whole;
+            } else {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) top = umax(top, mag(x[j][i]));
+                k = block_scale(max16(top), 448.f);
+            }
+            if (r + j < p.R && c < p.C) {
+                store8_bytes(p.q + (int64_t)(r + j) * p.ldq, c, p.C, to_e4m3(x[j], k));
+                if (!SQUARE && lane_c == 0) p.scale[(int64_t)(r + j) * row_blocks + bc] = k.s;
+            }
+        }
+    }
+    if (p.qt == nullptr) return;
+    if constexpr (!SQUARE) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) top = umax(top, mag(x[j][i]));
+            auto s = __builtin_amdgcn_permlane16_swap(top, top, false, false);
+            top = umax(s[0], s[1]);
+            s = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+            top = umax(s[0], s[1]);
+            if ((tid & 63) < 16) col_top[wave][lane_c * kVec + i] = top;
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+        const int cc = lane_c * kVec + i;
+        Scale k;
+        if constexpr (SQUARE) {
+            k = whole;
+        } else {
+            k = block_scale(umax(umax(col_top[0][cc], col_top[1][cc]), umax(col_top[2][cc], col_top[3][cc])), 448.f);
+            if (lane_r == 0 && c0 + cc < p.C) p.scale_t[(int64_t)(c0 + cc) * col_blocks + br] = k.s;
+        }
+        float t[kVec];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) t[j] = x[j][i];
+        bytes_t[cc][lane_r] = to_e4m3(t, k);
+    }
+    __syncthreads();
+    // 16 lanes write one row of 128 bytes
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) {
+        const int cc = j * 16 + lane_r;
+        if (c0 + cc < p.C) store8_bytes(p.qt + (int64_t)(c0 + cc) * p.ldqt, r0 + lane_c * kVec, p.R, bytes_t[cc][lane_c]);
+    }
+}
+
+template <typename TT>
+void launch(const QuantArgs& a, hipStream_t stream) {
+    const unsigned grid = (unsigned)(ceil_div(a.C, kQBlock) * ceil_div(a.R, kQBlock));
+    if (a.square)
+        quant_kernel<TT, true><<<grid, 256, 0, stream>>>(a);
+    else
+        quant_kernel<TT, false><<<grid, 256, 0, stream>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_quant_fp8(const QuantArgs& a, hipStream_t stream) {
+    if (a.dtype == MAXSIM_F16)
+        launch<F16>(a, stream);
+    else if (a.dtype == MAXSIM_BF16)
+        launch<BF16>(a, stream);
+    else
+        launch<F32>(a, stream);
+    return hipGetLastError();
+}
+
+}  // namespace maxsim

@@ -1,0 +1,328 @@
+// rmsnorm.hip -- RMS norm of rows with the residual's addition, 16-bit or
+// 8-bit output, and its backward, for gfx950 (MI355X).
+//
+//     h = x + residual;  r = 1 / sqrt(mean(h^2) + eps);  y = h r w
+//     g = dy w;  xh = h r;  dx = r (g - xh mean(g xh)) + dsum;  dw = sum_rows dy xh
+//
+// Both are bound by HBM (a few operations per byte), so the design is one pass:
+// a row is read once into the registers of 16 lanes to a whole workgroup, its
+// sum goes over the lanes by DPP (and over waves through LDS), and everything
+// that depends on it is formed from those registers.  A lane holds vectors of
+// 8 neighbouring columns, so 16 lanes hold exactly one block of 128 columns and
+// an e4m3 block's scale is a 16-lane maximum.
+#include <algorithm>
+#include <type_traits>
+
+#include "encoder_dev.h"
+
+namespace maxsim {
+namespace {
+
+// TPR threads hold a row, NV vectors of 8 columns each: column
+// (v * TPR + lane) * 8.  Rows of up to 64 threads share a 256-thread workgroup.
+template <int TPR>
+struct Rows {
+    static constexpr int threads = TPR < 256 ? 256 : TPR;
+    static constexpr int per_group = threads / TPR;
+    static constexpr int waves = TPR / 64;  // of one row, when it is a whole workgroup
+};
+
+// Sum (or maximum) over a row's threads, the same in each of them.  Waves meet
+// in `part` (one word per wave), which each call uses anew.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* part) {
+    if constexpr (TPR == 16) return sum16(v);
+    v = sum64(v);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = part[0];
+#pragma unroll
+        for (int w = 1; w < Rows<TPR>::waves; ++w) v += part[w];
+    }
+    return v;
+}
+template <int TPR>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part) {
+    if constexpr (TPR == 16) return max16(v);
+    v = max64(v);
+    if constexpr (TPR > 64) {
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = part[0];
+#pragma unroll
+        for (int w = 1; w < Rows<TPR>::waves; ++w) v = umax(v, part[w]);
+    }
+    return v;
+}
+
+// The gain of 8 columns in fp32.
+template <typename T>
+__device__ __forceinline__ void load_gain(const void* weight, int f32, int c, int n, float* w) {
+    if (weight == nullptr) {
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) w[i] = 1.f;
+    } else if (f32) {
+        const auto v = load8<float>((const float*)weight, c, n);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) w[i] = v[i];
+    } else {
+        const auto v = load8<T>((const T*)weight, c, n);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) w[i] = (float)v[i];
+    }
+}
+
+template <typename TT, int TPR, int NV>
+__global__ __launch_bounds__(Rows<TPR>::threads) void rmsnorm_fwd_kernel(NormArgs p) {
+    typedef typename TT::type T;
+    constexpr int PER = Rows<TPR>::per_group;
+    __shared__ float part_sum[2][TPR > 64 ? Rows<TPR>::waves : 1];
+    __shared__ uint32_t part_max[2][TPR > 64 ? Rows<TPR>::waves : 1];
+    const int lane = threadIdx.x % TPR;
+    int turn = 0;  // two sets of words in LDS in turn: a wave may be a row ahead of another's read
+    // a row that all its threads leave together: rows of up to 64 threads meet no barrier
+    for (int64_t row = (int64_t)blockIdx.x * PER + threadIdx.x / TPR; row < p.R;
+         row += (int64_t)gridDim.x * PER, turn ^= 1) {
+        const T* x = (const T*)p.x + row * p.ldx;
+        float h[NV][kVec];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const auto a = load8<T>(x, (v * TPR + lane) * kVec, p.H);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) h[v][i] = (float)a[i];
+        }
+        if (p.residual != nullptr) {
+            const T* res = (const T*)p.residual + row * p.ldr;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const auto a = load8<T>(res, (v * TPR + lane) * kVec, p.H);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) h[v][i] += (float)a[i];
+            }
+        }
+        float ss = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) ss = __builtin_fmaf(h[v][i], h[v][i], ss);
+        if (p.sum != nullptr) {
+            T* sum = (T*)p.sum + row * p.lds;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) store8<T>(sum, (v * TPR + lane) * kVec, p.H, h[v]);
+        }
+        ss = row_sum<TPR>(ss, part_sum[turn]);
+        const float r = 1.f / __builtin_sqrtf(ss / (float)p.H + p.eps);
+        if (p.rstd != nullptr && lane == 0) p.rstd[row] = r;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float w[kVec];
+            load_gain<T>(p.weight, p.weight_f32, (v * TPR + lane) * kVec, p.H, w);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) h[v][i] = h[v][i] * r * w[i];
+        }
+        if (p.out_dtype == MAXSIM_E4M3) {
+            const int64_t blocks = (p.H + kQBlock - 1) / kQBlock;
+            uint8_t* y = (uint8_t*)p.y + row * p.ldy;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) top = umax(top, mag(h[v][i]));
+                const Scale k = block_scale(max16(top), 448.f);
+                const int c = (v * TPR + lane) * kVec;
+                if (c < p.H) {
+                    store8_bytes(y, c, p.H, to_e4m3(h[v], k));
+                    if (c % kQBlock == 0) p.scale[row * blocks + c / kQBlock] = k.s;
+                }
+            }
+        } else if (p.out_dtype == MAXSIM_I8) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int v = 0; v < NV; ++v)
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) top = umax(top, mag(h[v][i]));
+            const Scale k = block_scale(row_max<TPR>(top, part_max[turn]), 127.f);
+            if (lane == 0) p.scale[row] = k.s;
+            uint8_t* y = (uint8_t*)p.y + row * p.ldy;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) store8_bytes(y, (v * TPR + lane) * kVec, p.H, to_i8(h[v], k));
+        } else if (p.out_dtype == MAXSIM_F32) {
+            float* y = (float*)p.y + row * p.ldy;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) store8<float>(y, (v * TPR + lane) * kVec, p.H, h[v]);
+        } else if (p.out_dtype == MAXSIM_BF16) {
+            __bf16* y = (__bf16*)p.y + row * p.ldy;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) store8<__bf16>(y, (v * TPR + lane) * kVec, p.H, h[v]);
+        } else {
+            _Float16* y = (_Float16*)p.y + row * p.ldy;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) store8<_Float16>(y, (v * TPR + lane) * kVec, p.H, h[v]);
+        }
+    }
+}
+
+// Rows in turn, a workgroup's every gridDim-th; each thread keeps its columns'
+// share of dw in registers over all of them and the workgroup writes one
+// partial row at the end.
+template <typename TT, int TPR, int NV>
+__global__ __launch_bounds__(Rows<TPR>::threads) void rmsnorm_bwd_kernel(NormBwdArgs p) {
+    typedef typename TT::type T;
+    constexpr int PER = Rows<TPR>::per_group;
+    __shared__ float part[2][TPR > 64 ? Rows<TPR>::waves : 1];
+    __shared__ float share[PER > 1 ? PER : 1][PER > 1 ? TPR * kVec : 1];
+    const int lane = threadIdx.x % TPR;
+    const int sub = threadIdx.x / TPR;
+    float w[NV][kVec], dw[NV][kVec];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        load_gain<T>(p.weight, p.weight_f32, (v * TPR + lane) * kVec, p.H, w[v]);
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) dw[v][i] = 0.f;
+    }
+    const float inv_h = 1.f / (float)p.H;
+    int turn = 0;
+    for (int64_t row = (int64_t)blockIdx.x * PER + sub; row < p.R; row += (int64_t)gridDim.x * PER, turn ^= 1) {
+        const T* dyr = (const T*)p.dy + row * p.lddy;
+        const T* hr = (const T*)p.h + row * p.ldh;
+        typename Pack8<T>::V dy[NV], h[NV], ds[NV];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            dy[v] = load8<T>(dyr, (v * TPR + lane) * kVec, p.H);
+            h[v] = load8<T>(hr, (v * TPR + lane) * kVec, p.H);
+        }
+        if (p.dsum != nullptr) {
+            const T* dsr = (const T*)p.dsum + row * p.ldds;
+#pragma unroll
+            for (int v = 0; v < NV; ++v) ds[v] = load8<T>(dsr, (v * TPR + lane) * kVec, p.H);
+        }
+        const float r = p.rstd[row];
+        float c = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const float t = (float)dy[v][i] * ((float)h[v][i] * r);
+                dw[v][i] += t;
+                c = __builtin_fmaf(t, w[v][i], c);
+            }
+        // two words of LDS in turn: a wave may be a row ahead of another's read
+        c = row_sum<TPR>(c, part[turn]) * inv_h;
+        T* dxr = (T*)p.dx + row * p.lddx;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            float dx[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const float g = (float)dy[v][i] * w[v][i];
+                dx[i] = r * (g - (float)h[v][i] * r * c);
+            }
+            if (p.dsum != nullptr) {
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) dx[i] += (float)ds[v][i];
+            }
+            store8<T>(dxr, (v * TPR + lane) * kVec, p.H, dx);
+        }
+    }
+    if (p.dweight == nullptr) return;
+    float* out = p.partial + (int64_t)blockIdx.x * p.H;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = (v * TPR + lane) * kVec;
+        if constexpr (PER > 1) {  // the workgroup's rows, added in order
+            if (v > 0) __syncthreads();
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) share[sub][lane * kVec + i] = dw[v][i];
+            __syncthreads();
+            for (int k = threadIdx.x; k < TPR * kVec; k += Rows<TPR>::threads) {
+                float s = share[0][k];
+                for (int q = 1; q < PER; ++q) s += share[q][k];
+                if (v * TPR * kVec + k < p.H) out[v * TPR * kVec + k] = s;
+            }
+        } else {
+            store8<float>(out, c, p.H, dw[v]);
+        }
+    }
+}
+
+// dweight = the partial rows, added in order: 16 columns x 16 runs of rows to a
+// workgroup, so that a few hundred partial rows are read by many waves.
+constexpr int kReduceCols = 16;
+__global__ __launch_bounds__(256) void rmsnorm_dweight_kernel(const float* partial, int groups, int H, float* dw) {
+    __shared__ float run[16][kReduceCols];
+    const int col = threadIdx.x % kReduceCols, part = threadIdx.x / kReduceCols;
+    const int c = blockIdx.x * kReduceCols + col;
+    const int per = (groups + 15) / 16;
+    const int end = min(groups, (part + 1) * per);
+    float s = 0.f;
+    if (c < H)
+        for (int g = part * per; g < end; ++g) s += partial[(int64_t)g * H + c];
+    run[part][col] = s;
+    __syncthreads();
+    if (part == 0 && c < H) {
+        for (int q = 1; q < 16; ++q) s += run[q][col];
+        dw[c] = s;
+    }
+}
+
+// Threads to a row: few enough that a lane has a full vector, and as many as a
+// row's columns ask for.
+template <typename F>
+void by_width(int H, F&& go) {
+    if (H <= 128) return go(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
+    if (H <= 512) return go(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
+    if (H <= 1024) return go(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
+    if (H <= 2048) return go(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
+    if (H <= 4096) return go(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+    if (H <= 8192) return go(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
+    if (H <= 16384) return go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
+    return go(std::integral_constant<int, 1024>{}, std::integral_constant<int, 4>{});
+}
+template <typename F>
+void by_type(int dtype, F&& go) {
+    if (dtype == MAXSIM_F16) return go(F16{});
+    if (dtype == MAXSIM_BF16) return go(BF16{});
+    return go(F32{});
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm_fwd(const NormArgs& a, hipStream_t stream) {
+    by_type(a.dtype, [&](auto t) {
+        by_width(a.H, [&](auto tpr, auto nv) {
+            constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+            // at most 2^22 workgroups (a launch holds fewer than 2^32 threads); more rows go round
+            const int grid = (int)std::min<int64_t>(ceil_div(a.R, Rows<TPR>::per_group), 1 << 22);
+            rmsnorm_fwd_kernel<decltype(t), TPR, NV><<<grid, Rows<TPR>::threads, 0, stream>>>(a);
+        });
+    });
+    return hipGetLastError();
+}
+
+int norm_bwd_groups(int R, int H) {
+    const int per = H <= 128 ? 16 : H <= 1024 ? 4 : 1;
+    const int64_t rows = ceil_div(R, per);
+    const int most = H <= 8192 ? 1024 : 512;
+    return (int)(rows < most ? rows : most);
+}
+
+hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, hipStream_t stream) {
+    const int groups = norm_bwd_groups(a.R, a.H);
+    if (groups > 0) {
+        by_type(a.dtype, [&](auto t) {
+            by_width(a.H, [&](auto tpr, auto nv) {
+                constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+                rmsnorm_bwd_kernel<decltype(t), TPR, NV><<<groups, Rows<TPR>::threads, 0, stream>>>(a);
+            });
+        });
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    if (a.dweight != nullptr)
+        rmsnorm_dweight_kernel<<<(a.H + kReduceCols - 1) / kReduceCols, 256, 0, stream>>>(a.partial, groups, a.H,
+                                                                                          a.dweight);
+    return hipGetLastError();
+}
+
+}  // namespace maxsim
