@@ -28,6 +28,7 @@ namespace {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void* lptr_t;
 
 constexpr int kStep = kQBlock;  // bytes of K a step
@@ -36,49 +37,78 @@ constexpr uint32_t kOutside = 0xF0000000u;  // an offset past any buffer: reads 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-// An operand of one MFMA block: a lane's 32 bytes, or their 32 values in fp16
-// (which holds every e4m3 value).
+// A lane's part of a block of 128 along K: 32 bytes for an operand of 16 rows, two times 32
+// for one of 32 rows; or the values in fp16, which holds every e4m3 value.  Which of the 128
+// a lane holds is the same for both operands, and does not matter otherwise.
+__device__ __forceinline__ void to_f16(i32x8 bytes, f16x8* v) {
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+        const f16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)bytes[w], 1.f, false);
+        const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)bytes[w], 1.f, true);
+        v[w >> 1][(w & 1) * 4 + 0] = lo[0];
+        v[w >> 1][(w & 1) * 4 + 1] = lo[1];
+        v[w >> 1][(w & 1) * 4 + 2] = hi[0];
+        v[w >> 1][(w & 1) * 4 + 3] = hi[1];
+    }
+}
 template <bool FINE>
 struct Operand {
-    i32x8 v;
+    i32x8 v[2];
 };
 template <>
 struct Operand<true> {
-    f16x8 v[4];
+    f16x8 v[8];
 };
 template <bool FINE>
-__device__ __forceinline__ Operand<FINE> operand_of(i32x8 bytes) {
+__device__ __forceinline__ Operand<FINE> operand_of(i32x8 lo, i32x8 hi) {
     Operand<FINE> o;
     if constexpr (FINE) {
-#pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            const f16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)bytes[w], 1.f, false);
-            const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((unsigned)bytes[w], 1.f, true);
-            o.v[w >> 1][(w & 1) * 4 + 0] = lo[0];
-            o.v[w >> 1][(w & 1) * 4 + 1] = lo[1];
-            o.v[w >> 1][(w & 1) * 4 + 2] = hi[0];
-            o.v[w >> 1][(w & 1) * 4 + 3] = hi[1];
-        }
+        to_f16(lo, o.v);
+        to_f16(hi, o.v + 4);
     } else {
-        o.v = bytes;
+        o.v[0] = lo;
+        o.v[1] = hi;
     }
     return o;
 }
 
-// The unscaled sum of one block of 128.  The 8-bit instruction aligns a block's
-// products to the largest and keeps about 13 bits below it (measured against
-// exact sums of normal values: 1.4e-5 relative, at most 2^-13.4 of the largest product; 2 bits
-// fewer than a 16-bit result needs).  An fp32 result takes the values through fp16, whose
-// products and sums are exact to fp32 (1.2e-8), at half the rate.
+__device__ __forceinline__ f32x16 zero16() {
+    f32x16 z;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) z[e] = 0.f;
+    return z;
+}
+
+// The unscaled sum of one block of 128, for 16 x 16 or 32 x 32 results.  The
+// 8-bit instructions align the products to the largest and keep about 13
+// bits below it (measured against exact sums of normal values: 1.4e-5 relative, at most 2^-13.4 of
+// the largest product), which is far below a 16-bit result's rounding.  An fp32
+// result takes the values through fp16, whose products and sums are exact to
+// fp32 (1.2e-8), at half the rate.  Both scale operands 0: the compiler emits the 8-bit instruction without scales.
 template <bool FINE>
-__device__ __forceinline__ f32x4 mfma(const Operand<FINE>& b, const Operand<FINE>& a) {
+__device__ __forceinline__ f32x4 mfma16(i32x8 b, i32x8 a) {
     f32x4 d = {0.f, 0.f, 0.f, 0.f};
     if constexpr (FINE) {
+        f16x8 x[4], y[4];
+        to_f16(b, x);
+        to_f16(a, y);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(b.v[q], a.v[q], d, 0, 0, 0);
+        for (int q = 0; q < 4; ++q) d = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[q], y[q], d, 0, 0, 0);
     } else {
-        // both scale operands 0: the compiler emits the instruction without scales
-        d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b.v, a.v, d, 0, 0, 0, 0, 0, 0);
+        d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, d, 0, 0, 0, 0, 0, 0);
+    }
+    return d;
+}
+template <bool FINE>
+__device__ __forceinline__ f32x16 mfma32(const Operand<FINE>& b, const Operand<FINE>& a) {
+    f32x16 d = zero16();
+    if constexpr (FINE) {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) d = __builtin_amdgcn_mfma_f32_32x32x16_f16(b.v[q], a.v[q], d, 0, 0, 0);
+    } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            d = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(b.v[q], a.v[q], d, 0, 0, 0, 0, 0, 0);
     }
     return d;
 }
@@ -112,39 +142,30 @@ __device__ __forceinline__ void tile_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// 4 (a vector) neighbouring values of a row of c, rounded once.
-__device__ __forceinline__ void store4(const GemmArgs& p, int64_t row, int n, f32x4 v) {
-    typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
-    typedef __bf16 bf16x4u __attribute__((ext_vector_type(4), aligned(2)));
-    typedef _Float16 f16x4u __attribute__((ext_vector_type(4), aligned(2)));
-    if (n >= p.N) return;
-    const int64_t at = row * p.ldc + n;
-    const int left = p.N - n;
-    if (p.out_dtype == MAXSIM_F32) {
-        float* c = (float*)p.c + at;
-        if (left >= 4)
-            *reinterpret_cast<f32x4u*>(c) = v;
-        else
-            for (int i = 0; i < left; ++i) c[i] = v[i];
-    } else if (p.out_dtype == MAXSIM_BF16) {
-        __bf16* c = (__bf16*)p.c + at;
-        bf16x4u w;
+// N neighbouring values of a row of c, rounded once.
+template <typename T, int N>
+__device__ __forceinline__ void store_n(T* c, int left, const float* v) {
+    typedef T VN __attribute__((ext_vector_type(N), aligned(sizeof(T))));
+    VN w;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = (__bf16)v[i];
-        if (left >= 4)
-            *reinterpret_cast<bf16x4u*>(c) = w;
-        else
-            for (int i = 0; i < left; ++i) c[i] = w[i];
+    for (int i = 0; i < N; ++i) w[i] = (T)v[i];
+    if (left >= N) {
+        *reinterpret_cast<VN*>(c) = w;
     } else {
-        _Float16* c = (_Float16*)p.c + at;
-        f16x4u w;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = (_Float16)v[i];
-        if (left >= 4)
-            *reinterpret_cast<f16x4u*>(c) = w;
-        else
-            for (int i = 0; i < left; ++i) c[i] = w[i];
+        for (int i = 0; i < N; ++i)
+            if (i < left) c[i] = w[i];
     }
+}
+__device__ __forceinline__ void store4(const GemmArgs& p, int64_t row, int n, f32x4 v) {
+    const int64_t at = row * p.ldc + n;
+    const float f[4] = {v[0], v[1], v[2], v[3]};
+    if (p.out_dtype == MAXSIM_F32)
+        store_n<float, 4>((float*)p.c + at, p.N - n, f);
+    else if (p.out_dtype == MAXSIM_BF16)
+        store_n<__bf16, 4>((__bf16*)p.c + at, p.N - n, f);
+    else
+        store_n<_Float16, 4>((_Float16*)p.c + at, p.N - n, f);
 }
 
 struct TilePlan {
@@ -154,17 +175,27 @@ struct TilePlan {
 };
 
 // A workgroup of WGM x WGN waves makes a tile of TM rows of A x TN rows of B; a
-// wave makes (TM / WGM) x (TN / WGN), which lies within 128 rows of B.
+// wave makes (TM / WGM) x (TN / WGN), which lies within 128 rows of B, in
+// blocks of 32 x 32 (the 32x32x64 instruction ran 1.22x the rate of 16x16x128).
 // ROWS: b_scale by the row; FINE: products in fp16
 template <int TM, int TN, int WGM, int WGN, bool ROWS, bool FINE>
 __global__ __launch_bounds__(64 * WGM * WGN) void gemm_tile_kernel(GemmArgs p, TilePlan plan) {
     constexpr int WAVES = WGM * WGN;
-    constexpr int NI = TM / WGM / 16, NJ = TN / WGN / 16;
-    constexpr int LA = TM / 8 / WAVES, LB = TN / 8 / WAVES;  // a wave's direct loads of 8 rows
-    constexpr int SCALES = TM + (ROWS ? TN : 0);
-    static_assert(LA * 8 * WAVES == TM && LB * 8 * WAVES == TN && TN / WGN <= kQBlock, "tile");
-    __shared__ __align__(16) uint8_t tile[2][(TM + TN) * kStep];
-    __shared__ __align__(16) float scale[2][SCALES];
+    constexpr int NI = TM / WGM / 32, NJ = TN / WGN / 32;
+    // Issuing a tile's direct loads holds a wave up for about as long as a SIMD
+    // works on a step, so with two waves on each SIMD the first issues all of them and the
+    // second keeps the matrix pipe busy.
+    constexpr int LOADERS = WAVES == 8 ? 4 : WAVES;
+    constexpr int LA = TM / 8 / LOADERS, LB = TN / 8 / LOADERS;  // a loading wave's direct loads of 8 rows
+    constexpr int SA = TM, SB = ROWS ? TN : 64;  // scales of a step: of each row, or of 128 rows of B in 64 words
+    static_assert(LA * 8 * LOADERS == TM && LB * 8 * LOADERS == TN && TN / WGN <= kQBlock && LA % 2 == 0 && LB % 4 == 0,
+                  "tile");
+    // Two arrays and a loop unrolled by two, not one array indexed by the step:
+    // the compiler then sees that a step's reads and the next tile's direct
+    // loads touch different memory, and does not make the reads wait for them.
+    __shared__ __align__(16) uint8_t tile_0[(TM + TN) * kStep], tile_1[(TM + TN) * kStep];
+    constexpr int LS = ((SA + SB) / 64 + LOADERS - 1) / LOADERS;  // a wave's loads of 64 scales
+    __shared__ __align__(16) float scale_0[LS * LOADERS * 64], scale_1[LS * LOADERS * 64];
     const int tid = threadIdx.x;
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -184,140 +215,214 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_tile_kernel(GemmArgs p, T
 
     const int rows_a = min(TM, p.M - m0), rows_b = min(TN, p.N - n0);
     const uint32_t k16 = ((uint32_t)p.K + 15u) & ~15u;  // readable bytes of a row that are used
-    const uint8_t* base_a = p.A + (int64_t)m0 * p.lda;
-    const uint8_t* base_b = p.B + (int64_t)n0 * p.ldb;
-    const uint32_t bytes_a = (uint32_t)(rows_a - 1) * (uint32_t)p.lda + k16;
-    const uint32_t bytes_b = (uint32_t)(rows_b - 1) * (uint32_t)p.ldb + k16;
-
-    // LDS row r holds its 16-byte chunk c at position c ^ swizzle(r).  The
-    // 16 rows a wave reads at once are neighbours in A; in B they are 4 runs of 4
-    // rows, 4 * NJ apart, so that a lane's NJ results are neighbouring columns of c.
+    // LDS row r holds its 16-byte chunk c at position c ^ swizzle(r), so that the
+    // 16 rows of a quarter wave's read fall on all 64 banks.  They are neighbours
+    // in A.  In B a block's row rr is row rr / 8 * 4 + rr / 4 % 2 * 16 + rr % 4 of
+    // its 32, so that a lane's 16 results are neighbouring columns of c.
     auto swz_a = [](int r) { return (r >> 1) & 7; };
-    auto swz_b = [](int r) { return ((r >> 1) & 1) | (((r / (4 * NJ)) & 3) << 1); };
+    auto swz_b = [](int r) { return ((r >> 1) & 3) | (((r >> 4) & 1) << 2); };
 
-    // this lane's part of each direct load: row (group * 8 + lane / 8), position lane % 8
-    uint32_t off_a[LA], off_b[LB];
-    uint32_t chunk_a[LA], chunk_b[LB];
+    // Direct loads: 8 rows each, row lane / 8 at position lane % 8 a lane.  A's
+    // swizzle changes with every group of 8 rows and B's with every second one,
+    // both between two values, so a lane's offsets are 4 in all.
+    uint32_t off_a[2], off_b[2], chunk_a[2], chunk_b[2];
 #pragma unroll
-    for (int j = 0; j < LA; ++j) {
-        const int r = (wave * LA + j) * 8 + (lane >> 3);
-        chunk_a[j] = (uint32_t)((lane & 7) ^ swz_a(r)) * 16;
-        off_a[j] = r < rows_a ? (uint32_t)r * (uint32_t)p.lda : kOutside;
-    }
-#pragma unroll
-    for (int j = 0; j < LB; ++j) {
-        const int r = (wave * LB + j) * 8 + (lane >> 3);
-        chunk_b[j] = (uint32_t)((lane & 7) ^ swz_b(r)) * 16;
-        off_b[j] = r < rows_b ? (uint32_t)r * (uint32_t)p.ldb : kOutside;
+    for (int j = 0; j < 2; ++j) {
+        chunk_a[j] = (uint32_t)((lane & 7) ^ swz_a((wave * LA + j) * 8 + (lane >> 3))) * 16;
+        chunk_b[j] = (uint32_t)((lane & 7) ^ swz_b((wave * LB + 2 * j) * 8 + (lane >> 3))) * 16;
+        off_a[j] = (uint32_t)(lane >> 3) * (uint32_t)p.lda + chunk_a[j];
+        off_b[j] = (uint32_t)(lane >> 3) * (uint32_t)p.ldb + chunk_b[j];
     }
     const float* sa = p.a_scale + (int64_t)m0 * plan.steps;
     const float* sb = p.b_scale + (int64_t)(ROWS ? n0 : n0 / kQBlock) * plan.steps;
+    const int scales_b = ROWS ? rows_b : (rows_b + kQBlock - 1) / kQBlock;
 
-    auto load = [&](int kb, int buf) {
-        const uint32_t at = (uint32_t)kb * kStep;
+    // One operand's part of tile kb: rows [first, first + 8 * L) of the `rows` of the tile.
+    auto load_rows = [&](const uint8_t* base, int64_t ld, int first, int rows, const uint32_t* off, const uint32_t* chunk,
+                         int kb, uint8_t* to, auto count, auto period) {
+        constexpr int L = decltype(count)::value, P = decltype(period)::value;
+        const uint32_t left = kb < k_end ? k16 - (uint32_t)kb * kStep : 0u;  // bytes of K from this step on
+        const uint8_t* at = base + (int64_t)first * ld + (int64_t)kb * kStep;
 #pragma unroll
-        for (int j = 0; j < LA; ++j) {
-            const uint32_t k = at + chunk_a[j];
-            load_lds<16>(base_a, bytes_a, k < k16 ? off_a[j] + k : kOutside,
-                         (lptr_t)&tile[buf][(wave * LA + j) * 8 * kStep]);
+        for (int j = 0; j < L; ++j) {
+            const int n = min(8, rows - first - j * 8);  // rows of this load; none: reads zeros
+            const uint32_t bytes = n > 0 && left > 0 ? (uint32_t)(n - 1) * (uint32_t)ld + left : 0u;
+            const uint32_t o = chunk[j / P & 1] < left ? off[j / P & 1] : kOutside;
+            load_lds<16>(at, bytes, o, (lptr_t)(to + j * 8 * kStep));
+            at += 8 * ld;
         }
+    };
+    auto load = [&](int kb, uint8_t* tile, float* scale) {
+        if (wave >= LOADERS) return;
+        load_rows(p.A + (int64_t)m0 * p.lda, p.lda, wave * LA * 8, rows_a, off_a, chunk_a, kb, tile + wave * LA * 8 * kStep,
+                  std::integral_constant<int, LA>{}, std::integral_constant<int, 1>{});
+        load_rows(p.B + (int64_t)n0 * p.ldb, p.ldb, wave * LB * 8, rows_b, off_b, chunk_b, kb,
+                  tile + (TM + wave * LB * 8) * kStep, std::integral_constant<int, LB>{}, std::integral_constant<int, 2>{});
+        // scales, 64 to a load; those past the end read 0, as do the loads of waves that have none left
 #pragma unroll
-        for (int j = 0; j < LB; ++j) {
-            const uint32_t k = at + chunk_b[j];
-            load_lds<16>(base_b, bytes_b, k < k16 ? off_b[j] + k : kOutside,
-                         (lptr_t)&tile[buf][(TM + (wave * LB + j) * 8) * kStep]);
-        }
-        // scales: 64 rows a wave; rows past the end read 0
-#pragma unroll
-        for (int q = 0; q < SCALES / 64; ++q) {
-            if (q % WAVES != wave) continue;
-            const bool is_a = q < TM / 64;
-            const int r = (is_a ? q : q - TM / 64) * 64 + lane;
-            const int rows = is_a ? rows_a : rows_b;
-            load_lds<4>(is_a ? sa : sb, (uint32_t)rows * (uint32_t)plan.steps * 4u,
-                        r < rows ? ((uint32_t)r * (uint32_t)plan.steps + (uint32_t)kb) * 4u : kOutside,
-                        (lptr_t)&scale[buf][q * 64]);
+        for (int u = 0; u < LS; ++u) {
+            const int q = u * LOADERS + wave;
+            const bool is_a = q < SA / 64;
+            const int r = (is_a ? q : q - SA / 64) * 64 + lane;
+            const int rows = kb < k_end ? is_a ? rows_a : scales_b : 0;
+            load_lds<4>((is_a ? sa : sb) + kb, rows > 0 ? ((uint32_t)rows * (uint32_t)plan.steps - (uint32_t)kb) * 4u : 0u,
+                        r < rows ? (uint32_t)r * (uint32_t)plan.steps * 4u : kOutside, (lptr_t)&scale[q * 64]);
         }
     };
 
     const int wm = wave / WGN * (TM / WGM), wn = wave % WGN * (TN / WGN);
-    const int col = lane & 15, grp = lane >> 4;
-    const int row_b = wn + (col >> 2) * (4 * NJ) + (col & 3);  // + 4 j
-    f32x4 acc[NI][NJ];
+    const int col = lane & 31, half = lane >> 5;
+    const int row_b = wn + (col >> 3) * 4 + ((col >> 2) & 1) * 16 + (col & 3);
+    uint32_t lds_a = (uint32_t)((wm + col) * kStep + (((2 * half) ^ swz_a(wm + col)) << 4));
+    uint32_t lds_b = (uint32_t)((TM + row_b) * kStep + (((2 * half) ^ swz_b(row_b)) << 4));
+    f32x16 acc[NI][NJ];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < NJ; ++j) acc[i][j] = zero16();
 
-    if (k_begin < k_end) load(k_begin, 0);
-    for (int kb = k_begin; kb < k_end; ++kb) {
-        const int buf = (kb - k_begin) & 1;
-        float s_block = 1.f;
-        if constexpr (!ROWS) {
-            const int b = min(wn, rows_b - 1) / kQBlock;  // a wave past the last row: any scale
-            s_block = sb[(int64_t)b * plan.steps + kb];
+    // LAG: a block is added while the next one is on the matrix pipe, and a
+    // step's last block while the next step's first is.  Scales by the row and
+    // fp16 operands leave no registers for a second block; there the other
+    // wave of the SIMD fills the pipe.
+    constexpr bool LAG = !ROWS && !FINE;
+    constexpr bool AHEAD = LAG || NI * NJ < 8;  // the next rows of B are read while these are multiplied
+    f32x16 d_last = zero16();
+    float s_last = 0.f;
+    auto add = [&](f32x16& c, const f32x16& d, const f32x4* t, float s) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) c[e] = __builtin_fmaf(ROWS ? d[e] * t[e >> 2][e & 3] : d[e], s, c[e]);
+        asm volatile("" : "+v"(c));  // here, and not sunk to a later block that reads c
+    };
+    // K ends inside a chunk: clear what follows it there
+    auto end_of_k = [&](int kb, uint8_t* tile) {
+        if (kb != plan.steps - 1 || (p.K & 15) == 0) return;
+        const int last = (p.K & (kStep - 1)) >> 4, keep = p.K & 15;
+        for (int r = tid; r < TM + TN; r += 64 * WAVES) {
+            const int s = r < TM ? swz_a(r) : swz_b(r - TM);
+            uint32_t* w = reinterpret_cast<uint32_t*>(tile + r * kStep + (last ^ s) * 16);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int left = keep - 4 * i;
+                if (left < 4) w[i] = left <= 0 ? 0u : w[i] & ((1u << (8 * left)) - 1u);
+            }
         }
         tile_barrier();
-        if (kb + 1 < k_end) load(kb + 1, buf ^ 1);
-        if (kb == plan.steps - 1 && (p.K & 15) != 0) {  // clear what follows K in its last chunk
-            const int last = (p.K & (kStep - 1)) >> 4, keep = p.K & 15;
-            for (int r = tid; r < TM + TN; r += 64 * WAVES) {
-                const int s = r < TM ? swz_a(r) : swz_b(r - TM);
-                uint32_t* w = reinterpret_cast<uint32_t*>(&tile[buf][r * kStep + (last ^ s) * 16]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int left = keep - 4 * i;
-                    if (left < 4) w[i] = left <= 0 ? 0u : w[i] & ((1u << (8 * left)) - 1u);
-                }
-            }
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
-            __builtin_amdgcn_s_barrier();
-            asm volatile("" ::: "memory");
-        }
-        auto operand = [&](int r, int s) {
-            const uint8_t* w = &tile[buf][r * kStep];
-            return join(*reinterpret_cast<const u32x4*>(w + ((2 * grp) ^ s) * 16),
-                        *reinterpret_cast<const u32x4*>(w + ((2 * grp + 1) ^ s) * 16));
+    };
+    auto step = [&](int kb, uint8_t* tile, const float* scale, uint8_t* next, float* next_scale) {
+        tile_barrier();
+        end_of_k(kb, tile);
+        load(kb + 1, next, next_scale);
+        // Half `half` of the wave holds chunks 2 half, 2 half + 1 of each 64 of K; blocks of 32 rows share a lane's
+        // swizzle.  The compiler may not keep all these addresses over the loop: registers are short, adds are not.
+        asm volatile("" : "+v"(lds_a), "+v"(lds_b));
+        auto operand = [&](uint32_t at, int block) {
+            auto chunk = [&](uint32_t flip) {
+                return *reinterpret_cast<const u32x4*>(tile + (at ^ flip) + block * 32 * kStep);
+            };
+            return operand_of<FINE>(join(chunk(0), chunk(16)), join(chunk(64), chunk(80)));
         };
+        const float s_block = ROWS ? 1.f : scale[SA + wn / kQBlock];
         Operand<FINE> a[NI];
         float s[NI];
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const int r = wm + i * 16 + col;
-            a[i] = operand_of<FINE>(operand(r, swz_a(r)));
-            s[i] = scale[buf][r] * s_block;
+            a[i] = operand(lds_a, i);
+            s[i] = scale[wm + i * 32 + col] * s_block;
         }
+        Operand<FINE> b;
+        if (AHEAD) b = operand(lds_b, 0);
 #pragma unroll
         for (int j = 0; j < NJ; ++j) {
-            const int r = row_b + 4 * j;
-            const Operand<FINE> b = operand_of<FINE>(operand(TM + r, swz_b(r)));
-            f32x4 t = {1.f, 1.f, 1.f, 1.f};
-            if constexpr (ROWS)
-                t = *reinterpret_cast<const f32x4*>(&scale[buf][TM + wn + grp * (4 * NJ) + 4 * j]);
+            f32x4 t[4];
+            if constexpr (ROWS) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    t[q] = *reinterpret_cast<const f32x4*>(&scale[SA + wn + 32 * j + 16 * half + 4 * q]);
+            }
+            if (!AHEAD) b = operand(lds_b, j);
+            Operand<FINE> b_next = b;
 #pragma unroll
             for (int i = 0; i < NI; ++i) {
-                const f32x4 d = mfma<FINE>(b, a[i]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    acc[i][j][e] = __builtin_fmaf(ROWS ? d[e] * t[e] : d[e], s[i], acc[i][j][e]);
+                const f32x16 d = mfma32<FINE>(b, a[i]);
+                if (AHEAD && i == 0 && j + 1 < NJ) b_next = operand(lds_b, j + 1);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (LAG) {
+                    add(i > 0 ? acc[i - 1][j] : acc[NI - 1][j > 0 ? j - 1 : NJ - 1], d_last, t, s_last);
+                    d_last = d;
+                    s_last = s[i];
+                } else {
+                    add(acc[i][j], d, t, s[i]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
             }
+            b = b_next;
         }
+    };
+    if (k_begin < k_end) {
+        load(k_begin, tile_0, scale_0);
+        // an odd number of steps: the last one adds zeros
+        for (int kb = k_begin; kb < k_end; kb += 2) {
+            step(kb, tile_0, scale_0, tile_1, scale_1);
+            step(kb + 1, tile_1, scale_1, tile_0, scale_0);
+        }
+        if constexpr (LAG) add(acc[NI - 1][NJ - 1], d_last, nullptr, s_last);
     }
+    // Results leave through LDS, 32 rows of each row of waves at a time, so that
+    // neighbouring lanes store neighbouring 16 bytes: straight from the accumulators a
+    // store would put 8 bytes each into 64 cache lines (41 us a tile of 256 x 256).
+    // 16-byte chunks are XOR-swizzled by the row.
+    auto leave = [&](auto type, auto* c, int64_t ld, int width) {
+        typedef decltype(type) T;
+        constexpr int V = 16 / sizeof(T), CH = TN / V;  // values of a chunk, chunks of a row
+        constexpr int ROWS_NOW = WGM * 32;
+        static_assert(ROWS_NOW * TN * sizeof(T) <= sizeof(tile_0) && CH >= 16, "LDS");
+        typedef T VT __attribute__((ext_vector_type(V)));
+        VT* box = reinterpret_cast<VT*>(tile_0);
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const int m = m0 + wm + i * 16 + col;
-        if (m >= p.M) continue;
+        for (int i = 0; i < NI; ++i) {
+            __syncthreads();
+            const int r = wave / WGN * 32 + col;
 #pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int n = n0 + wn + grp * (4 * NJ) + 4 * j;
-            if (plan.splits == 1) {
-                store4(p, m, n, acc[i][j]);
-            } else {  // N4 = N rounded up to 4: whole vectors
-                const int64_t n4 = (p.N + 3) & ~3;
-                if (n < p.N) *reinterpret_cast<f32x4*>(p.partial + ((int64_t)z * p.M + m) * n4 + n) = acc[i][j];
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int q = 0; q < 16 / V; ++q) {
+                    VT v;
+#pragma unroll
+                    for (int e = 0; e < V; ++e) v[e] = (T)acc[i][j][q * V + e];
+                    box[r * CH + (((wn + 32 * j + 16 * half) / V + q) ^ (r & (CH - 1)))] = v;
+                }
+            __syncthreads();
+#pragma unroll 4
+            for (int k = tid; k < ROWS_NOW * CH; k += 64 * WAVES) {
+                const int r2 = k / CH, ch = k % CH;
+                const int m = m0 + r2 / 32 * (TM / WGM) + i * 32 + r2 % 32, n = n0 + ch * V;
+                if (m >= p.M || n >= width) continue;
+                const VT v = box[r2 * CH + (ch ^ (r2 & (CH - 1)))];
+                T* to = c + (int64_t)m * ld + n;
+                typedef T VU __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+                if (n + V <= width) {
+                    *reinterpret_cast<VU*>(to) = v;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < V; ++e)
+                        if (n + e < width) to[e] = v[e];
+                }
             }
         }
+    };
+    if constexpr (TN * WGM * 32 * sizeof(float) <= sizeof(tile_0)) {
+        if (plan.splits > 1) {  // rows of N rounded up to 4: the join reads whole vectors
+            const int64_t n4 = (p.N + 3) & ~3;
+            return leave(0.f, p.partial + (int64_t)z * p.M * n4, n4, (int)n4);
+        }
+        if constexpr (FINE) return leave(0.f, (float*)p.c, p.ldc, p.N);
+    }
+    if constexpr (!FINE) {
+        if (p.out_dtype == MAXSIM_BF16)
+            leave((__bf16)0.f, (__bf16*)p.c, p.ldc, p.N);
+        else
+            leave((_Float16)0.f, (_Float16*)p.c, p.ldc, p.N);
     }
 }
 
@@ -360,8 +465,7 @@ __global__ __launch_bounds__(512) void gemm_rows_kernel(GemmArgs p, int steps) {
 #pragma unroll
     for (int i = 0; i < NI; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    auto fold = [&](int kb, i32x8 b_bytes, const i32x8* a_bytes) {
-        const Operand<FINE> bv = operand_of<FINE>(b_bytes);
+    auto fold = [&](int kb, i32x8 bv, const i32x8* av) {
         f32x4 t;
         if constexpr (ROWS) {
 #pragma unroll
@@ -372,7 +476,7 @@ __global__ __launch_bounds__(512) void gemm_rows_kernel(GemmArgs p, int steps) {
         }
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            const f32x4 d = mfma<FINE>(bv, operand_of<FINE>(a_bytes[i]));
+            const f32x4 d = mfma16<FINE>(bv, av[i]);
             const float s = sa[i][kb];
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[i][e] = __builtin_fmaf(d[e] * t[e], s, acc[i][e]);
@@ -443,7 +547,7 @@ TilePlan plan_tiles(int M, int N, int K, int tm, int tn) {
 }
 
 // 256 x 256 tiles where they still give every CU one; else 128 x 128.
-bool big_tiles(int M, int N) { return ceil_div(M, 256) * ceil_div(N, 256) >= kCUs / 2; }
+bool big_tiles(int M, int N, bool fine) { return !fine && ceil_div(M, 256) * ceil_div(N, 256) >= kCUs / 2; }
 
 template <typename F>
 void by_kind(const GemmArgs& a, F&& go) {
@@ -458,8 +562,9 @@ template <int TM, int TN, int WGM, int WGN>
 void launch_tiles(const GemmArgs& a, const TilePlan& t, hipStream_t stream) {
     const unsigned grid = (unsigned)(t.tiles_m * t.tiles_n * t.splits);
     by_kind(a, [&](auto rows, auto fine) {
-        gemm_tile_kernel<TM, TN, WGM, WGN, decltype(rows)::value, decltype(fine)::value>
-            <<<grid, 64 * WGM * WGN, 0, stream>>>(a, t);
+        constexpr bool ROWS = decltype(rows)::value, FINE = decltype(fine)::value;
+        if constexpr (!FINE || TM * TN <= 128 * 128)  // fp16 operands of a larger tile do not fit the registers
+            gemm_tile_kernel<TM, TN, WGM, WGN, ROWS, FINE><<<grid, 64 * WGM * WGN, 0, stream>>>(a, t);
     });
 }
 
@@ -475,7 +580,7 @@ void launch_rows(const GemmArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t gemm_fp8_workspace_bytes(int M, int N, int K) {
-    if (M <= kFewRows || big_tiles(M, N)) return 0;
+    if (M <= kFewRows) return 0;
     const TilePlan t = plan_tiles(M, N, K, 128, 128);
     return t.splits == 1 ? 0 : (size_t)t.splits * M * (size_t)((N + 3) & ~3) * sizeof(float);
 }
@@ -493,7 +598,7 @@ hipError_t launch_gemm_fp8(const GemmArgs& a, hipStream_t stream) {
             launch_rows<4>(a, stream);
         return hipGetLastError();
     }
-    if (big_tiles(a.M, a.N)) {
+    if (big_tiles(a.M, a.N, a.out_dtype == MAXSIM_F32)) {
         TilePlan t = plan_tiles(a.M, a.N, a.K, 256, 256);
         t.splits = 1;
         t.per_split = t.steps;
