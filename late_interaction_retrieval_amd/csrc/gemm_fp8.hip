@@ -15,8 +15,8 @@
 //   * Workgroups that share rows of A or B follow each other on one XCD.
 //   * Where tiles are few, K is split over workgroups whose fp32 partial sums
 //     a second launch adds in order.
-//   * Up to 64 rows of A (single queries) take a kernel bound by the bytes of B:
-//     operands go straight to registers and a workgroup's waves split K.
+//   * Few rows of A (a query) take a kernel bound by the bytes of B: operands go
+//     straight to registers and a workgroup's waves split K.
 #include <algorithm>
 #include <type_traits>
 
@@ -133,11 +133,12 @@ __device__ __forceinline__ void load_lds(const void* base, uint32_t nbytes, uint
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, lds, 4, (int)voff, 0, 0, 0);
 }
 
-// Every direct load of this wave has landed; then the workgroup's barrier, for
-// LDS only (__syncthreads would not keep the next tile's loads in flight).
+// This wave's direct loads have landed (LANDED) and its LDS accesses are done;
+// then the workgroup's barrier (__syncthreads would not keep the next tile's loads in flight).
+template <bool LANDED>
 __device__ __forceinline__ void tile_barrier() {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt(LANDED ? 0x0070 : 0xC07F);  // vmcnt(0) lgkmcnt(0), or lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
@@ -190,12 +191,14 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_tile_kernel(GemmArgs p, T
     constexpr int SA = TM, SB = ROWS ? TN : 64;  // scales of a step: of each row, or of 128 rows of B in 64 words
     static_assert(LA * 8 * LOADERS == TM && LB * 8 * LOADERS == TN && TN / WGN <= kQBlock && LA % 2 == 0 && LB % 4 == 0,
                   "tile");
+    constexpr int LS = ((SA + SB) / 64 + LOADERS - 1) / LOADERS;  // a loading wave's loads of 64 scales
     // Two arrays and a loop unrolled by two, not one array indexed by the step:
     // the compiler then sees that a step's reads and the next tile's direct
     // loads touch different memory, and does not make the reads wait for them.
-    __shared__ __align__(16) uint8_t tile_0[(TM + TN) * kStep], tile_1[(TM + TN) * kStep];
-    constexpr int LS = ((SA + SB) / 64 + LOADERS - 1) / LOADERS;  // a wave's loads of 64 scales
-    __shared__ __align__(16) float scale_0[LS * LOADERS * 64], scale_1[LS * LOADERS * 64];
+    // (A third buffer was slower: 256 x 128 tiles 37 -> 40 us, 97 -> 108 us.)
+    constexpr int TILE = (TM + TN) * kStep, SCALES = LS * LOADERS * 64;
+    __shared__ __align__(16) uint8_t tile_0[TILE], tile_1[TILE];
+    __shared__ __align__(16) float scale_0[SCALES], scale_1[SCALES];
     const int tid = threadIdx.x;
     const int lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
@@ -237,6 +240,17 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_tile_kernel(GemmArgs p, T
     const float* sb = p.b_scale + (int64_t)(ROWS ? n0 : n0 / kQBlock) * plan.steps;
     const int scales_b = ROWS ? rows_b : (rows_b + kQBlock - 1) / kQBlock;
 
+    // Step `at` takes block `at` of K; or, where each row of A is read once (one
+    // column of tiles), the blocks turned by the tile: workgroups all at the same
+    // distance from their rows' starts would press on a few of HBM's channels.
+    constexpr bool TURN = TM > TN;
+    const int count = k_end - k_begin, turn = TURN && plan.tiles_n == 1 && count > 0 ? (int)((m0 / TM) % count) : 0;
+    auto block_of = [&](int at) {
+        if constexpr (!TURN) return at;
+        const int kb = at + turn;
+        return at >= k_end ? k_end : kb >= k_end ? kb - count : kb;
+    };
+
     // One operand's part of tile kb: rows [first, first + 8 * L) of the `rows` of the tile.
     auto load_rows = [&](const uint8_t* base, int64_t ld, int first, int rows, const uint32_t* off, const uint32_t* chunk,
                          int kb, uint8_t* to, auto count, auto period) {
@@ -252,8 +266,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_tile_kernel(GemmArgs p, T
             at += 8 * ld;
         }
     };
-    auto load = [&](int kb, uint8_t* tile, float* scale) {
+    auto load = [&](int at, uint8_t* tile, float* scale) {
         if (wave >= LOADERS) return;
+        const int kb = block_of(at);
         load_rows(p.A + (int64_t)m0 * p.lda, p.lda, wave * LA * 8, rows_a, off_a, chunk_a, kb, tile + wave * LA * 8 * kStep,
                   std::integral_constant<int, LA>{}, std::integral_constant<int, 1>{});
         load_rows(p.B + (int64_t)n0 * p.ldb, p.ldb, wave * LB * 8, rows_b, off_b, chunk_b, kb,
@@ -295,8 +310,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_tile_kernel(GemmArgs p, T
         asm volatile("" : "+v"(c));  // here, and not sunk to a later block that reads c
     };
     // K ends inside a chunk: clear what follows it there
-    auto end_of_k = [&](int kb, uint8_t* tile) {
-        if (kb != plan.steps - 1 || (p.K & 15) == 0) return;
+    auto end_of_k = [&](int at, uint8_t* tile) {
+        if (block_of(at) != plan.steps - 1 || (p.K & 15) == 0) return;
         const int last = (p.K & (kStep - 1)) >> 4, keep = p.K & 15;
         for (int r = tid; r < TM + TN; r += 64 * WAVES) {
             const int s = r < TM ? swz_a(r) : swz_b(r - TM);
@@ -307,10 +322,10 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_tile_kernel(GemmArgs p, T
                 if (left < 4) w[i] = left <= 0 ? 0u : w[i] & ((1u << (8 * left)) - 1u);
             }
         }
-        tile_barrier();
+        tile_barrier<false>();
     };
     auto step = [&](int kb, uint8_t* tile, const float* scale, uint8_t* next, float* next_scale) {
-        tile_barrier();
+        tile_barrier<true>();
         end_of_k(kb, tile);
         load(kb + 1, next, next_scale);
         // Half `half` of the wave holds chunks 2 half, 2 half + 1 of each 64 of K; blocks of 32 rows share a lane's
@@ -375,43 +390,48 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_tile_kernel(GemmArgs p, T
     auto leave = [&](auto type, auto* c, int64_t ld, int width) {
         typedef decltype(type) T;
         constexpr int V = 16 / sizeof(T), CH = TN / V;  // values of a chunk, chunks of a row
-        constexpr int ROWS_NOW = WGM * 32;
-        static_assert(ROWS_NOW * TN * sizeof(T) <= sizeof(tile_0) && CH >= 16, "LDS");
+        // rows of waves at a time
+        constexpr int FIT = TILE / (32 * TN * (int)sizeof(T)), NOW = FIT >= WGM ? WGM : FIT >= WGM / 2 ? WGM / 2 : WGM / 4;
+        static_assert(NOW >= 1 && NOW * 32 * TN * sizeof(T) <= TILE && CH >= 16, "LDS");
         typedef T VT __attribute__((ext_vector_type(V)));
         VT* box = reinterpret_cast<VT*>(tile_0);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-            __syncthreads();
-            const int r = wave / WGN * 32 + col;
+        for (int i = 0; i < NI; ++i)
 #pragma unroll
-            for (int j = 0; j < NJ; ++j)
+            for (int g = 0; g < WGM; g += NOW) {
+                __syncthreads();
+                if (wave / WGN >= g && wave / WGN < g + NOW) {
+                    const int r = (wave / WGN - g) * 32 + col;
 #pragma unroll
-                for (int q = 0; q < 16 / V; ++q) {
-                    VT v;
+                    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) v[e] = (T)acc[i][j][q * V + e];
-                    box[r * CH + (((wn + 32 * j + 16 * half) / V + q) ^ (r & (CH - 1)))] = v;
+                        for (int q = 0; q < 16 / V; ++q) {
+                            VT v;
+#pragma unroll
+                            for (int e = 0; e < V; ++e) v[e] = (T)acc[i][j][q * V + e];
+                            box[r * CH + (((wn + 32 * j + 16 * half) / V + q) ^ (r & (CH - 1)))] = v;
+                        }
                 }
-            __syncthreads();
+                __syncthreads();
 #pragma unroll 4
-            for (int k = tid; k < ROWS_NOW * CH; k += 64 * WAVES) {
-                const int r2 = k / CH, ch = k % CH;
-                const int m = m0 + r2 / 32 * (TM / WGM) + i * 32 + r2 % 32, n = n0 + ch * V;
-                if (m >= p.M || n >= width) continue;
-                const VT v = box[r2 * CH + (ch ^ (r2 & (CH - 1)))];
-                T* to = c + (int64_t)m * ld + n;
-                typedef T VU __attribute__((ext_vector_type(V), aligned(sizeof(T))));
-                if (n + V <= width) {
-                    *reinterpret_cast<VU*>(to) = v;
-                } else {
+                for (int k = tid; k < NOW * 32 * CH; k += 64 * WAVES) {
+                    const int r = k / CH, ch = k % CH;
+                    const int m = m0 + (g + r / 32) * (TM / WGM) + i * 32 + r % 32, n = n0 + ch * V;
+                    if (m >= p.M || n >= width) continue;
+                    const VT v = box[r * CH + (ch ^ (r & (CH - 1)))];
+                    T* to = c + (int64_t)m * ld + n;
+                    typedef T VU __attribute__((ext_vector_type(V), aligned(sizeof(T))));
+                    if (n + V <= width) {
+                        *reinterpret_cast<VU*>(to) = v;
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < V; ++e)
-                        if (n + e < width) to[e] = v[e];
+                        for (int e = 0; e < V; ++e)
+                            if (n + e < width) to[e] = v[e];
+                    }
                 }
             }
-        }
     };
-    if constexpr (TN * WGM * 32 * sizeof(float) <= sizeof(tile_0)) {
+    if constexpr (TN <= 128) {  // tiles that split K, or have fp32 results
         if (plan.splits > 1) {  // rows of N rounded up to 4: the join reads whole vectors
             const int64_t n4 = (p.N + 3) & ~3;
             return leave(0.f, p.partial + (int64_t)z * p.M * n4, n4, (int)n4);
@@ -528,26 +548,53 @@ __global__ __launch_bounds__(512) void gemm_rows_kernel(GemmArgs p, int steps) {
     }
 }
 
-constexpr int kFewRows = 64;
 constexpr int kCUs = 256;
 
-TilePlan plan_tiles(int M, int N, int K, int tm, int tn) {
-    TilePlan t;
-    t.tiles_m = (int)ceil_div(M, tm);
-    t.tiles_n = (int)ceil_div(N, tn);
-    t.steps = (int)ceil_div(K, kStep);
-    const int64_t tiles = (int64_t)t.tiles_m * t.tiles_n;
-    // fewer tiles than half the CUs: split K, at least 8 steps to a split
-    int s = tiles * 2 > kCUs ? 1 : (int)(kCUs / tiles);
-    s = std::max(1, std::min(s, t.steps / 8));
-    t.per_split = (int)ceil_div(t.steps, s);
-    t.splits = t.per_split ? (int)ceil_div(t.steps, t.per_split) : 1;
-    t.splits = std::max(1, t.splits);
-    return t;
-}
+// Few rows: each lane's share of A comes from memory as often as B's, so long
+// rows of more than a few tokens are better shared through LDS.  Us by
+// this kernel and by tiles (N x K): 32 rows 2048 x 2048 5.6, 8.0; 4096 x 4096 9.3, 11.3;
+// 8192 x 8192 30, 18; 16 rows of it 20, 17; 1 row of it 12.4, 16.5.
+bool few_rows(int M, int K) { return M <= 4 || (M <= 32 && K <= 4096); }
 
-// 256 x 256 tiles where they still give every CU one; else 128 x 128.
-bool big_tiles(int M, int N, bool fine) { return !fine && ceil_div(M, 256) * ceil_div(N, 256) >= kCUs / 2; }
+// How a product is cut up: by 256 x 256 tiles where they give every other CU
+// one; by 256 x 128 where they give every CU one (or, for fp32 results, where K
+// split does); else by 128 x 128, or 64 x 128 where those are too few.
+// Us by 128 x 128 and 64 x 128: 512 x 2048 x 2048 14.6, 12.8; 100 x 2048 x 2048
+// 11.7, 9.3; by 128 x 128 and 256 x 128, 65536 x 128 x 2048: 43, 37.
+enum TileKind { kBig, kTall, kSmall, kLow };
+struct Cut {
+    TileKind kind;
+    TilePlan plan;
+};
+Cut cut(int M, int N, int K, bool fine) {
+    const int64_t tall = ceil_div(M, 256) * ceil_div(N, 128), steps = ceil_div(K, kStep);
+    Cut c;
+    if (!fine && N > 128 && ceil_div(M, 256) * ceil_div(N, 256) >= kCUs / 2)
+        c.kind = kBig;
+    else if (tall >= kCUs || (fine && tall * (steps / 8) >= kCUs))
+        c.kind = kTall;
+    else
+        c.kind = ceil_div(M, 128) * ceil_div(N, 128) > kCUs / 2 ? kSmall : kLow;
+    TilePlan& t = c.plan;
+    t.tiles_m = (int)ceil_div(M, c.kind == kLow ? 64 : c.kind == kSmall ? 128 : 256);
+    t.tiles_n = (int)ceil_div(N, c.kind == kBig ? 256 : 128);
+    t.steps = (int)steps;
+    // Split K while it pays: a step costs about this, the second launch 4 us
+    // and the partial sums' way to memory and back.
+    const double step_us = c.kind == kTall ? (fine ? 2.2 : 1.3) : c.kind == kSmall ? 0.9 : 0.75;
+    const double sums_us = (double)M * N * 8 / 4e6;
+    const int64_t tiles = (int64_t)t.tiles_m * t.tiles_n;
+    const int64_t most = c.kind == kBig ? 1 : std::min<int64_t>(kCUs / tiles, steps / 4);
+    int best = 1;
+    double best_us = steps * step_us;
+    for (int s = 2; s <= most; ++s) {
+        const double us = (double)ceil_div(steps, s) * step_us + 4 + s * sums_us;
+        if (us < best_us) best = s, best_us = us;
+    }
+    t.per_split = (int)ceil_div(steps, best);
+    t.splits = t.per_split ? (int)ceil_div(steps, t.per_split) : 1;
+    return c;
+}
 
 template <typename F>
 void by_kind(const GemmArgs& a, F&& go) {
@@ -563,7 +610,7 @@ void launch_tiles(const GemmArgs& a, const TilePlan& t, hipStream_t stream) {
     const unsigned grid = (unsigned)(t.tiles_m * t.tiles_n * t.splits);
     by_kind(a, [&](auto rows, auto fine) {
         constexpr bool ROWS = decltype(rows)::value, FINE = decltype(fine)::value;
-        if constexpr (!FINE || TM * TN <= 128 * 128)  // fp16 operands of a larger tile do not fit the registers
+        if constexpr (!FINE || TN <= 128)  // fp16 operands of a larger tile do not fit the registers
             gemm_tile_kernel<TM, TN, WGM, WGN, ROWS, FINE><<<grid, 64 * WGM * WGN, 0, stream>>>(a, t);
     });
 }
@@ -580,36 +627,32 @@ void launch_rows(const GemmArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t gemm_fp8_workspace_bytes(int M, int N, int K) {
-    if (M <= kFewRows) return 0;
-    const TilePlan t = plan_tiles(M, N, K, 128, 128);
-    return t.splits == 1 ? 0 : (size_t)t.splits * M * (size_t)((N + 3) & ~3) * sizeof(float);
+    if (few_rows(M, K)) return 0;
+    const size_t partial = (size_t)M * (size_t)((N + 3) & ~3) * sizeof(float);
+    const int s = std::max(cut(M, N, K, false).plan.splits, cut(M, N, K, true).plan.splits);
+    return s > 1 ? s * partial : 0;  // enough for every type of result
 }
 
 hipError_t launch_gemm_fp8(const GemmArgs& a, hipStream_t stream) {
-    if (a.M <= kFewRows) {
-        const int ni = (a.M + 15) / 16;
-        if (ni == 1)
+    if (few_rows(a.M, a.K)) {
+        if (a.M <= 16)
             launch_rows<1>(a, stream);
-        else if (ni == 2)
-            launch_rows<2>(a, stream);
-        else if (ni == 3)
-            launch_rows<3>(a, stream);
         else
-            launch_rows<4>(a, stream);
+            launch_rows<2>(a, stream);
         return hipGetLastError();
     }
-    if (big_tiles(a.M, a.N, a.out_dtype == MAXSIM_F32)) {
-        TilePlan t = plan_tiles(a.M, a.N, a.K, 256, 256);
-        t.splits = 1;
-        t.per_split = t.steps;
-        launch_tiles<256, 256, 4, 2>(a, t, stream);
-        return hipGetLastError();
-    }
-    const TilePlan t = plan_tiles(a.M, a.N, a.K, 128, 128);
-    launch_tiles<128, 128, 2, 2>(a, t, stream);
-    if (t.splits > 1) {
+    const Cut c = cut(a.M, a.N, a.K, a.out_dtype == MAXSIM_F32);
+    if (c.kind == kBig)
+        launch_tiles<256, 256, 4, 2>(a, c.plan, stream);
+    else if (c.kind == kTall)
+        launch_tiles<256, 128, 4, 2>(a, c.plan, stream);
+    else if (c.kind == kSmall)
+        launch_tiles<128, 128, 4, 2>(a, c.plan, stream);
+    else
+        launch_tiles<64, 128, 2, 4>(a, c.plan, stream);
+    if (c.plan.splits > 1) {
         const int64_t vecs = (int64_t)a.M * ((a.N + 3) / 4);
-        gemm_join_kernel<<<(unsigned)std::min<int64_t>(ceil_div(vecs, 256), 4096), 256, 0, stream>>>(a, t.splits);
+        gemm_join_kernel<<<(unsigned)std::min<int64_t>(ceil_div(vecs, 256), 4096), 256, 0, stream>>>(a, c.plan.splits);
     }
     return hipGetLastError();
 }
