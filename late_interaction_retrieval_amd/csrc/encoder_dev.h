@@ -116,27 +116,27 @@ __device__ __forceinline__ float sum64(float v) {
 // multiplies and corrects its values.
 struct Scale {
     float s;     // as stored
-    float inv;   // 1 / s
+    float inv;   // 1 / s to a unit in the last place
     bool zeros;  // the block is held as zeros (too small, or not finite)
 };
+// v / s correctly rounded in 3 operations (a division has ten), given inv =
+// 1 / s to a unit in the last place: the product is within 3 units, its
+// remainder is exact in a fused multiply-add, and the correction rounds once.
+__device__ __forceinline__ float quotient(float v, float s, float inv) {
+    const float q = v * inv;
+    return __builtin_fmaf(__builtin_fmaf(-q, s, v), inv, q);
+}
 __device__ __forceinline__ Scale block_scale(uint32_t top, float largest) {
     Scale r;
     const bool tiny = top < 0x0D800000u;    // 2^-100
     const bool broken = top >= 0x7F800000u;  // infinity or NaN
-    r.s = tiny ? 1.f : __uint_as_float(top) / largest;
+    r.s = tiny ? 1.f : quotient(__uint_as_float(top), largest, 1.f / largest);
     if (broken) r.s = __uint_as_float(0x7FC00000u);
-    r.inv = 1.f / r.s;
+    r.inv = __builtin_amdgcn_rcpf(r.s);
     r.zeros = tiny || broken;
     return r;
 }
-// v / s correctly rounded, in 3 operations in place of a division's ten: the
-// product with the rounded reciprocal is within 2 units in the last place, the
-// remainder of it is exact in a fused multiply-add, and the correction rounds once.
-__device__ __forceinline__ float scaled(float v, const Scale& k) {
-    const float q = v * k.inv;
-    const float r = __builtin_fmaf(-q, k.s, v);
-    return __builtin_fmaf(r, k.inv, q);
-}
+__device__ __forceinline__ float scaled(float v, const Scale& k) { return quotient(v, k.s, k.inv); }
 // 8 values in e4m3 (the conversion rounds to nearest even; |v / s| is at most
 // 448 and a rounding error, which rounds to 448).
 __device__ __forceinline__ u32x2 to_e4m3(const float* v, const Scale& k) {

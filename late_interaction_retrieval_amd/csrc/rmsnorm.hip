@@ -246,22 +246,25 @@ __global__ __launch_bounds__(Rows<TPR>::threads) void rmsnorm_bwd_kernel(NormBwd
     }
 }
 
-// dweight = the partial rows, added in order: 16 columns x 16 runs of rows to a
-// workgroup, so that a few hundred partial rows are read by many waves.
-constexpr int kReduceCols = 16;
-__global__ __launch_bounds__(256) void rmsnorm_dweight_kernel(const float* partial, int groups, int H, float* dw) {
-    __shared__ float run[16][kReduceCols];
+// dweight = the partial rows, added in a fixed order: a workgroup takes 32
+// columns (one line of each row), its 32 runs of 32 threads every 32nd row, so
+// that a few hundred rows are on their way at once.
+constexpr int kReduceCols = 32, kReduceRuns = 32;
+__global__ __launch_bounds__(kReduceCols * kReduceRuns) void rmsnorm_dweight_kernel(const float* partial, int groups,
+                                                                                   int H, float* dw) {
+    __shared__ float run[kReduceRuns][kReduceCols];
     const int col = threadIdx.x % kReduceCols, part = threadIdx.x / kReduceCols;
     const int c = blockIdx.x * kReduceCols + col;
-    const int per = (groups + 15) / 16;
-    const int end = min(groups, (part + 1) * per);
     float s = 0.f;
-    if (c < H)
-        for (int g = part * per; g < end; ++g) s += partial[(int64_t)g * H + c];
+    if (c < H) {
+#pragma unroll 8
+        for (int g = part; g < groups; g += kReduceRuns) s += partial[(int64_t)g * H + c];
+    }
     run[part][col] = s;
     __syncthreads();
     if (part == 0 && c < H) {
-        for (int q = 1; q < 16; ++q) s += run[q][col];
+#pragma unroll
+        for (int q = 1; q < kReduceRuns; ++q) s += run[q][col];
         dw[c] = s;
     }
 }
@@ -303,7 +306,7 @@ hipError_t launch_rmsnorm_fwd(const NormArgs& a, hipStream_t stream) {
 int norm_bwd_groups(int R, int H) {
     const int per = H <= 128 ? 16 : H <= 1024 ? 4 : 1;
     const int64_t rows = ceil_div(R, per);
-    const int most = H <= 8192 ? 1024 : 512;
+    const int most = 512;
     return (int)(rows < most ? rows : most);
 }
 
@@ -320,7 +323,7 @@ hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, hipStream_t stream) {
         if (e != hipSuccess) return e;
     }
     if (a.dweight != nullptr)
-        rmsnorm_dweight_kernel<<<(a.H + kReduceCols - 1) / kReduceCols, 256, 0, stream>>>(a.partial, groups, a.H,
+        rmsnorm_dweight_kernel<<<(a.H + kReduceCols - 1) / kReduceCols, kReduceCols * kReduceRuns, 0, stream>>>(a.partial, groups, a.H,
                                                                                           a.dweight);
     return hipGetLastError();
 }
