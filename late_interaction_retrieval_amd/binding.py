@@ -646,15 +646,15 @@ def _on_its_device(f):
         dev = first.device
         if dev.type != "cuda":
             raise ValueError("%s: the tensors must be on the device" % f.__name__)
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError("%s: the stream is on %s, the tensors on %s" % (f.__name__, stream.device, dev))
-            with torch.cuda.stream(stream):
-                return f(first, *args, **kw)
-        if dev.index != torch._C._cuda_getDevice():
+        if stream is None and dev.index == torch._C._cuda_getDevice():
+            return f(first, *args, **kw)
+        if stream is None:
             with torch.cuda.device(dev):
                 return f(first, *args, **kw)
-        return f(first, *args, **kw)
+        if stream.device != dev:
+            raise ValueError("%s: the stream is on %s, the tensors on %s" % (f.__name__, stream.device, dev))
+        with torch.cuda.stream(stream):
+            return f(first, *args, **kw)
 
     return call
 
@@ -671,10 +671,13 @@ def _code(dtype, allowed, name):
 
 
 _FLOATS = (MAXSIM_F16, MAXSIM_BF16, MAXSIM_F32)
+_ALL = _FLOATS + (MAXSIM_I8, MAXSIM_E4M3)
 
 
 def _rows(t, name, shape, dtype, dev):
     """The pitch of t as rows of its last dimension; t has `shape` and `dtype` and lies on `dev`."""
+    if t.dtype is dtype and t.is_contiguous() and t.shape == shape and t.device == dev:
+        return shape[-1]
     if t.device != dev:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
     if t.dtype != dtype:
@@ -682,8 +685,6 @@ def _rows(t, name, shape, dtype, dev):
     if t.shape != shape:
         raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     width = shape[-1]
-    if t.is_contiguous():
-        return width
     # rows one pitch apart through all leading dimensions, neighbours within a row
     pitch, rows = None, 1
     for d in range(len(shape) - 2, -1, -1):
@@ -705,6 +706,8 @@ def _rows(t, name, shape, dtype, dev):
 
 def _flat(t, name, n, dtype, dev):
     """t holds n values of `dtype` back to back on `dev`."""
+    if t.dtype is dtype and t.is_contiguous() and t.numel() == n and t.device == dev:
+        return
     if t.device != dev:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
     if t.dtype != dtype:
@@ -713,16 +716,18 @@ def _flat(t, name, n, dtype, dev):
         raise ValueError("%s must hold %d contiguous values" % (name, n))
 
 
-def _empty_e4m3(shape, dev):
+def _empty_e4m3(like, shape):
     """[..., width] e4m3 with rows a multiple of 16 bytes apart, as the product reads them."""
     width = shape[-1]
     pad = -width % 16
     if pad == 0:
-        return torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev)
-    return torch.empty(tuple(shape[:-1]) + (width + pad,), dtype=torch.float8_e4m3fn, device=dev)[..., :width]
+        return like.new_empty(shape, dtype=torch.float8_e4m3fn)
+    return like.new_empty(tuple(shape[:-1]) + (width + pad,), dtype=torch.float8_e4m3fn)[..., :width]
 
 
 def _row_count(shape):
+    if len(shape) == 2:
+        return shape[0]
     n = 1
     for s in shape[:-1]:
         n *= s
@@ -747,39 +752,47 @@ def maxsim_rmsnorm_fwd(x, weight=None, eps=1e-6, residual=None, out_dtype=None, 
     maxsim_fwd_i8) or float8_e4m3fn (a scale for each 128 columns: the operand of maxsim_gemm_fp8).
     Returns (y, scale or None, sum or None, rstd or None); sum = x + residual in x's type, rstd [...] fp32.
     """
-    dev, shape = x.device, x.shape
+    dev, shape, dtype = x.device, x.shape, x.dtype
     H, R = shape[-1], _row_count(shape)
-    code = _code(x.dtype, _FLOATS, "x")
-    out_dtype = x.dtype if out_dtype is None else out_dtype
-    out = _code(out_dtype, (0, 1, 2, 3, 4), "out_dtype")
-    ldx = _rows(x, "x", shape, x.dtype, dev)
-    w, w_code = _gain(weight, H, x.dtype, dev)
-    ldr = lds = H
+    code = _code(dtype, _FLOATS, "x")
+    out_dtype = dtype if out_dtype is None else out_dtype
+    out = _code(out_dtype, _ALL, "out_dtype")
+    ldx = _rows(x, "x", shape, dtype, dev)
+    w, w_code = _gain(weight, H, dtype, dev)
+    ldr = lds = ldy = H
+    residual_at = sum_at = rstd_at = scale_at = None
     if residual is not None:
-        ldr = _rows(residual, "residual", shape, x.dtype, dev)
+        ldr = _rows(residual, "residual", shape, dtype, dev)
+        residual_at = residual.data_ptr()
         if sum is None:
-            sum = torch.empty(shape, dtype=x.dtype, device=dev)
-    if sum is not None:
-        lds = _rows(sum, "sum", shape, x.dtype, dev)
-    if y is None:
-        y = _empty_e4m3(shape, dev) if out == MAXSIM_E4M3 else torch.empty(shape, dtype=out_dtype, device=dev)
-    ldy = _rows(y, "y", shape, out_dtype, dev)
+            sum = x.new_empty(shape)
+            sum_at = sum.data_ptr()
+    if sum is not None and sum_at is None:
+        lds = _rows(sum, "sum", shape, dtype, dev)
+        sum_at = sum.data_ptr()
+    if y is not None or out == MAXSIM_E4M3:
+        if y is None:
+            y = _empty_e4m3(x, shape)
+        ldy = _rows(y, "y", shape, out_dtype, dev)
+    else:
+        y = x.new_empty(shape, dtype=out_dtype)
     if out >= MAXSIM_I8:
-        want = shape[:-1] + (-(-H // QBLOCK),) if out == MAXSIM_E4M3 else shape[:-1]
+        want = shape[:-1] if out == MAXSIM_I8 else shape[:-1] + (-(-H // QBLOCK),)
         if scale is None:
-            scale = torch.empty(want, dtype=torch.float32, device=dev)
+            scale = x.new_empty(want, dtype=torch.float32)
         else:
-            _flat(scale, "scale", R * (want[-1] if out == MAXSIM_E4M3 else 1), torch.float32, dev)
+            _flat(scale, "scale", R * (1 if out == MAXSIM_I8 else want[-1]), torch.float32, dev)
+        scale_at = scale.data_ptr()
     elif scale is not None:
         raise ValueError("scale goes with an 8-bit output")
     if rstd is not None:
         _flat(rstd, "rstd", R, torch.float32, dev)
     elif with_rstd:
-        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
-    st = _lib.maxsim_rmsnorm_fwd(x.data_ptr(), ldx, None if residual is None else residual.data_ptr(), ldr, w, w_code,
-                                 R, H, code, eps, out, y.data_ptr(), ldy, None if scale is None else scale.data_ptr(),
-                                 None if sum is None else sum.data_ptr(), lds,
-                                 None if rstd is None else rstd.data_ptr(), _raw_stream(dev))
+        rstd = x.new_empty(shape[:-1], dtype=torch.float32)
+    if rstd is not None:
+        rstd_at = rstd.data_ptr()
+    st = _lib.maxsim_rmsnorm_fwd(x.data_ptr(), ldx, residual_at, ldr, w, w_code, R, H, code, eps, out, y.data_ptr(),
+                                 ldy, scale_at, sum_at, lds, rstd_at, _raw_stream(dev))
     if st:
         _check(st, "maxsim_rmsnorm_fwd")
     return y, scale, sum, rstd
@@ -794,28 +807,31 @@ def maxsim_rmsnorm_bwd(dy, h, rstd, weight=None, dsum=None, with_dweight=True, d
     """Backward of the norm.  dy [..., H] is the gradient of y, h the forward's sum (x without a residual), rstd its
     rstd, dsum the gradient that arrives at sum itself.  Returns (dx, dweight [H] fp32 or None); dx is the gradient
     of x and of residual alike."""
-    dev, shape = h.device, h.shape
+    dev, shape, dtype = h.device, h.shape, h.dtype
     H, R = shape[-1], _row_count(shape)
-    code = _code(h.dtype, _FLOATS, "h")
-    ldh = _rows(h, "h", shape, h.dtype, dev)
-    lddy = _rows(dy, "dy", shape, h.dtype, dev)
+    code = _code(dtype, _FLOATS, "h")
+    ldh = _rows(h, "h", shape, dtype, dev)
+    lddy = _rows(dy, "dy", shape, dtype, dev)
     _flat(rstd, "rstd", R, torch.float32, dev)
-    w, w_code = _gain(weight, H, h.dtype, dev)
-    ldds = H if dsum is None else _rows(dsum, "dsum", shape, h.dtype, dev)
+    w, w_code = _gain(weight, H, dtype, dev)
+    ldds = H if dsum is None else _rows(dsum, "dsum", shape, dtype, dev)
+    lddx = H
     if dx is None:
-        dx = torch.empty(shape, dtype=h.dtype, device=dev)
-    lddx = _rows(dx, "dx", shape, h.dtype, dev)
+        dx = h.new_empty(shape)
+    else:
+        lddx = _rows(dx, "dx", shape, dtype, dev)
     nbytes = 0
     if dweight is None and with_dweight:
-        dweight = torch.empty(H, dtype=torch.float32, device=dev)
+        dweight = h.new_empty(H, dtype=torch.float32)
     elif dweight is not None:
         _flat(dweight, "dweight", H, torch.float32, dev)
     if dweight is not None:
         if workspace is None:
-            workspace = torch.empty(max(16, _lib.maxsim_rmsnorm_bwd_workspace_bytes(R, H)), dtype=torch.uint8,
-                                    device=dev)
-        _need(workspace, "workspace", device=dev)
-        nbytes = workspace.numel() * workspace.element_size()
+            nbytes = max(16, _lib.maxsim_rmsnorm_bwd_workspace_bytes(R, H))
+            workspace = h.new_empty(nbytes, dtype=torch.uint8)
+        else:
+            _need(workspace, "workspace", device=dev)
+            nbytes = workspace.numel() * workspace.element_size()
     st = _lib.maxsim_rmsnorm_bwd(dy.data_ptr(), lddy, h.data_ptr(), ldh, rstd.data_ptr(), w, w_code,
                                  None if dsum is None else dsum.data_ptr(), ldds, R, H, code, dx.data_ptr(), lddx,
                                  None if dweight is None else dweight.data_ptr(),
@@ -841,11 +857,11 @@ def maxsim_quant_fp8(x, block_rows=1, rows=True, transposed=False):
     rb, cb = -(-R // QBLOCK), -(-C // QBLOCK)
     q = scale = qt = scale_t = None
     if rows:
-        q = _empty_e4m3((R, C), dev)
-        scale = torch.empty((R if block_rows == 1 else rb, cb), dtype=torch.float32, device=dev)
+        q = _empty_e4m3(x, (R, C))
+        scale = x.new_empty((R if block_rows == 1 else rb, cb), dtype=torch.float32)
     if transposed:
-        qt = _empty_e4m3((C, R), dev)
-        scale_t = torch.empty((C if block_rows == 1 else cb, rb), dtype=torch.float32, device=dev)
+        qt = _empty_e4m3(x, (C, R))
+        scale_t = x.new_empty((C if block_rows == 1 else cb, rb), dtype=torch.float32)
     st = _lib.maxsim_quant_fp8(x.data_ptr(), ldx, R, C, code, block_rows,
                                None if q is None else q.data_ptr(), -(-C // 16) * 16,
                                None if scale is None else scale.data_ptr(),
@@ -859,6 +875,8 @@ def maxsim_quant_fp8(x, block_rows=1, rows=True, transposed=False):
 def _operand(t, name, dev):
     """The pitch of an e4m3 operand [rows, K]; every row is readable up to K rounded up to 16."""
     rows, K = t.shape
+    if K % 16 == 0 and t.is_contiguous() and t.dtype is torch.float8_e4m3fn and t.device == dev:
+        return K
     ld = _rows(t, name, t.shape, torch.float8_e4m3fn, dev)
     k16 = -(-K // 16) * 16
     if ld < k16 and rows <= 1:
@@ -886,16 +904,19 @@ def maxsim_gemm_fp8(A, a_scale, B, b_scale, out_dtype=torch.bfloat16, out=None, 
     _flat(a_scale, "a_scale", M * kb, torch.float32, dev)
     block_rows = 1 if b_scale.shape[0] == N else QBLOCK
     _flat(b_scale, "b_scale", -(-N // block_rows) * kb, torch.float32, dev)
+    ldc = N
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-    code = _code(out.dtype, _FLOATS, "out_dtype")
-    ldc = _rows(out, "out", (M, N), out.dtype, dev)
+        code = _code(out_dtype, _FLOATS, "out_dtype")
+        out = a_scale.new_empty((M, N), dtype=out_dtype)
+    else:
+        code = _code(out.dtype, _FLOATS, "out")
+        ldc = _rows(out, "out", (M, N), out.dtype, dev)
     nbytes = _lib.maxsim_gemm_fp8_workspace_bytes(M, N, K)
     if workspace is not None:
         _need(workspace, "workspace", device=dev)
         nbytes = workspace.numel() * workspace.element_size()
     elif nbytes:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        workspace = a_scale.new_empty(nbytes, dtype=torch.uint8)
     st = _lib.maxsim_gemm_fp8(A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(), ldb, b_scale.data_ptr(), block_rows,
                               M, N, K, code, out.data_ptr(), ldc, None if workspace is None else workspace.data_ptr(),
                               nbytes, _raw_stream(dev))
