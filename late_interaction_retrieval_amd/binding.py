@@ -108,6 +108,7 @@ def lib():
 
 
 lib()  # fail loudly at import time if the native library is missing
+from . import _fast  # noqa: E402  the usual calls of the embedding head's operators, natively (fast_binding.cpp)
 
 
 def _ptr(t):
@@ -743,15 +744,23 @@ def _gain(weight, H, dtype, dev):
     return weight.data_ptr(), _CODES[weight.dtype]
 
 
-@_on_its_device
 def maxsim_rmsnorm_fwd(x, weight=None, eps=1e-6, residual=None, out_dtype=None, with_rstd=False, y=None, scale=None,
-                       sum=None, rstd=None):
+                       sum=None, rstd=None, stream=None):
     """RMS norm of the rows of x [..., H] (fp16, bf16, fp32), of x + residual where one is given.
 
     out_dtype: x's (the default), float16, bfloat16, float32, int8 (a scale for each row: the operand of
     maxsim_fwd_i8) or float8_e4m3fn (a scale for each 128 columns: the operand of maxsim_gemm_fp8).
     Returns (y, scale or None, sum or None, rstd or None); sum = x + residual in x's type, rstd [...] fp32.
     """
+    if y is None and scale is None and sum is None and rstd is None and stream is None:
+        got = _fast.rmsnorm_fwd(x, weight, eps, residual, out_dtype, with_rstd)
+        if got is not None:
+            return got
+    return _rmsnorm_fwd(x, weight, eps, residual, out_dtype, with_rstd, y, scale, sum, rstd, stream=stream)
+
+
+@_on_its_device
+def _rmsnorm_fwd(x, weight, eps, residual, out_dtype, with_rstd, y, scale, sum, rstd):
     dev, shape, dtype = x.device, x.shape, x.dtype
     H, R = shape[-1], _row_count(shape)
     code = _code(dtype, _FLOATS, "x")
@@ -802,11 +811,20 @@ def maxsim_rmsnorm_bwd_workspace_bytes(R, H):
     return int(lib().maxsim_rmsnorm_bwd_workspace_bytes(R, H))
 
 
-@_on_its_device
-def maxsim_rmsnorm_bwd(dy, h, rstd, weight=None, dsum=None, with_dweight=True, dx=None, dweight=None, workspace=None):
+def maxsim_rmsnorm_bwd(dy, h, rstd, weight=None, dsum=None, with_dweight=True, dx=None, dweight=None, workspace=None,
+                       stream=None):
     """Backward of the norm.  dy [..., H] is the gradient of y, h the forward's sum (x without a residual), rstd its
     rstd, dsum the gradient that arrives at sum itself.  Returns (dx, dweight [H] fp32 or None); dx is the gradient
     of x and of residual alike."""
+    if dx is None and dweight is None and workspace is None and stream is None:
+        got = _fast.rmsnorm_bwd(dy, h, rstd, weight, dsum, with_dweight)
+        if got is not None:
+            return got
+    return _rmsnorm_bwd(dy, h, rstd, weight, dsum, with_dweight, dx, dweight, workspace, stream=stream)
+
+
+@_on_its_device
+def _rmsnorm_bwd(dy, h, rstd, weight, dsum, with_dweight, dx, dweight, workspace):
     dev, shape, dtype = h.device, h.shape, h.dtype
     H, R = shape[-1], _row_count(shape)
     code = _code(dtype, _FLOATS, "h")
@@ -841,11 +859,19 @@ def maxsim_rmsnorm_bwd(dy, h, rstd, weight=None, dsum=None, with_dweight=True, d
     return dx, dweight
 
 
-@_on_its_device
-def maxsim_quant_fp8(x, block_rows=1, rows=True, transposed=False):
+def maxsim_quant_fp8(x, block_rows=1, rows=True, transposed=False, stream=None):
     """x [R, C] (fp16, bf16, fp32) in e4m3 with a scale for each 128 columns of a row (block_rows 1) or each
     128 x 128 values (block_rows 128), for maxsim_gemm_fp8.  Returns (q [R, C], scale, qt [C, R], scale_t): qt is x
     transposed, with a scale for each 128 of x's rows; rows / transposed say which of the two are made (else None)."""
+    if stream is None:
+        got = _fast.quant_fp8(x, block_rows, rows, transposed)
+        if got is not None:
+            return got
+    return _quant_fp8(x, block_rows, rows, transposed, stream=stream)
+
+
+@_on_its_device
+def _quant_fp8(x, block_rows, rows, transposed):
     if x.dim() != 2:
         raise ValueError("x must be [R, C]")
     dev = x.device
@@ -890,10 +916,18 @@ def maxsim_gemm_fp8_workspace_bytes(M, N, K):
     return int(lib().maxsim_gemm_fp8_workspace_bytes(M, N, K))
 
 
-@_on_its_device
-def maxsim_gemm_fp8(A, a_scale, B, b_scale, out_dtype=torch.bfloat16, out=None, workspace=None):
+def maxsim_gemm_fp8(A, a_scale, B, b_scale, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None):
     """A B^T of e4m3 A [M, K] and B [N, K] with a_scale [M, ceil(K/128)] and b_scale [N, ceil(K/128)] or
     [ceil(N/128), ceil(K/128)] (a scale for 128 rows of B); fp32 sums, rounded once to out_dtype."""
+    if out is None and workspace is None and stream is None:
+        got = _fast.gemm_fp8(A, a_scale, B, b_scale, out_dtype)
+        if got is not None:
+            return got
+    return _gemm_fp8(A, a_scale, B, b_scale, out_dtype, out, workspace, stream=stream)
+
+
+@_on_its_device
+def _gemm_fp8(A, a_scale, B, b_scale, out_dtype, out, workspace):
     dev = A.device
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
         raise ValueError("A [M, K] and B [N, K] must share K")
@@ -970,6 +1004,7 @@ class AdamWTensors:
         if masters is not None:
             put("master", self.masters, torch.float32)
         self._table = table
+        self._address = table.ctypes.data
 
     @classmethod
     def zeros(cls, params, state_dtype=torch.float32, masters=True):
@@ -984,11 +1019,20 @@ class AdamWTensors:
                    scales() if eight else None, held)
 
 
-@_on_its_device
-def maxsim_adamw(tensors, grads, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, step_dev=None):
+def maxsim_adamw(tensors, grads, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, step_dev=None,
+                 stream=None):
     """One AdamW step of an AdamWTensors with these gradients (one tensor a parameter, all fp16, bf16 or fp32), in
     place.  step: the number of this step, from 1 on; or step_dev, a device int32 that holds it, for a step that is
     captured and replayed."""
+    if step_dev is None and stream is None:
+        if _fast.adamw(tensors._address, len(tensors.sizes), tensors.device.index, tensors.param_code,
+                       tensors.state_code, grads, lr, beta1, beta2, eps, weight_decay, step):
+            return
+    _adamw(tensors, grads, step, lr, beta1, beta2, eps, weight_decay, step_dev, stream=stream)
+
+
+@_on_its_device
+def _adamw(tensors, grads, step, lr, beta1, beta2, eps, weight_decay, step_dev):
     dev = tensors.device
     if len(grads) != len(tensors.sizes):
         raise ValueError("%d gradients for %d parameters" % (len(grads), len(tensors.sizes)))

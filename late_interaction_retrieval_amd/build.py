@@ -1,4 +1,5 @@
-"""Compile libmaxsim.so (HIP kernels + C ABI) for gfx950 with hipcc, in-tree.
+"""Compile libmaxsim.so (HIP kernels + C ABI) for gfx950 with hipcc, and the binding's Python extension
+_fast.so with the host compiler, in-tree.
 
 Usage: python -m late_interaction_retrieval_amd.build
 """
@@ -6,12 +7,14 @@ from concurrent.futures import ThreadPoolExecutor
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmaxsim.so")
+FAST = os.path.join(HERE, "_fast.so")
 SOURCES = ["fwd.hip", "bwd.hip", "topk.hip", "ooc.hip", "chamfer.hip", "noalloc.hip", "capi.cpp",
            "rmsnorm.hip", "quant.hip", "gemm_fp8.hip", "adamw.hip", "capi_encoder.cpp"]
 
@@ -66,9 +69,28 @@ def _compile(sources, lib, verbose, extra):
     return lib
 
 
+def _compile_fast(verbose):
+    """The extension: torch's C++ tensors, and libmaxsim.so beside it."""
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
+    tmp = FAST + ".tmp%d" % os.getpid()
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1",
+          "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), "-w",
+          "-I", os.path.join(ROOT, "include"), "-I", os.path.join(base, "include"),
+          "-I", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+          "-I", sysconfig.get_paths()["include"], "-I", os.path.join(rocm, "include"),
+          os.path.join(CSRC, "fast_binding.cpp"), "-o", tmp, "-L", HERE, "-lmaxsim", "-Wl,-rpath,$ORIGIN",
+          "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip"], verbose)
+    os.replace(tmp, FAST)
+
+
 def build(verbose=False, extra=()):
-    """Build libmaxsim.so."""
-    return _compile(SOURCES, LIB, verbose, extra)
+    """Build libmaxsim.so and _fast.so."""
+    _compile(SOURCES, LIB, verbose, extra)
+    _compile_fast(verbose)
+    return LIB
 
 
 if __name__ == "__main__":

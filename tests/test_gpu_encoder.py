@@ -231,3 +231,53 @@ def test_two_streams_at_once(bd):
     streams[0].synchronize()
     q2, s2, _, _ = bd.maxsim_rmsnorm_fwd(ins[0][0], gain, out_dtype=torch.float8_e4m3fn)
     assert torch.equal(c, bd.maxsim_gemm_fp8(q2, s2, wq, ws))
+
+
+@pytest.mark.parametrize("H", [256, 129])
+def test_both_ways_through_the_binding(bd, H):
+    """The usual calls go through the extension, all others through ctypes: the same results, and the extension leaves
+    alone what it does not handle."""
+    here = torch.cuda.current_stream()
+    same = lambda a, b: all((x is None and y is None) or (x.shape == y.shape and x.dtype == y.dtype  # noqa: E731
+                                                          and torch.equal(x.float(), y.float())) for x, y in zip(a, b))
+    x, r, w = randn(1, 5, 7, H), randn(2, 5, 7, H), randn(3, H)
+    for dt in (torch.float32, torch.bfloat16, torch.float16):
+        for out in (None, torch.float32, torch.int8, torch.float8_e4m3fn):
+            for res in (None, r.to(dt)):
+                a = bd.maxsim_rmsnorm_fwd(x.to(dt), w, residual=res, out_dtype=out, with_rstd=True)
+                b = bd.maxsim_rmsnorm_fwd(x.to(dt), w, residual=res, out_dtype=out, with_rstd=True, stream=here)
+                assert same(a, b)
+        h, rstd = x.to(dt), b[3]
+        for dsum in (None, r.to(dt)):
+            for with_dweight in (True, False):
+                assert same(bd.maxsim_rmsnorm_bwd(r.to(dt), h, rstd, w, dsum, with_dweight),
+                            bd.maxsim_rmsnorm_bwd(r.to(dt), h, rstd, w, dsum, with_dweight, stream=here))
+        m = randn(4, 160, H, dtype=dt)
+        for br in (1, 128):
+            for rows, both in ((True, False), (True, True), (False, True)):
+                assert same(bd.maxsim_quant_fp8(m, br, rows, both), bd.maxsim_quant_fp8(m, br, rows, both, stream=here))
+    q, s, _, _ = bd.maxsim_quant_fp8(randn(4, 160, H))
+    b, bs, _, _ = bd.maxsim_quant_fp8(randn(5, 100, H), 128)
+    for dt in (torch.float32, torch.bfloat16, torch.float16):
+        assert same([bd.maxsim_gemm_fp8(q, s, b, bs, dt)], [bd.maxsim_gemm_fp8(q, s, b, bs, dt, stream=here)])
+        assert same([bd.maxsim_gemm_fp8(q, s, q, s, dt)], [bd.maxsim_gemm_fp8(q, s, q, s, dt, stream=here)])
+    tabs = [bd.AdamWTensors.zeros([randn(6, 70), randn(7, 300)], torch.float8_e4m3fn) for _ in range(2)]
+    g = [randn(8, 70), randn(9, 300)]
+    before = tabs[0]._table.copy()
+    bd.maxsim_adamw(tabs[0], g, 1)
+    bd.maxsim_adamw(tabs[1], g, 1, stream=here)
+    assert (tabs[0]._table == before).all()
+    for f in ("params", "m", "v", "m_scales", "v_scales"):
+        assert same(getattr(tabs[0], f), getattr(tabs[1], f)), f
+    # not for the extension: None, and no launch
+    t = randn(1, 6, H)
+    assert bd._fast.rmsnorm_fwd(t[:, ::2], None, 1e-6, None, None, False) is None
+    assert bd._fast.rmsnorm_fwd(t.cpu(), None, 1e-6, None, None, False) is None
+    assert bd._fast.rmsnorm_fwd(t, t, 1e-6, None, None, False) is None
+    assert bd._fast.rmsnorm_fwd("x", None, 1e-6, None, None, False) is None
+    assert bd._fast.rmsnorm_fwd(t) is None
+    assert bd._fast.quant_fp8(t, 64, True, False) is None and bd._fast.quant_fp8(t.double(), 1, True, False) is None
+    assert bd._fast.gemm_fp8(q, s, b, bs[:0], torch.float32) is None
+    assert bd._fast.gemm_fp8(q, s, b, bs, torch.int8) is None
+    assert bd._fast.rmsnorm_bwd(t, t, t, None, None, True) is None
+    assert bd._fast.adamw(tabs[0]._address, 2, 0, 2, 4, g[:1], 1e-3, .9, .99, 1e-8, 0., 1) is None
