@@ -71,7 +71,7 @@ int maxsim_rmsnorm_fwd(const void* x, int64_t ldx, const void* residual, int64_t
                        int32_t weight_dtype, int32_t R, int32_t H, int32_t dtype, float eps, int32_t out_dtype,
                        void* y, int64_t ldy, float* scale, void* sum, int64_t lds, float* rstd, void* stream);
 
-/* Bytes of device workspace maxsim_rmsnorm_bwd needs (0 on bad sizes). */
+/* Bytes of device workspace maxsim_rmsnorm_bwd needs for dweight (0 for few rows, and on bad sizes). */
 size_t maxsim_rmsnorm_bwd_workspace_bytes(int32_t R, int32_t H);
 
 /*
@@ -85,7 +85,7 @@ size_t maxsim_rmsnorm_bwd_workspace_bytes(int32_t R, int32_t H);
  *             the memory of dy, h or dsum
  *   dweight   [H] fp32 out, or NULL; rows are added in a fixed order
  *   workspace of maxsim_rmsnorm_bwd_workspace_bytes() bytes, 16-byte aligned
- *             (NULL is fine without dweight).
+ *             (NULL is fine without dweight, or when that is 0).
  * Requires R >= 0 (dweight is 0 for R = 0), 1 <= H <= 32768.
  */
 int maxsim_rmsnorm_bwd(const void* dy, int64_t lddy, const void* h, int64_t ldh, const float* rstd,

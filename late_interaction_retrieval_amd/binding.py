@@ -845,8 +845,8 @@ def _rmsnorm_bwd(dy, h, rstd, weight, dsum, with_dweight, dx, dweight, workspace
         _flat(dweight, "dweight", H, torch.float32, dev)
     if dweight is not None:
         if workspace is None:
-            nbytes = max(16, _lib.maxsim_rmsnorm_bwd_workspace_bytes(R, H))
-            workspace = h.new_empty(nbytes, dtype=torch.uint8)
+            nbytes = _lib.maxsim_rmsnorm_bwd_workspace_bytes(R, H)
+            workspace = h.new_empty(nbytes, dtype=torch.uint8) if nbytes else None
         else:
             _need(workspace, "workspace", device=dev)
             nbytes = workspace.numel() * workspace.element_size()

@@ -60,7 +60,7 @@ int maxsim_rmsnorm_fwd(const void* x, int64_t ldx, const void* residual, int64_t
 }
 
 size_t maxsim_rmsnorm_bwd_workspace_bytes(int32_t R, int32_t H) {
-    if (R < 0 || H < 1 || H > maxsim::kMaxNormWidth) return 0;
+    if (R < 0 || H < 1 || H > maxsim::kMaxNormWidth || maxsim::norm_bwd_small(R, H)) return 0;
     return (size_t)maxsim::norm_bwd_groups(R, H) * (size_t)H * sizeof(float);
 }
 
@@ -74,12 +74,13 @@ int maxsim_rmsnorm_bwd(const void* dy, int64_t lddy, const void* h, int64_t ldh,
     if (!pitch_ok(lddy, H) || !pitch_ok(ldh, H) || !pitch_ok(lddx, H) || (dsum && !pitch_ok(ldds, H)))
         return MAXSIM_ERR_SHAPE;
     if (R == 0 && !dweight) return MAXSIM_OK;
-    if (R > 0 && (!dy || !h || !rstd || !dx || (dweight && !workspace))) return MAXSIM_ERR_NULL;
+    const size_t need = dweight ? maxsim_rmsnorm_bwd_workspace_bytes(R, H) : 0;
+    if (R > 0 && (!dy || !h || !rstd || !dx || (need > 0 && !workspace))) return MAXSIM_ERR_NULL;
     const uintptr_t e = elem(dtype);
     if (!aligned(dy, e) || !aligned(h, e) || !aligned(dsum, e) || !aligned(dx, e) || !aligned(rstd, 4) ||
         !aligned(weight, elem(weight_dtype)) || !aligned(dweight, 4) || !aligned(workspace, 16))
         return MAXSIM_ERR_ALIGN;
-    if (dweight && workspace_bytes < maxsim_rmsnorm_bwd_workspace_bytes(R, H)) return MAXSIM_ERR_WORKSPACE;
+    if (workspace_bytes < need) return MAXSIM_ERR_WORKSPACE;
     maxsim::NormBwdArgs a{};
     a.dy = dy;
     a.h = h;

@@ -44,6 +44,7 @@ struct NormBwdArgs {
     int R, H;
     int dtype, weight_f32;
 };
+bool norm_bwd_small(int R, int H);  // one launch and no partial sums
 int norm_bwd_groups(int R, int H);  // workgroups of the row pass = partial sums of dweight
 hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, hipStream_t stream);
 

@@ -137,13 +137,13 @@ PyObject* rmsnorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     size_t bytes = 0;
     if (dw_wanted) {
         dw = empty({H}, *h, at::kFloat);
-        bytes = std::max<size_t>(16, maxsim_rmsnorm_bwd_workspace_bytes((int32_t)R, (int32_t)H));
-        ws = empty({(int64_t)bytes}, *h, at::kByte);
+        bytes = maxsim_rmsnorm_bwd_workspace_bytes((int32_t)R, (int32_t)H);
+        if (bytes) ws = empty({(int64_t)bytes}, *h, at::kByte);
     }
     if (maxsim_rmsnorm_bwd(dy->data_ptr(), H, h->data_ptr(), H, rstd->data_ptr<float>(), at_(w),
                            w ? code_of(w->scalar_type()) : MAXSIM_F32, at_(ds), H, (int32_t)R, (int32_t)H, code,
                            dx.data_ptr(), H, dw_wanted ? dw.data_ptr<float>() : nullptr,
-                           dw_wanted ? ws.data_ptr() : nullptr, bytes, stream_of(*h)) != MAXSIM_OK)
+                           bytes ? ws.data_ptr() : nullptr, bytes, stream_of(*h)) != MAXSIM_OK)
         Py_RETURN_NONE;
     return tuple({dx, dw});
     END_HANDLE_TH_ERRORS

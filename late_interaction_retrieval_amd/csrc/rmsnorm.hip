@@ -269,6 +269,81 @@ __global__ __launch_bounds__(kReduceCols * kReduceRuns) void rmsnorm_dweight_ker
     }
 }
 
+// Few values: dx and dweight in one launch.  dweight does not need the rows'
+// means, so workgroups past those of the rows take 32 columns each over all
+// rows (read a second time, from L2) and no partial sums go to memory.
+constexpr int kSmallThreads = 1024;
+template <typename TT, int TPR, int NV>
+__global__ __launch_bounds__(kSmallThreads) void rmsnorm_bwd_small_kernel(NormBwdArgs p, int row_groups) {
+    typedef typename TT::type T;
+    constexpr int PER = kSmallThreads / TPR;
+    __shared__ float run[kReduceRuns][kReduceCols];
+    if ((int)blockIdx.x >= row_groups) {
+        const int col = threadIdx.x % kReduceCols, part = threadIdx.x / kReduceCols;
+        const int c = ((int)blockIdx.x - row_groups) * kReduceCols + col;
+        float s = 0.f;
+        if (c < p.H) {
+#pragma unroll 8
+            for (int r = part; r < p.R; r += kReduceRuns)
+                s += (float)((const T*)p.dy)[r * p.lddy + c] * ((float)((const T*)p.h)[r * p.ldh + c] * p.rstd[r]);
+        }
+        run[part][col] = s;
+        __syncthreads();
+        if (part == 0 && c < p.H) {
+#pragma unroll
+            for (int q = 1; q < kReduceRuns; ++q) s += run[q][col];
+            p.dweight[c] = s;
+        }
+        return;
+    }
+    const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const int64_t row = (int64_t)blockIdx.x * PER + sub;
+    const bool on = row < p.R;
+    typename Pack8<T>::V dy[NV], h[NV];
+    float w[NV][kVec];
+    float c = 0.f, r = 0.f;
+    if (on) {
+        r = p.rstd[row];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            dy[v] = load8<T>((const T*)p.dy + row * p.lddy, (v * TPR + lane) * kVec, p.H);
+            h[v] = load8<T>((const T*)p.h + row * p.ldh, (v * TPR + lane) * kVec, p.H);
+            load_gain<T>(p.weight, p.weight_f32, (v * TPR + lane) * kVec, p.H, w[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) c = __builtin_fmaf((float)dy[v][i] * ((float)h[v][i] * r), w[v][i], c);
+    }
+    if constexpr (TPR == 16) {
+        c = sum16(c);
+    } else {
+        c = sum64(c);
+        if constexpr (TPR > 64) {  // the row's waves, in order
+            constexpr int W = TPR / 64;
+            if ((threadIdx.x & 63) == 0) run[0][threadIdx.x >> 6] = c;
+            __syncthreads();
+            c = run[0][sub * W];
+#pragma unroll
+            for (int q = 1; q < W; ++q) c += run[0][sub * W + q];
+        }
+    }
+    if (!on) return;
+    c *= 1.f / (float)p.H;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        float dx[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) dx[i] = r * ((float)dy[v][i] * w[v][i] - (float)h[v][i] * r * c);
+        if (p.dsum != nullptr) {
+            const auto ds = load8<T>((const T*)p.dsum + row * p.ldds, (v * TPR + lane) * kVec, p.H);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) dx[i] += (float)ds[i];
+        }
+        store8<T>((T*)p.dx + row * p.lddx, (v * TPR + lane) * kVec, p.H, dx);
+    }
+}
+
 // Threads to a row: few enough that a lane has a full vector, and as many as a
 // row's columns ask for.
 template <typename F>
@@ -303,6 +378,10 @@ hipError_t launch_rmsnorm_fwd(const NormArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Us in one launch and in two: 1 x 128 3.3, 5.4; 1003 x 769 7.9, 9.9; 200 x 2048
+// 4.1, 7.9; 64 x 8192 6.3, 8.7; but 3000 x 128 11.7, 7.0; 1000 x 2048 10.9, 9.8.
+bool norm_bwd_small(int R, int H) { return R <= 512 || (R <= 1024 && H <= 1024); }
+
 int norm_bwd_groups(int R, int H) {
     const int per = H <= 128 ? 16 : H <= 1024 ? 4 : 1;
     const int64_t rows = ceil_div(R, per);
@@ -311,6 +390,24 @@ int norm_bwd_groups(int R, int H) {
 }
 
 hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, hipStream_t stream) {
+    if (a.dweight != nullptr && a.R > 0 && norm_bwd_small(a.R, a.H)) {
+        by_type(a.dtype, [&](auto t) {
+            by_width(a.H, [&](auto tpr, auto nv) {
+                constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
+                const int rows = (int)ceil_div(a.R, kSmallThreads / TPR), cols = (int)ceil_div(a.H, kReduceCols);
+                auto go = [&](int grid, int row_groups) {
+                    rmsnorm_bwd_small_kernel<decltype(t), TPR, NV><<<grid, kSmallThreads, 0, stream>>>(a, row_groups);
+                };
+                if (a.dx == a.dy || a.dx == a.h) {  // in place: the columns read what the rows overwrite
+                    go(cols, 0);
+                    go(rows, rows);
+                } else {
+                    go(rows + cols, rows);
+                }
+            });
+        });
+        return hipGetLastError();
+    }
     const int groups = norm_bwd_groups(a.R, a.H);
     if (groups > 0) {
         by_type(a.dtype, [&](auto t) {

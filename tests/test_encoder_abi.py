@@ -69,9 +69,9 @@ def norm_bwd(**kw):
 @pytest.mark.parametrize("want,kw", [
     (SHAPE, dict(R=-1)), (SHAPE, dict(H=0)), (SHAPE, dict(lddy=1)), (SHAPE, dict(ldh=1)), (SHAPE, dict(lddx=1)),
     (SHAPE, dict(ldds=1)), (UNSUPPORTED, dict(dt=E4M3)), (UNSUPPORTED, dict(wdt=BF16)),
-    (NULL, dict(dy=None)), (NULL, dict(h=None)), (NULL, dict(rstd=None)), (NULL, dict(dx=None)), (NULL, dict(ws=None)),
-    (ALIGN, dict(dy=M)), (ALIGN, dict(h=M)), (ALIGN, dict(ds=M)), (ALIGN, dict(dx=M)), (ALIGN, dict(dw=M)),
-    (ALIGN, dict(ws=M)), (WORKSPACE, dict(nbytes=64)), (OK, dict(R=0, dw=None)),
+    (NULL, dict(dy=None)), (NULL, dict(h=None)), (NULL, dict(rstd=None)), (NULL, dict(dx=None)),
+    (NULL, dict(R=5000, ws=None)), (ALIGN, dict(dy=M)), (ALIGN, dict(h=M)), (ALIGN, dict(ds=M)), (ALIGN, dict(dx=M)), (ALIGN, dict(dw=M)),
+    (ALIGN, dict(ws=M)), (WORKSPACE, dict(R=5000, nbytes=64)), (OK, dict(R=0, dw=None)),
 ], ids=str)
 def test_rmsnorm_bwd_refusals(want, kw):
     assert norm_bwd(**kw) == want

@@ -153,11 +153,16 @@ def test_in_place(bd):
     x2, res2 = x.clone(), res.clone()
     bd.maxsim_rmsnorm_fwd(x2, residual=res2, y=x2, sum=res2)
     assert torch.equal(x2, y) and torch.equal(res2, h)
-    dy = rows(3, R, H, torch.bfloat16).to(DEV)
-    dx, dw = bd.maxsim_rmsnorm_bwd(dy, h, r)
-    dy2 = dy.clone()
-    _, dw2 = bd.maxsim_rmsnorm_bwd(dy2, h, r, dx=dy2)
-    assert torch.equal(dy2, dx) and torch.equal(dw2, dw)
+    # few rows (one launch, or two in place) and many
+    for R, H in ((50, 700), (1000, 1000), (512, 8000), (3000, 300)):
+        h, dy = rows(2, R, H, torch.bfloat16).to(DEV), rows(3, R, H, torch.bfloat16).to(DEV)
+        ds = rows(4, R, H, torch.bfloat16).to(DEV)
+        _, _, _, r = bd.maxsim_rmsnorm_fwd(h, with_rstd=True)
+        dx, dw = bd.maxsim_rmsnorm_bwd(dy, h, r, dsum=ds)
+        for over in range(3):
+            ins = [dy.clone(), h.clone(), ds.clone()]
+            dx2, dw2 = bd.maxsim_rmsnorm_bwd(ins[0], ins[1], r, dsum=ins[2], dx=ins[over])
+            assert dx2 is ins[over] and torch.equal(dx2, dx) and torch.equal(dw2, dw), (R, H, over)
 
 
 def test_zero_rows_and_extremes(bd):
@@ -239,7 +244,9 @@ def test_binding_refusals(bd):
         bd.maxsim_rmsnorm_fwd(x, scale=torch.ones(4, device=DEV))
     with pytest.raises(bd.MaxSimError):
         bd.maxsim_rmsnorm_fwd(torch.zeros(1, 32769, device=DEV))
+    many = torch.zeros(5000, 128, device=DEV)
     with pytest.raises(bd.MaxSimError):
-        bd.maxsim_rmsnorm_bwd(x, x, torch.ones(4, device=DEV), workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+        bd.maxsim_rmsnorm_bwd(many, many, many[:, 0].contiguous(),
+                              workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError):
         bd.maxsim_rmsnorm_bwd(x, x, torch.ones(3, device=DEV))
