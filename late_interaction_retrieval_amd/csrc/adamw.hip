@@ -6,7 +6,7 @@
 //
 // HBM-bound: every value is read and written once (28 bytes with fp32 weights,
 // gradients and states).  The tensors' table travels in the kernel's arguments,
-// 40 to a launch, so there is nothing to copy or keep on the device and a
+// 56 to a launch, so there is nothing to copy or keep on the device and a
 // captured launch holds its own table.  Workgroups of 2048 values are dealt to the
 // tensors in order; each finds its tensor by a search over the first workgroups.
 //
@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kChunk = kThreads * kVec;  // values of one workgroup
-constexpr int kTensors = 40;             // entries of one launch's table
+constexpr int kTensors = 56;             // entries of one launch's table
 
 struct Table {
     maxsim_adamw_tensor t[kTensors];

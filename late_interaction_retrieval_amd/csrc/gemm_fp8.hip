@@ -453,6 +453,7 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs p, int splits) 
     const f32x4* part = reinterpret_cast<const f32x4*>(p.partial);
     for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < each; k += (int64_t)gridDim.x * 256) {
         f32x4 v = part[k];
+#pragma unroll 8
         for (int z = 1; z < splits; ++z) v += part[z * each + k];
         const int64_t row = k / n4;
         store4(p, row, (int)(k - row * n4) * 4, v);

@@ -19,26 +19,28 @@ namespace maxsim {
 namespace {
 
 // TPR threads hold a row, NV vectors of 8 columns each: column
-// (v * TPR + lane) * 8.  Rows of up to 64 threads share a 256-thread workgroup.
+// (v * TPR + lane) * 8.  Rows of 16 or 64 threads share a workgroup of 256;
+// wider rows (TPR 0 here) have one of as many waves as their columns ask for.
+constexpr int kWide = 0;
+constexpr int kMostWaves = 8;  // of a row: leaves a thread 256 registers
 template <int TPR>
 struct Rows {
-    static constexpr int threads = TPR < 256 ? 256 : TPR;
-    static constexpr int per_group = threads / TPR;
-    static constexpr int waves = TPR / 64;  // of one row, when it is a whole workgroup
+    static constexpr int threads = TPR == kWide ? 64 * kMostWaves : 256;
+    static constexpr int per_group = TPR == kWide ? 1 : 256 / TPR;
+    __device__ static __forceinline__ int wide() { return TPR == kWide ? (int)blockDim.x : TPR; }
 };
 
-// Sum (or maximum) over a row's threads, the same in each of them.  Waves meet
-// in `part` (one word per wave), which each call uses anew.
+// Sum (or maximum) over a row's threads, the same in each of them.  The waves of
+// a wide row meet in `part` (one word each), which each call uses anew.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* part) {
     if constexpr (TPR == 16) return sum16(v);
     v = sum64(v);
-    if constexpr (TPR > 64) {
+    if constexpr (TPR == kWide) {
         if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
         __syncthreads();
         v = part[0];
-#pragma unroll
-        for (int w = 1; w < Rows<TPR>::waves; ++w) v += part[w];
+        for (int w = 1; w < (int)blockDim.x >> 6; ++w) v += part[w];
     }
     return v;
 }
@@ -46,12 +48,11 @@ template <int TPR>
 __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* part) {
     if constexpr (TPR == 16) return max16(v);
     v = max64(v);
-    if constexpr (TPR > 64) {
+    if constexpr (TPR == kWide) {
         if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
         __syncthreads();
         v = part[0];
-#pragma unroll
-        for (int w = 1; w < Rows<TPR>::waves; ++w) v = umax(v, part[w]);
+        for (int w = 1; w < (int)blockDim.x >> 6; ++w) v = umax(v, part[w]);
     }
     return v;
 }
@@ -63,11 +64,13 @@ __device__ __forceinline__ void load_gain(const void* weight, int f32, int c, in
 #pragma unroll
         for (int i = 0; i < kVec; ++i) w[i] = 1.f;
     } else if (f32) {
-        const auto v = load8<float>((const float*)weight, c, n);
+        auto v = near8<float>((const float*)weight, c, n);
+        fit8<float>(v, c, n);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) w[i] = v[i];
     } else {
-        const auto v = load8<T>((const T*)weight, c, n);
+        auto v = near8<T>((const T*)weight, c, n);
+        fit8<T>(v, c, n);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) w[i] = (float)v[i];
     }
@@ -77,28 +80,38 @@ template <typename TT, int TPR, int NV>
 __global__ __launch_bounds__(Rows<TPR>::threads) void rmsnorm_fwd_kernel(NormArgs p) {
     typedef typename TT::type T;
     constexpr int PER = Rows<TPR>::per_group;
-    __shared__ float part_sum[2][TPR > 64 ? Rows<TPR>::waves : 1];
-    __shared__ uint32_t part_max[2][TPR > 64 ? Rows<TPR>::waves : 1];
-    const int lane = threadIdx.x % TPR;
+    constexpr bool TOGETHER = NV <= 2;
+    __shared__ float part_sum[2][kMostWaves];
+    __shared__ uint32_t part_max[2][kMostWaves];
+    const int tpr = Rows<TPR>::wide();
+    const int lane = TPR == kWide ? threadIdx.x : threadIdx.x % tpr;
     int turn = 0;  // two sets of words in LDS in turn: a wave may be a row ahead of another's read
     // a row that all its threads leave together: rows of up to 64 threads meet no barrier
-    for (int64_t row = (int64_t)blockIdx.x * PER + threadIdx.x / TPR; row < p.R;
+    for (int64_t row = (int64_t)blockIdx.x * PER + (TPR == kWide ? 0 : threadIdx.x / tpr); row < p.R;
          row += (int64_t)gridDim.x * PER, turn ^= 1) {
         const T* x = (const T*)p.x + row * p.ldx;
         float h[NV][kVec];
+        typename Pack8<T>::V in[NV];
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const auto a = load8<T>(x, (v * TPR + lane) * kVec, p.H);
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) h[v][i] = (float)a[i];
-        }
+        for (int v = 0; v < NV; ++v) in[v] = near8<T, TOGETHER>(x, (v * tpr + lane) * kVec, p.H);
         if (p.residual != nullptr) {
             const T* res = (const T*)p.residual + row * p.ldr;
+            typename Pack8<T>::V also[NV];
+#pragma unroll
+            for (int v = 0; v < NV; ++v) also[v] = near8<T, TOGETHER>(res, (v * tpr + lane) * kVec, p.H);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                const auto a = load8<T>(res, (v * TPR + lane) * kVec, p.H);
+                fit8<T, TOGETHER>(in[v], (v * tpr + lane) * kVec, p.H);
+                fit8<T, TOGETHER>(also[v], (v * tpr + lane) * kVec, p.H);
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) h[v][i] += (float)a[i];
+                for (int i = 0; i < kVec; ++i) h[v][i] = (float)in[v][i] + (float)also[v][i];
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                fit8<T, TOGETHER>(in[v], (v * tpr + lane) * kVec, p.H);
+#pragma unroll
+                for (int i = 0; i < kVec; ++i) h[v][i] = (float)in[v][i];
             }
         }
         float ss = 0.f;
@@ -109,7 +122,7 @@ __global__ __launch_bounds__(Rows<TPR>::threads) void rmsnorm_fwd_kernel(NormArg
         if (p.sum != nullptr) {
             T* sum = (T*)p.sum + row * p.lds;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) store8<T>(sum, (v * TPR + lane) * kVec, p.H, h[v]);
+            for (int v = 0; v < NV; ++v) store8<T>(sum, (v * tpr + lane) * kVec, p.H, h[v]);
         }
         ss = row_sum<TPR>(ss, part_sum[turn]);
         const float r = 1.f / __builtin_sqrtf(ss / (float)p.H + p.eps);
@@ -117,7 +130,7 @@ __global__ __launch_bounds__(Rows<TPR>::threads) void rmsnorm_fwd_kernel(NormArg
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             float w[kVec];
-            load_gain<T>(p.weight, p.weight_f32, (v * TPR + lane) * kVec, p.H, w);
+            load_gain<T>(p.weight, p.weight_f32, (v * tpr + lane) * kVec, p.H, w);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) h[v][i] = h[v][i] * r * w[i];
         }
@@ -130,7 +143,7 @@ __global__ __launch_bounds__(Rows<TPR>::threads) void rmsnorm_fwd_kernel(NormArg
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) top = umax(top, mag(h[v][i]));
                 const Scale k = block_scale(max16(top), 448.f);
-                const int c = (v * TPR + lane) * kVec;
+                const int c = (v * tpr + lane) * kVec;
                 if (c < p.H) {
                     store8_bytes(y, c, p.H, to_e4m3(h[v], k));
                     if (c % kQBlock == 0) p.scale[row * blocks + c / kQBlock] = k.s;
@@ -146,19 +159,19 @@ __global__ __launch_bounds__(Rows<TPR>::threads) void rmsnorm_fwd_kernel(NormArg
             if (lane == 0) p.scale[row] = k.s;
             uint8_t* y = (uint8_t*)p.y + row * p.ldy;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) store8_bytes(y, (v * TPR + lane) * kVec, p.H, to_i8(h[v], k));
+            for (int v = 0; v < NV; ++v) store8_bytes(y, (v * tpr + lane) * kVec, p.H, to_i8(h[v], k));
         } else if (p.out_dtype == MAXSIM_F32) {
             float* y = (float*)p.y + row * p.ldy;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) store8<float>(y, (v * TPR + lane) * kVec, p.H, h[v]);
+            for (int v = 0; v < NV; ++v) store8<float>(y, (v * tpr + lane) * kVec, p.H, h[v]);
         } else if (p.out_dtype == MAXSIM_BF16) {
             __bf16* y = (__bf16*)p.y + row * p.ldy;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) store8<__bf16>(y, (v * TPR + lane) * kVec, p.H, h[v]);
+            for (int v = 0; v < NV; ++v) store8<__bf16>(y, (v * tpr + lane) * kVec, p.H, h[v]);
         } else {
             _Float16* y = (_Float16*)p.y + row * p.ldy;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) store8<_Float16>(y, (v * TPR + lane) * kVec, p.H, h[v]);
+            for (int v = 0; v < NV; ++v) store8<_Float16>(y, (v * tpr + lane) * kVec, p.H, h[v]);
         }
     }
 }
@@ -170,14 +183,18 @@ template <typename TT, int TPR, int NV>
 __global__ __launch_bounds__(Rows<TPR>::threads) void rmsnorm_bwd_kernel(NormBwdArgs p) {
     typedef typename TT::type T;
     constexpr int PER = Rows<TPR>::per_group;
-    __shared__ float part[2][TPR > 64 ? Rows<TPR>::waves : 1];
-    __shared__ float share[PER > 1 ? PER : 1][PER > 1 ? TPR * kVec : 1];
-    const int lane = threadIdx.x % TPR;
-    const int sub = threadIdx.x / TPR;
-    float w[NV][kVec], dw[NV][kVec];
+    constexpr bool TOGETHER = NV <= 4;
+    __shared__ float part[2][kMostWaves];
+    __shared__ float share[PER][PER > 1 ? TPR * kVec : 1];
+    const int tpr = Rows<TPR>::wide();
+    const int lane = TPR == kWide ? threadIdx.x : threadIdx.x % tpr;
+    const int sub = TPR == kWide ? 0 : threadIdx.x / tpr;
+    // the gain stays in registers, or, where a row takes too many, comes from L2 for each row
+    constexpr bool KEEP = NV <= 4;
+    float w[KEEP ? NV : 1][kVec], dw[NV][kVec];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        load_gain<T>(p.weight, p.weight_f32, (v * TPR + lane) * kVec, p.H, w[v]);
+        if constexpr (KEEP) load_gain<T>(p.weight, p.weight_f32, (v * tpr + lane) * kVec, p.H, w[v]);
 #pragma unroll
         for (int i = 0; i < kVec; ++i) dw[v][i] = 0.f;
     }
@@ -189,47 +206,61 @@ __global__ __launch_bounds__(Rows<TPR>::threads) void rmsnorm_bwd_kernel(NormBwd
         typename Pack8<T>::V dy[NV], h[NV], ds[NV];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            dy[v] = load8<T>(dyr, (v * TPR + lane) * kVec, p.H);
-            h[v] = load8<T>(hr, (v * TPR + lane) * kVec, p.H);
+            dy[v] = near8<T, TOGETHER>(dyr, (v * tpr + lane) * kVec, p.H);
+            h[v] = near8<T, TOGETHER>(hr, (v * tpr + lane) * kVec, p.H);
         }
-        if (p.dsum != nullptr) {
+        if (NV < 8 && p.dsum != nullptr) {  // 8 vectors have no registers for it before dx
             const T* dsr = (const T*)p.dsum + row * p.ldds;
 #pragma unroll
-            for (int v = 0; v < NV; ++v) ds[v] = load8<T>(dsr, (v * TPR + lane) * kVec, p.H);
+            for (int v = 0; v < NV; ++v) ds[v] = near8<T, TOGETHER>(dsr, (v * tpr + lane) * kVec, p.H);
         }
         const float r = p.rstd[row];
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int at = (v * tpr + lane) * kVec;
+            fit8<T, TOGETHER>(dy[v], at, p.H);
+            fit8<T, TOGETHER>(h[v], at, p.H);
+            if (NV < 8 && p.dsum != nullptr) fit8<T, TOGETHER>(ds[v], at, p.H);
+        }
         float c = 0.f;
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
+        for (int v = 0; v < NV; ++v) {
+            if constexpr (!KEEP) load_gain<T>(p.weight, p.weight_f32, (v * tpr + lane) * kVec, p.H, w[0]);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
                 const float t = (float)dy[v][i] * ((float)h[v][i] * r);
                 dw[v][i] += t;
-                c = __builtin_fmaf(t, w[v][i], c);
+                c = __builtin_fmaf(t, w[KEEP ? v : 0][i], c);
             }
+        }
         // two words of LDS in turn: a wave may be a row ahead of another's read
         c = row_sum<TPR>(c, part[turn]) * inv_h;
         T* dxr = (T*)p.dx + row * p.lddx;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             float dx[kVec];
+            if constexpr (!KEEP) load_gain<T>(p.weight, p.weight_f32, (v * tpr + lane) * kVec, p.H, w[0]);
 #pragma unroll
             for (int i = 0; i < kVec; ++i) {
-                const float g = (float)dy[v][i] * w[v][i];
+                const float g = (float)dy[v][i] * w[KEEP ? v : 0][i];
                 dx[i] = r * (g - (float)h[v][i] * r * c);
             }
             if (p.dsum != nullptr) {
+                if constexpr (NV >= 8) {
+                    ds[v] = near8<T, TOGETHER>((const T*)p.dsum + row * p.ldds, (v * tpr + lane) * kVec, p.H);
+                    fit8<T, TOGETHER>(ds[v], (v * tpr + lane) * kVec, p.H);
+                }
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) dx[i] += (float)ds[v][i];
             }
-            store8<T>(dxr, (v * TPR + lane) * kVec, p.H, dx);
+            store8<T>(dxr, (v * tpr + lane) * kVec, p.H, dx);
         }
     }
     if (p.dweight == nullptr) return;
     float* out = p.partial + (int64_t)blockIdx.x * p.H;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-        const int c = (v * TPR + lane) * kVec;
+        const int c = (v * tpr + lane) * kVec;
         if constexpr (PER > 1) {  // the workgroup's rows, added in order
             if (v > 0) __syncthreads();
 #pragma unroll
@@ -344,10 +375,24 @@ __global__ __launch_bounds__(kSmallThreads) void rmsnorm_bwd_small_kernel(NormBw
     }
 }
 
-// Threads to a row: few enough that a lane has a full vector, and as many as a
-// row's columns ask for.
-template <typename F>
-void by_width(int H, F&& go) {
+// Threads to a row: 16 or 64 for narrow ones; else as many waves as its columns
+// fill with one vector a thread, two past 2560 columns, and so on.  Go is
+// called with (threads to a row or kWide, vectors a thread, threads of a workgroup).
+template <typename Go>
+void by_width(int H, Go&& go) {
+    typedef std::integral_constant<int, kWide> wide;
+    const auto waves = [&](int nv) { return 64 * (int)ceil_div(H, 64 * kVec * nv); };
+    if (H <= 128) return go(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{}, 256);
+    if (H <= 512) return go(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{}, 256);
+    if (H <= 1024) return go(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{}, 256);
+    if (H <= 2560) return go(wide{}, std::integral_constant<int, 1>{}, waves(1));
+    if (H <= 8192) return go(wide{}, std::integral_constant<int, 2>{}, waves(2));
+    if (H <= 16384) return go(wide{}, std::integral_constant<int, 4>{}, waves(4));
+    return go(wide{}, std::integral_constant<int, 8>{}, waves(8));
+}
+// The one-launch backward has 1024 threads whatever the width.
+template <typename Go>
+void by_width_small(int H, Go&& go) {
     if (H <= 128) return go(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
     if (H <= 512) return go(std::integral_constant<int, 64>{}, std::integral_constant<int, 1>{});
     if (H <= 1024) return go(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
@@ -368,11 +413,11 @@ void by_type(int dtype, F&& go) {
 
 hipError_t launch_rmsnorm_fwd(const NormArgs& a, hipStream_t stream) {
     by_type(a.dtype, [&](auto t) {
-        by_width(a.H, [&](auto tpr, auto nv) {
+        by_width(a.H, [&](auto tpr, auto nv, int threads) {
             constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
             // at most 2^22 workgroups (a launch holds fewer than 2^32 threads); more rows go round
             const int grid = (int)std::min<int64_t>(ceil_div(a.R, Rows<TPR>::per_group), 1 << 22);
-            rmsnorm_fwd_kernel<decltype(t), TPR, NV><<<grid, Rows<TPR>::threads, 0, stream>>>(a);
+            rmsnorm_fwd_kernel<decltype(t), TPR, NV><<<grid, threads, 0, stream>>>(a);
         });
     });
     return hipGetLastError();
@@ -383,16 +428,15 @@ hipError_t launch_rmsnorm_fwd(const NormArgs& a, hipStream_t stream) {
 bool norm_bwd_small(int R, int H) { return R <= 512 || (R <= 1024 && H <= 1024); }
 
 int norm_bwd_groups(int R, int H) {
-    const int per = H <= 128 ? 16 : H <= 1024 ? 4 : 1;
-    const int64_t rows = ceil_div(R, per);
-    const int most = 512;
-    return (int)(rows < most ? rows : most);
+    // fewer than four rows each do not pay for a workgroup's partial row, once there are enough of them
+    if (H > 1024) return std::min({R, 512, std::max(256, R / 4)});
+    return (int)std::min<int64_t>(ceil_div(R, H <= 128 ? 16 : 4), 512);
 }
 
 hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, hipStream_t stream) {
     if (a.dweight != nullptr && a.R > 0 && norm_bwd_small(a.R, a.H)) {
         by_type(a.dtype, [&](auto t) {
-            by_width(a.H, [&](auto tpr, auto nv) {
+            by_width_small(a.H, [&](auto tpr, auto nv) {
                 constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
                 const int rows = (int)ceil_div(a.R, kSmallThreads / TPR), cols = (int)ceil_div(a.H, kReduceCols);
                 auto go = [&](int grid, int row_groups) {
@@ -411,17 +455,17 @@ hipError_t launch_rmsnorm_bwd(const NormBwdArgs& a, hipStream_t stream) {
     const int groups = norm_bwd_groups(a.R, a.H);
     if (groups > 0) {
         by_type(a.dtype, [&](auto t) {
-            by_width(a.H, [&](auto tpr, auto nv) {
+            by_width(a.H, [&](auto tpr, auto nv, int threads) {
                 constexpr int TPR = decltype(tpr)::value, NV = decltype(nv)::value;
-                rmsnorm_bwd_kernel<decltype(t), TPR, NV><<<groups, Rows<TPR>::threads, 0, stream>>>(a);
+                rmsnorm_bwd_kernel<decltype(t), TPR, NV><<<groups, threads, 0, stream>>>(a);
             });
         });
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (a.dweight != nullptr)
-        rmsnorm_dweight_kernel<<<(a.H + kReduceCols - 1) / kReduceCols, kReduceCols * kReduceRuns, 0, stream>>>(a.partial, groups, a.H,
-                                                                                          a.dweight);
+        rmsnorm_dweight_kernel<<<(a.H + kReduceCols - 1) / kReduceCols, kReduceCols * kReduceRuns, 0, stream>>>(
+            a.partial, groups, a.H, a.dweight);
     return hipGetLastError();
 }
 

@@ -118,7 +118,7 @@ def test_roots_are_never_lost(bd):
 
 def test_many_tensors(bd):
     """More tensors than one launch's table holds, empty ones among them."""
-    sizes = [(i * 37) % 300 for i in range(131)]
+    sizes = [(i * 37) % 300 for i in range(171)]
     s = state(3, sizes, torch.float32, torch.float32)
     before = [(a.clone(), b.clone(), c.clone()) for a, b, c in zip(s["p"], s["m"], s["v"])]
     bd.maxsim_adamw(bd.AdamWTensors(s["p"], s["m"], s["v"]), s["g"], 2, **HYPER)
