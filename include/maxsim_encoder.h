@@ -115,8 +115,11 @@ size_t maxsim_gemm_fp8_workspace_bytes(int32_t M, int32_t N, int32_t K);
  *   A        [M, K] e4m3, pitch lda;  a_scale [M, ceil(K/128)] fp32
  *   B        [N, K] e4m3, pitch ldb;  b_scale [ceil(N/b_block_rows), ceil(K/128)] fp32, b_block_rows 1 or 128
  *   c        [M, N] F16, BF16 or F32 (out_dtype), pitch ldc
- * Each block's products are added in fp32 on the matrix cores, the scaled
- * blocks in fp32; c is rounded once.  A, B: 16-byte aligned, lda and ldb
+ * The scaled blocks are added in fp32 and c is rounded once.  A block's products
+ * are added on the matrix cores: for an F32 c in fp32; for F16 and BF16 by the
+ * 8-bit instruction, which keeps about 13 bits below the block's largest product
+ * (1.4e-5 relative on normal values, where a 16-bit result's rounding is 2e-4 or
+ * 2e-3; where large products cancel inside a block, take an F32 c).  A, B: 16-byte aligned, lda and ldb
  * multiples of 16, at least K rounded up to 16, and every row readable that far (what lies
  * there after K is not used).  workspace: maxsim_gemm_fp8_workspace_bytes()
  * bytes, 16-byte aligned (NULL is fine when that is 0).

@@ -966,7 +966,8 @@ _TENSOR = np.dtype([("param", np.uint64), ("grad", np.uint64), ("master", np.uin
 class AdamWTensors:
     """The tensors that maxsim_adamw steps over: parameters (all fp16, bf16 or fp32), moments m and v, and for 16-bit
     parameters fp32 masters that they are rounded from (optional).  Moments are fp32, or float8_e4m3fn with m_scales
-    and v_scales (fp32, one for each 128 values; v is then held as its square root).  zeros() makes them."""
+    and v_scales (fp32, one for each 128 values; v is then held as its square root).  zeros() makes them.  The tensors
+    have to keep their memory: the table holds where it is."""
 
     def __init__(self, params, m, v, m_scales=None, v_scales=None, masters=None):
         params = list(params)
@@ -1062,6 +1063,7 @@ class RMSNormFunction(torch.autograd.Function):
         return y if residual is None else (y, h)
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dsum=None):
         h, weight, rstd = ctx.saved_tensors
         dx, dw = maxsim_rmsnorm_bwd(dy.contiguous(), h, rstd, weight,
@@ -1074,7 +1076,7 @@ class RMSNormFunction(torch.autograd.Function):
 def rms_norm(x, weight=None, residual=None, eps=1e-6):
     """x / sqrt(mean(x^2) + eps) * weight over the last dimension, with autograd support.  With a residual of x's shape: the norm
     of x + residual, and the sum itself, (y, sum)."""
-    return RMSNormFunction.apply(x, weight, residual, eps)
+    return RMSNormFunction.apply(x.contiguous(), weight, None if residual is None else residual.contiguous(), eps)
 
 
 class LinearFP8Function(torch.autograd.Function):
@@ -1083,19 +1085,21 @@ class LinearFP8Function(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight):
-        rows = x.reshape(-1, x.shape[-1])
+        rows = x.reshape(_row_count(x.shape), x.shape[-1]).contiguous()
         need_x, need_w = ctx.needs_input_grad
         q, s, qt, st = maxsim_quant_fp8(rows, transposed=need_w)
-        w, ws, wt, wst = maxsim_quant_fp8(weight, block_rows=QBLOCK, transposed=need_x)
+        w, ws, wt, wst = maxsim_quant_fp8(weight.contiguous(), block_rows=QBLOCK, transposed=need_x)
         ctx.save_for_backward(qt, st, wt, wst)
         ctx.x_shape, ctx.x_dtype, ctx.w_dtype = x.shape, x.dtype, weight.dtype
         return maxsim_gemm_fp8(q, s, w, ws, out_dtype=x.dtype).reshape(x.shape[:-1] + (weight.shape[0],))
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         qt, st, wt, wst = ctx.saved_tensors
         need_x, need_w = ctx.needs_input_grad
-        g, gs, gt, gst = maxsim_quant_fp8(dy.reshape(-1, dy.shape[-1]).contiguous(), rows=need_x, transposed=need_w)
+        g, gs, gt, gst = maxsim_quant_fp8(dy.reshape(_row_count(dy.shape), dy.shape[-1]).contiguous(), rows=need_x,
+                                          transposed=need_w)
         dx = dw = None
         if need_x:
             dx = maxsim_gemm_fp8(g, gs, wt, wst, out_dtype=ctx.x_dtype).reshape(ctx.x_shape)

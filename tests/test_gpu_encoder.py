@@ -281,3 +281,30 @@ def test_both_ways_through_the_binding(bd, H):
     assert bd._fast.gemm_fp8(q, s, b, bs, torch.int8) is None
     assert bd._fast.rmsnorm_bwd(t, t, t, None, None, True) is None
     assert bd._fast.adamw(tabs[0]._address, 2, 0, 2, 4, g[:1], 1e-3, .9, .99, 1e-8, 0., 1) is None
+
+
+def test_autograd_corners(bd):
+    """No tokens, views that are not contiguous, a leaf used twice, a second derivative (refused)."""
+    w = randn(1, 130, 64).requires_grad_()
+    x = torch.zeros(0, 64, device=DEV, requires_grad=True)
+    y = bd.linear_fp8(x, w)
+    y.sum().backward()
+    assert y.shape == (0, 130) and x.grad.shape == (0, 64) and torch.all(w.grad == 0)
+    wide = randn(2, 64, 50)
+    a, b = wide.t().clone().requires_grad_(), wide.clone().requires_grad_()
+    v = randn(3, 64, 130)
+    bd.linear_fp8(a, v.t()).square().sum().backward()
+    bd.linear_fp8(b.t(), v.t().contiguous()).square().sum().backward()
+    assert torch.equal(a.grad, b.grad.t())
+    n = bd.rms_norm(b.detach().t())
+    assert torch.equal(n, bd.rms_norm(b.detach().t().contiguous()))
+    both = randn(4, 40, 64).requires_grad_()
+    one, two = both.detach().clone().requires_grad_(), both.detach().clone().requires_grad_()
+    (bd.linear_fp8(both, w.detach()).sum() + 2 * bd.linear_fp8(both, w.detach()).sum()).backward()
+    bd.linear_fp8(one, w.detach()).sum().backward()
+    (2 * bd.linear_fp8(two, w.detach()).sum()).backward()
+    assert torch.allclose(both.grad, one.grad + two.grad, rtol=4 * ref.U, atol=0)
+    x = randn(5, 4, 64).requires_grad_()
+    g, = torch.autograd.grad(bd.rms_norm(x).square().sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.sum().backward()
