@@ -58,6 +58,23 @@ bool fits(int64_t n) { return n <= INT32_MAX; }
 Tensor empty(at::IntArrayRef shape, const Tensor& like, at::ScalarType type) {
     return at::empty(shape, like.options().dtype(type).requires_grad(false));
 }
+int64_t round16(int64_t n) { return (n + 15) / 16 * 16; }
+// [rows, width] e4m3 in rows a multiple of 16 bytes apart, as the product reads them.
+Tensor empty_e4m3(int64_t rows, int64_t width, const Tensor& like) {
+    const int64_t pitch = round16(width);
+    Tensor t = empty({rows, pitch}, like, at::kFloat8_e4m3fn);
+    return pitch == width ? t : t.narrow(1, 0, width);
+}
+// The pitch of such an operand, every row of which is readable up to its width rounded up to 16; 0: not one.
+int64_t operand_pitch(const Tensor& t, at::Device dev) {
+    if (t.scalar_type() != at::kFloat8_e4m3fn || t.device() != dev || t.dim() != 2) return 0;
+    const int64_t rows = t.size(0), width = t.size(1), wide = round16(width);
+    if (wide == width && t.is_contiguous()) return width;
+    if (rows < 1 || width < 1 || t.stride(1) != 1) return 0;
+    const int64_t ld = rows == 1 ? wide : t.stride(0);
+    if (ld < wide || t.storage_offset() + (rows - 1) * ld + wide > (int64_t)t.storage().nbytes()) return 0;
+    return ld;
+}
 PyObject* wrap(const Tensor& t) {
     if (t.defined()) return THPVariable_Wrap(t);
     Py_RETURN_NONE;
@@ -89,13 +106,13 @@ PyObject* rmsnorm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::ScalarType out = a[4] == Py_None ? type : reinterpret_cast<THPDtype*>(a[4])->scalar_type;
     const int code = code_of(type), out_code = code_of(out);
     const int64_t H = x->size(-1), R = H ? x->numel() / H : 0;
-    if (!is_float(code) || out_code < 0 || H < 1 || !fits(H) || !fits(R) || (out_code == MAXSIM_E4M3 && H % 16 != 0))
-        Py_RETURN_NONE;
+    const bool odd = out_code == MAXSIM_E4M3 && H % 16 != 0;  // rows that are padded
+    if (!is_float(code) || out_code < 0 || H < 1 || !fits(H) || !fits(R) || (odd && x->dim() != 2)) Py_RETURN_NONE;
     if (w && (!(good(*w, type, x->device()) || good(*w, at::kFloat, x->device())) || w->numel() != H)) Py_RETURN_NONE;
     if (res && (!good(*res, type, x->device()) || res->sizes() != x->sizes())) Py_RETURN_NONE;
     const int rstd_wanted = PyObject_IsTrue(a[5]);
     if (rstd_wanted < 0) return nullptr;
-    Tensor y = empty(x->sizes(), *x, out), scale, sum, rstd;
+    Tensor y = odd ? empty_e4m3(R, H, *x) : empty(x->sizes(), *x, out), scale, sum, rstd;
     const at::IntArrayRef rows = x->sizes().slice(0, x->dim() - 1);
     if (out_code == MAXSIM_I8) scale = empty(rows, *x, at::kFloat);
     if (out_code == MAXSIM_E4M3) {
@@ -106,7 +123,7 @@ PyObject* rmsnorm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (res) sum = empty(x->sizes(), *x, type);
     if (rstd_wanted) rstd = empty(rows, *x, at::kFloat);
     if (maxsim_rmsnorm_fwd(x->data_ptr(), H, at_(res), H, at_(w), w ? code_of(w->scalar_type()) : MAXSIM_F32, (int32_t)R,
-                           (int32_t)H, code, (float)eps, out_code, y.data_ptr(), H,
+                           (int32_t)H, code, (float)eps, out_code, y.data_ptr(), odd ? round16(H) : H,
                            scale.defined() ? scale.data_ptr<float>() : nullptr, sum.defined() ? sum.data_ptr() : nullptr,
                            H, rstd.defined() ? rstd.data_ptr<float>() : nullptr, stream_of(*x)) != MAXSIM_OK)
         Py_RETURN_NONE;
@@ -164,18 +181,19 @@ PyObject* quant_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         Py_RETURN_NONE;
     const int code = code_of(x->scalar_type());
     const int64_t R = x->size(0), C = x->size(1);
-    if (!is_float(code) || !fits(R) || !fits(C) || (rows && C % 16 != 0) || (both && R % 16 != 0)) Py_RETURN_NONE;
+    if (!is_float(code) || !fits(R) || !fits(C)) Py_RETURN_NONE;
     Tensor q, scale, qt, scale_t;
     if (rows) {
-        q = empty({R, C}, *x, at::kFloat8_e4m3fn);
+        q = empty_e4m3(R, C, *x);
         scale = empty({br == 1 ? R : blocks(R), blocks(C)}, *x, at::kFloat);
     }
     if (both) {
-        qt = empty({C, R}, *x, at::kFloat8_e4m3fn);
+        qt = empty_e4m3(C, R, *x);
         scale_t = empty({br == 1 ? C : blocks(C), blocks(R)}, *x, at::kFloat);
     }
-    if (maxsim_quant_fp8(x->data_ptr(), C, (int32_t)R, (int32_t)C, code, (int32_t)br, rows ? q.data_ptr() : nullptr, C,
-                         rows ? scale.data_ptr<float>() : nullptr, both ? qt.data_ptr() : nullptr, R,
+    if (maxsim_quant_fp8(x->data_ptr(), C, (int32_t)R, (int32_t)C, code, (int32_t)br, rows ? q.data_ptr() : nullptr,
+                         round16(C),
+                         rows ? scale.data_ptr<float>() : nullptr, both ? qt.data_ptr() : nullptr, round16(R),
                          both ? scale_t.data_ptr<float>() : nullptr, stream_of(*x)) != MAXSIM_OK)
         Py_RETURN_NONE;
     return tuple({q, scale, qt, scale_t});
@@ -193,16 +211,16 @@ PyObject* gemm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Device dev = A->device();
     const int64_t M = A->size(0), K = A->size(1), N = B->size(0), kb = blocks(K);
     const at::ScalarType out = reinterpret_cast<THPDtype*>(a[4])->scalar_type;
-    if (!good(*A, at::kFloat8_e4m3fn, dev) || !good(*B, at::kFloat8_e4m3fn, dev) || !good(*sa, at::kFloat, dev) ||
-        !good(*sb, at::kFloat, dev) || B->size(1) != K || K % 16 != 0 || !fits(M) || !fits(N) || !fits(K) ||
-        !is_float(code_of(out)))
+    const int64_t lda = operand_pitch(*A, dev), ldb = operand_pitch(*B, dev);
+    if (!lda || !ldb || !good(*sa, at::kFloat, dev) || !good(*sb, at::kFloat, dev) || B->size(1) != K || !fits(M) ||
+        !fits(N) || !fits(K) || !is_float(code_of(out)))
         Py_RETURN_NONE;
     const int32_t rows = sb->size(0) == N ? 1 : MAXSIM_QBLOCK;
     if (sa->numel() != M * kb || sb->numel() != (rows == 1 ? N : blocks(N)) * kb) Py_RETURN_NONE;
     Tensor c = empty({M, N}, *A, out), ws;
     const size_t bytes = maxsim_gemm_fp8_workspace_bytes((int32_t)M, (int32_t)N, (int32_t)K);
     if (bytes) ws = empty({(int64_t)bytes}, *A, at::kByte);
-    if (maxsim_gemm_fp8(A->data_ptr(), K, sa->data_ptr<float>(), B->data_ptr(), K, sb->data_ptr<float>(), rows, (int32_t)M,
+    if (maxsim_gemm_fp8(A->data_ptr(), lda, sa->data_ptr<float>(), B->data_ptr(), ldb, sb->data_ptr<float>(), rows, (int32_t)M,
                         (int32_t)N, (int32_t)K, code_of(out), c.data_ptr(), N, bytes ? ws.data_ptr() : nullptr, bytes,
                         stream_of(*A)) != MAXSIM_OK)
         Py_RETURN_NONE;
