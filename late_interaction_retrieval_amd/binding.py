@@ -966,8 +966,8 @@ _TENSOR = np.dtype([("param", np.uint64), ("grad", np.uint64), ("master", np.uin
 class AdamWTensors:
     """The tensors that maxsim_adamw steps over: parameters (all fp16, bf16 or fp32), moments m and v, and for 16-bit
     parameters fp32 masters that they are rounded from (optional).  Moments are fp32, or float8_e4m3fn with m_scales
-    and v_scales (fp32, one for each 128 values; v is then held as its square root).  zeros() makes them.  The tensors
-    have to keep their memory: the table holds where it is."""
+    and v_scales (fp32, one for each 128 values; v is then held as its square root).  zeros() makes them.  No two of
+    them may share memory (a tied weight is listed once), and each has to keep its own (a step checks that)."""
 
     def __init__(self, params, m, v, m_scales=None, v_scales=None, masters=None):
         params = list(params)
@@ -1006,6 +1006,17 @@ class AdamWTensors:
             put("master", self.masters, torch.float32)
         self._table = table
         self._address = table.ctypes.data
+        fields = [self.params, self.m, self.v] + ([self.m_scales, self.v_scales] if m_scales is not None else [])
+        self._held = [t for of_one in zip(*(fields + ([self.masters] if masters is not None else []))) for t in of_one]
+        self._held_at = [t.data_ptr() for t in self._held]
+        ends = sorted((at, at + t.numel() * t.element_size()) for at, t in zip(self._held_at, self._held) if t.numel())
+        if any(this[1] > following[0] for this, following in zip(ends, ends[1:])):
+            raise ValueError("two of the tensors share memory")
+
+    def _check_memory(self):
+        # a tensor whose .data was replaced, or whose storage was freed, would be updated where it no longer is
+        if any(t.data_ptr() != at for t, at in zip(self._held, self._held_at)):
+            raise ValueError("a tensor's memory has moved since this AdamWTensors was made")
 
     @classmethod
     def zeros(cls, params, state_dtype=torch.float32, masters=True):
@@ -1016,7 +1027,7 @@ class AdamWTensors:
         scales = lambda: [torch.zeros(-(-p.numel() // QBLOCK), device=p.device) for p in params]  # noqa: E731
         eight = state_dtype == torch.float8_e4m3fn
         held = [p.detach().float() for p in params] if masters and params[0].dtype != torch.float32 else None
-        return cls([p.detach() for p in params], moments(), moments(), scales() if eight else None,
+        return cls(params, moments(), moments(), scales() if eight else None,
                    scales() if eight else None, held)
 
 
@@ -1024,10 +1035,11 @@ def maxsim_adamw(tensors, grads, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8
                  stream=None):
     """One AdamW step of an AdamWTensors with these gradients (one tensor a parameter, all fp16, bf16 or fp32), in
     place.  step: the number of this step, from 1 on; or step_dev, a device int32 that holds it, for a step that is
-    captured and replayed."""
+    captured and replayed.  A graph that saved a parameter before the step refuses its backward after it, as after any
+    change in place."""
     if step_dev is None and stream is None:
         if _fast.adamw(tensors._address, len(tensors.sizes), tensors.device.index, tensors.param_code,
-                       tensors.state_code, grads, lr, beta1, beta2, eps, weight_decay, step):
+                       tensors.state_code, tensors._held, grads, lr, beta1, beta2, eps, weight_decay, step):
             return
     _adamw(tensors, grads, step, lr, beta1, beta2, eps, weight_decay, step_dev, stream=stream)
 
@@ -1035,6 +1047,7 @@ def maxsim_adamw(tensors, grads, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8
 @_on_its_device
 def _adamw(tensors, grads, step, lr, beta1, beta2, eps, weight_decay, step_dev):
     dev = tensors.device
+    tensors._check_memory()
     if len(grads) != len(tensors.sizes):
         raise ValueError("%d gradients for %d parameters" % (len(grads), len(tensors.sizes)))
     dtype = grads[0].dtype
@@ -1051,6 +1064,7 @@ def _adamw(tensors, grads, step, lr, beta1, beta2, eps, weight_decay, step_dev):
                            _raw_stream(dev))
     if st:
         _check(st, "maxsim_adamw")
+    torch.autograd.graph.increment_version([p for p in tensors.params if not p.is_inference()])
 
 
 class RMSNormFunction(torch.autograd.Function):

@@ -228,29 +228,42 @@ PyObject* gemm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// (table address, count, device index, param code, state code, grads, lr, beta1, beta2, eps, decay, step) -> True:
-// the table's entries with these gradients; its own memory is not written.
+// (table address, count, device index, param code, state code, held, grads, lr, beta1, beta2, eps, decay, step) ->
+// True: the table's entries with these gradients; its own memory is not written.  held: for each entry the tensors
+// param, m, v, (with 8-bit states) m_scale, v_scale, (with masters) master, which must be where the table says.
 PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 12 || !PyList_Check(a[5])) Py_RETURN_NONE;
+    if (n != 13 || !PyList_Check(a[5]) || !PyList_Check(a[6])) Py_RETURN_NONE;
     const auto* table = reinterpret_cast<const maxsim_adamw_tensor*>(PyLong_AsVoidPtr(a[0]));
     const Py_ssize_t count = PyLong_AsSsize_t(a[1]);
     const long device = PyLong_AsLong(a[2]), param = PyLong_AsLong(a[3]), state = PyLong_AsLong(a[4]);
     double v[5];
-    for (int i = 0; i < 5; ++i) v[i] = PyFloat_AsDouble(a[6 + i]);
-    const long step = PyLong_AsLong(a[11]);
+    for (int i = 0; i < 5; ++i) v[i] = PyFloat_AsDouble(a[7 + i]);
+    const long step = PyLong_AsLong(a[12]);
     if (PyErr_Occurred()) {
         PyErr_Clear();
         Py_RETURN_NONE;
     }
-    if (count < 1 || PyList_GET_SIZE(a[5]) != count || step < 1 || step > INT32_MAX ||
+    if (count < 1 || PyList_GET_SIZE(a[6]) != count || step < 1 || step > INT32_MAX ||
         device != c10::hip::current_device())
         Py_RETURN_NONE;
     std::vector<maxsim_adamw_tensor> t(table, table + count);
+    const bool packed = state == MAXSIM_E4M3;
+    const Py_ssize_t each = PyList_GET_SIZE(a[5]) / count, states = packed ? 5 : 3;
+    if (PyList_GET_SIZE(a[5]) != each * count || (each != states && each != states + 1)) Py_RETURN_NONE;
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        const void* at[6] = {t[i].param, t[i].m, t[i].v, t[i].m_scale, t[i].v_scale, nullptr};
+        at[states] = t[i].master;
+        for (Py_ssize_t j = 0; j < each; ++j) {
+            bool plain = true;
+            const Tensor* held = tensor(PyList_GET_ITEM(a[5], i * each + j), plain);
+            if (!held || held->data_ptr() != at[j]) Py_RETURN_NONE;
+        }
+    }
     at::ScalarType type = at::kFloat;
     for (Py_ssize_t i = 0; i < count; ++i) {
         bool plain = true;
-        const Tensor* g = tensor(PyList_GET_ITEM(a[5], i), plain);
+        const Tensor* g = tensor(PyList_GET_ITEM(a[6], i), plain);
         if (!g || !g->is_cuda() || g->device().index() != device || !g->is_contiguous() || g->numel() != t[i].n)
             Py_RETURN_NONE;
         if (i == 0) type = g->scalar_type();
@@ -261,6 +274,10 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!is_float(code_of(type)) || maxsim_adamw(t.data(), (int32_t)count, (int32_t)param, code_of(type), (int32_t)state,
                                                  v[0], v[1], v[2], v[3], v[4], (int32_t)step, nullptr, stream) != MAXSIM_OK)
         Py_RETURN_NONE;
+    for (Py_ssize_t i = 0; i < count; ++i) {  // the parameters have changed
+        const Tensor& param = THPVariable_Unpack(PyList_GET_ITEM(a[5], i * each));
+        if (!param.is_inference()) param.unsafeGetTensorImpl()->bump_version();
+    }
     Py_RETURN_TRUE;
     END_HANDLE_TH_ERRORS
 }

@@ -188,8 +188,9 @@ def test_binding_optimiser_table_refusals():
     s = [torch.zeros(5), torch.zeros(130)]
     q = [t.to(torch.float8_e4m3fn) for t in s]
     c = [torch.zeros(1), torch.zeros(2)]
-    assert bd.AdamWTensors(p, s, s).sizes == [5, 130]
-    bd.AdamWTensors(p, q, q, c, c)
+    other = lambda ts: [t.clone() for t in ts]  # noqa: E731
+    assert bd.AdamWTensors(p, s, other(s)).sizes == [5, 130]
+    bd.AdamWTensors(p, q, other(q), c, other(c))
     with pytest.raises(ValueError):
         bd.AdamWTensors([], [], [])
     with pytest.raises(ValueError):
@@ -208,3 +209,31 @@ def test_binding_optimiser_table_refusals():
         bd.AdamWTensors([t.int() for t in p], s, s)
     z = bd.AdamWTensors.zeros([t.bfloat16() for t in p], torch.float8_e4m3fn)
     assert z.masters[1].dtype == torch.float32 and z.m_scales[1].numel() == 2
+
+
+def test_binding_optimiser_memory():
+    """Tensors that share memory are refused when the table is made, and ones that have moved when it is used."""
+    make = lambda *sizes: [torch.zeros(n) for n in sizes]  # noqa: E731
+    p = make(5, 130)
+    for bad in ([p[0], p[0]], [torch.zeros(200)[:130], p[0]]):
+        with pytest.raises(ValueError):
+            bd.AdamWTensors(bad, make(5, 5), make(5, 5))
+    both = torch.zeros(200)
+    with pytest.raises(ValueError, match="share memory"):
+        bd.AdamWTensors([p[0], p[0]], make(5, 5), make(5, 5))
+    with pytest.raises(ValueError, match="share memory"):
+        bd.AdamWTensors([both[:100], both[99:]], make(100, 101), make(100, 101))
+    with pytest.raises(ValueError, match="share memory"):
+        bd.AdamWTensors(p, p, make(5, 130))
+    bd.AdamWTensors([both[:100], both[100:]], make(100, 100), make(100, 100))  # neighbours
+    bd.AdamWTensors([torch.zeros(0), p[0], torch.zeros(0)], make(0, 5, 0), make(0, 5, 0))
+    w = torch.nn.Parameter(torch.zeros(7))
+    tab = bd.AdamWTensors.zeros([w])
+    tab._check_memory()
+    w.data = torch.ones(7)
+    with pytest.raises(ValueError, match="moved"):
+        tab._check_memory()
+    tab = bd.AdamWTensors.zeros([w])
+    tab.m[0].untyped_storage().resize_(0)
+    with pytest.raises(ValueError, match="moved"):
+        tab._check_memory()

@@ -191,3 +191,26 @@ def test_binding_refusals(bd):
         bd.maxsim_adamw(tab, s["g"], 0)
     with pytest.raises(TypeError):
         bd.maxsim_adamw(tab, s["g"], 0, step_dev=torch.zeros(1, device=DEV))
+
+
+@pytest.mark.parametrize("device_step", [False, True])
+def test_parameters_of_autograd(bd, device_step):
+    """A parameter whose memory was replaced is refused, and a graph that saved one before the step refuses its
+    backward: both ways of making the call."""
+    w = torch.nn.Parameter(torch.ones(200, device=DEV))
+    tab = bd.AdamWTensors.zeros([w])
+    step = dict(step_dev=torch.ones(1, dtype=torch.int32, device=DEV)) if device_step else {}
+    loss = (w * w).sum()
+    bd.maxsim_adamw(tab, [torch.ones(200, device=DEV)], 1, **step)
+    assert torch.all(w < 1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        plain = torch.ones(200, device=DEV)
+    bd.maxsim_adamw(bd.AdamWTensors.zeros([plain]), [torch.ones(200, device=DEV)], 1, **step)
+    assert torch.equal(plain, w.detach())
+    was = w.data
+    w.data = was.clone()
+    with pytest.raises(ValueError, match="moved"):
+        bd.maxsim_adamw(tab, [torch.ones(200, device=DEV)], 2, **step)
+    assert torch.equal(was, w.data)
