@@ -153,3 +153,20 @@ def test_refusals(bd):
     big = [operand(1, 128, 1 << 16), torch.ones(128, 512, device=DEV)]
     with pytest.raises(bd.MaxSimError):
         bd.maxsim_gemm_fp8(*big, *big, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("N", [1 << 26, (1 << 27) + 5])
+def test_one_row_by_very_many(bd, N):
+    """More rows of B than one launch of the kernel for few rows of A holds threads for."""
+    codes = torch.arange(33, 94, dtype=torch.uint8, device=DEV)  # positive normal values
+    B = codes.repeat(N * 16 // 61 + 1)[:N * 16].view(torch.float8_e4m3fn).view(N, 16)
+    A = torch.full((1, 16), 0.5, device=DEV).to(torch.float8_e4m3fn)
+    one = torch.ones(1, 1, device=DEV)
+    sb = torch.arange(1, -(-N // 128) + 1, device=DEV).remainder_(7).add_(1).float().unsqueeze(1)
+    c = bd.maxsim_gemm_fp8(A, one, B, sb, out_dtype=torch.bfloat16)
+    for at in (0, 12345 * 128, (1 << 26) - 300, N - 200):
+        want = B[at:at + 200].double().sum(1) * 0.5
+        want = want * sb[:, 0].double()[torch.arange(at, min(at + 200, N), device=DEV) // 128]
+        got = c[0, at:at + 200].double()
+        # one rounding to bf16, and 16 products that the matrix cores add to 13 bits below the largest
+        assert torch.all((got - want).abs() <= want.abs() * (2.0 ** -8 * 1.01 + 16 * 2.0 ** -13)), at
