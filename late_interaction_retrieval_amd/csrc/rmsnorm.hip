@@ -10,6 +10,12 @@
 // that depends on it is formed from those registers.  A lane holds vectors of
 // 8 neighbouring columns, so 16 lanes hold exactly one block of 128 columns and
 // an e4m3 block's scale is a 16-lane maximum.
+//
+// Measured (bf16, the times of the kernels alone): forward 32768 x 2048 with a
+// residual, its sum and e4m3 out 95 us, 472 MB at 5.0 TB/s; backward 16384 x
+// 2048 with a gradient of the sum 54 us + 5 us for the gains, 268 MB at 4.6
+// TB/s; a copy of 1 GiB reaches 5.2.  32 x 128 fp32 to int8 2.8 us, 1003 x 769
+// fp16 backward 7.5 us: launches and the chain load, sum, store.
 #include <algorithm>
 #include <type_traits>
 
