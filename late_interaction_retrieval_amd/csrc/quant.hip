@@ -7,9 +7,9 @@
 // neighbouring values: a row block's maximum goes over 16 lanes by DPP, a
 // column block's over the thread's 8 rows, the lane groups and, through LDS,
 // the 4 waves.  HBM-bound: 2 (bf16) + 1 + 1 bytes a value.  Measured: 16384 x
-// 4096 bf16 both ways, scales by 128 values, 64-67 us (273 MB, 4.2 TB/s; 57 us
-// without the scales' writes, 4 bytes into a line each); 128 x 2048 in square
-// blocks 6.2 us, a launch and one tile's way through.
+// 4096 bf16 both ways, scales by 128 values, 55 us (273 MB, 5.0 TB/s; what is above
+// the 46 us of square blocks are the scales, 4 bytes into a line each); 128 x 2048
+// in square blocks 5.6 us, a launch and one tile's way through.
 #include "encoder_dev.h"
 
 namespace maxsim {
@@ -26,10 +26,11 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p) {
     const int64_t col_blocks = (p.R + kQBlock - 1) / kQBlock;  // scales of a row of qt
     // A row's scales share cache lines.  Where they are few, or all that is written
     // besides q, bands of 128 rows go to the XCDs in turn, so that such a line
-    // fills in one L2 (else each 4 bytes went to memory alone): 16384 x 4096
-    // rows alone 47.6 -> 44.2 us, 30001 x 1000 both ways 33.7 -> 29.9; but 16384 x 4096 both ways 60.1 -> 62.5.
+    // fills in one L2 (else each 4 bytes went to memory alone): 16384 x 4096 rows
+    // alone 37.9 -> 36.3 us, 65536 x 1024 38.3 -> 36.3, 30001 x 1000 both ways
+    // 32.3 -> 28.5; but 16384 x 2048 both ways 31.2 -> 32.0, x 4096 54.8 -> 57.4.
     uint32_t bc = blockIdx.x % (uint32_t)row_blocks, br = blockIdx.x / (uint32_t)row_blocks;
-    if (p.qt == nullptr || row_blocks <= 16) {
+    if (p.qt == nullptr || row_blocks <= 8) {
         const uint32_t eight = br >> 3, rest = blockIdx.x - eight * 8 * (uint32_t)row_blocks;
         if (8 * (eight + 1) <= (uint32_t)col_blocks) {
             bc = rest >> 3;
@@ -38,17 +39,34 @@ __global__ __launch_bounds__(256) void quant_kernel(QuantArgs p) {
     }
     const int c0 = (int)bc * kQBlock, r0 = (int)br * kQBlock;
     const int c = c0 + lane_c * kVec, r = r0 + lane_r * kVec;
+    // All 8 rows' loads are on their way together: rows past the end read the last
+    // one again, and what is not the tile's becomes 0 afterwards.  (With a branch at
+    // each load they waited for each other: 16384 x 4096 both ways 61.4 -> 55.3 us,
+    // 128 x 128 blocks 55.0 -> 46.0; 128 x 2048 6.4 -> 5.6.)
+    typename Pack8<T>::V in[kVec];
+    const T* rows[kVec];
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) rows[j] = (const T*)p.x + (int64_t)min(r + j, p.R - 1) * p.ldx;
+    if (p.C >= kVec) {
+        const int at = min(c, p.C - kVec);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) in[j] = *reinterpret_cast<const typename Pack8<T>::V*>(rows[j] + at);
+    } else {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) in[j] = load8<T>(rows[j], c, p.C);
+    }
     float x[kVec][kVec];
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
-        if (r + j < p.R) {
-            const auto v = load8<T>((const T*)p.x + (int64_t)(r + j) * p.ldx, c, p.C);
+        fit8<T>(in[j], c, p.C);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) x[j][i] = (float)v[i];
-        } else {
+        for (int i = 0; i < kVec; ++i) x[j][i] = (float)in[j][i];
+    }
+    if (r0 + kQBlock > p.R) {
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) x[j][i] = 0.f;
-        }
+        for (int j = 0; j < kVec; ++j)
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) x[j][i] = r + j < p.R ? x[j][i] : 0.f;
     }
     Scale whole;
     if constexpr (SQUARE) {
