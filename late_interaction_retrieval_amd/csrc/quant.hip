@@ -7,9 +7,10 @@
 // neighbouring values: a row block's maximum goes over 16 lanes by DPP, a
 // column block's over the thread's 8 rows, the lane groups and, through LDS,
 // the 4 waves.  HBM-bound: 2 (bf16) + 1 + 1 bytes a value.  Measured: 16384 x
-// 4096 bf16 both ways, scales by 128 values, 55 us (273 MB, 5.0 TB/s; what is above
-// the 46 us of square blocks are the scales, 4 bytes into a line each); 128 x 2048
-// in square blocks 5.6 us, a launch and one tile's way through.
+// 4096 bf16 both ways, scales by 128 values, 55 us where the outputs' memory is
+// written again and again, 62 where it is not (273 MB, 5.0 and 4.4 TB/s; square
+// blocks, without the scales' 4 bytes into a line each, 46); 128 x 2048 in square
+// blocks 5.4 us, a launch and one tile's way through.
 #include "encoder_dev.h"
 
 namespace maxsim {
