@@ -27,10 +27,13 @@
  *     of values to be held in 8 bits has one that is not finite, the block's
  *     scale is NaN and its values are 0.
  *
- * 8-bit values.  A block of values v shares one fp32 scale,
- *     scale = max|v| / 448 (e4m3) or max|v| / 127 (int8), held as round(v / scale),
- * ties to even, both divisions correctly rounded in fp32.  A block whose
- * largest magnitude is below 2^-100 is held as zeros with scale 1, so that 1 / scale never overflows.
+ * 8-bit values.  A block of values v shares one fp32 scale and is held as
+ * round(v / scale), ties to even:
+ *     e4m3  scale = max|v| * c, c the fp32 value next to 1/448 (what torch's division of
+ *           a tensor by 448.0 does on the device: scales and codes equal the plain form's);
+ *     int8  scale = max|v| / 127, correctly rounded in fp32.
+ * A block whose largest magnitude is below 2^-100 is held as zeros with scale 1, so
+ * that 1 / scale never overflows.
  * e4m3 is the OCP 8-bit format (4 exponent bits, 3 mantissa bits, largest value 448).
  */
 #ifndef MAXSIM_ENCODER_H
