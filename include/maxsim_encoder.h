@@ -154,7 +154,9 @@ typedef struct {
  *   step         t >= 1, the number of this step; or, where step_dev is not
  *                NULL, the device int32 there holds it when the work runs (for
  *                a captured step that is replayed; a captured `step` stays what it was)
- * E4M3 states: the update uses the new m and v in fp32, before they are held
+ * The moments are formed in fp32 as written here, left to right: beta m rounded, then
+ * the gradient's term (g^2 rounded) added with one rounding.  (So a gradient past 1.8e19
+ * makes v infinite.)  E4M3 states: the update uses the new m and v in fp32, before they are held
  * in 8 bits again; a second moment that is not 0 is never held as 0 (its root
  * is at least the smallest e4m3 value, 2^-9, times the block's scale).
  * All-zero memory is a valid start for both kinds of state.
