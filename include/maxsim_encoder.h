@@ -160,7 +160,8 @@ typedef struct {
  * in 8 bits again; a second moment that is not 0 is never held as 0 (its root
  * is at least the smallest e4m3 value, 2^-9, times the block's scale).
  * All-zero memory is a valid start for both kinds of state.
- * Up to 56 tensors go into one launch.  Requires 0 <= beta1, beta2 < 1.
+ * Up to 56 tensors go into one launch.  After MAXSIM_ERR_HIP some of the tensors may have
+ * been stepped: the step is not to be made again from this state.  Requires 0 <= beta1, beta2 < 1.
  */
 int maxsim_adamw(const maxsim_adamw_tensor* tensors, int32_t count, int32_t param_dtype, int32_t grad_dtype,
                  int32_t state_dtype, double lr, double beta1, double beta2, double eps, double weight_decay,

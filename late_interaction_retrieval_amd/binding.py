@@ -1038,9 +1038,10 @@ def maxsim_adamw(tensors, grads, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8
     captured and replayed.  A graph that saved a parameter before the step refuses its backward after it, as after any
     change in place."""
     if step_dev is None and stream is None:
-        if _fast.adamw(tensors._address, len(tensors.sizes), tensors.device.index, tensors.param_code,
-                       tensors.state_code, tensors._held, grads, lr, beta1, beta2, eps, weight_decay, step):
-            return
+        st = _fast.adamw(tensors._address, len(tensors.sizes), tensors.device.index, tensors.param_code,
+                         tensors.state_code, tensors._held, grads, lr, beta1, beta2, eps, weight_decay, step)
+        if st is not None:  # the call was made: never make it again, the step is in place
+            return _check(st, "maxsim_adamw")
     _adamw(tensors, grads, step, lr, beta1, beta2, eps, weight_decay, step_dev, stream=stream)
 
 
@@ -1062,9 +1063,9 @@ def _adamw(tensors, grads, step, lr, beta1, beta2, eps, weight_decay, step_dev):
     st = _lib.maxsim_adamw(table.ctypes.data, len(grads), tensors.param_code, code, tensors.state_code, lr, beta1,
                            beta2, eps, weight_decay, step, None if step_dev is None else step_dev.data_ptr(),
                            _raw_stream(dev))
-    if st:
-        _check(st, "maxsim_adamw")
-    torch.autograd.graph.increment_version([p for p in tensors.params if not p.is_inference()])
+    if st in (MAXSIM_OK, MAXSIM_ERR_HIP):  # the parameters have changed, or some may have
+        torch.autograd.graph.increment_version([p for p in tensors.params if not p.is_inference()])
+    _check(st, "maxsim_adamw")
 
 
 class RMSNormFunction(torch.autograd.Function):

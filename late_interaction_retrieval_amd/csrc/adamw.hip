@@ -188,6 +188,9 @@ void launch_by_grad(int grad_dtype, const Table& tab, const Step& st, bool packe
 
 hipError_t launch_adamw(const maxsim_adamw_tensor* t, int count, int param_dtype, int grad_dtype, int state_dtype,
                         const AdamWHyper& hp, hipStream_t stream) {
+    // An error that an earlier call of the program left unread is not this step's: reported
+    // after the launches it would make a step that ran look like one that did not.
+    (void)hipGetLastError();
     Step st{};
     // doubles up to here: 1 - 0.999 in fp32 is off by 1e-5 of itself
     st.beta1 = (float)hp.beta1;

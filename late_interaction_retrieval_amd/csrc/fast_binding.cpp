@@ -7,6 +7,8 @@
 // current device, outputs to be allocated -- and returns its results; anything
 // else, and any status but MAXSIM_OK, gives None, and the binding function
 // goes its own way, which handles the general case and names what is wrong.
+// adamw() returns the status instead, and None only where it made no call: a step
+// in place that may have been launched must not be made again.
 #include <Python.h>
 
 #include <ATen/ATen.h>
@@ -229,7 +231,7 @@ PyObject* gemm_fp8(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 // (table address, count, device index, param code, state code, held, grads, lr, beta1, beta2, eps, decay, step) ->
-// True: the table's entries with these gradients; its own memory is not written.  held: for each entry the tensors
+// the call's status: the table's entries with these gradients; its own memory is not written.  held: for each entry the tensors
 // param, m, v, (with 8-bit states) m_scale, v_scale, (with masters) master, which must be where the table says.
 PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
@@ -271,14 +273,16 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
         t[i].grad = g->data_ptr();
     }
     void* stream = c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream();
-    if (!is_float(code_of(type)) || maxsim_adamw(t.data(), (int32_t)count, (int32_t)param, code_of(type), (int32_t)state,
-                                                 v[0], v[1], v[2], v[3], v[4], (int32_t)step, nullptr, stream) != MAXSIM_OK)
-        Py_RETURN_NONE;
-    for (Py_ssize_t i = 0; i < count; ++i) {  // the parameters have changed
-        const Tensor& param = THPVariable_Unpack(PyList_GET_ITEM(a[5], i * each));
-        if (!param.is_inference()) param.unsafeGetTensorImpl()->bump_version();
+    if (!is_float(code_of(type))) Py_RETURN_NONE;
+    const int status = maxsim_adamw(t.data(), (int32_t)count, (int32_t)param, code_of(type), (int32_t)state, v[0], v[1], v[2],
+                                    v[3], v[4], (int32_t)step, nullptr, stream);
+    if (status == MAXSIM_OK || status == MAXSIM_ERR_HIP) {  // the parameters have changed, or some may have
+        for (Py_ssize_t i = 0; i < count; ++i) {
+            const Tensor& param = THPVariable_Unpack(PyList_GET_ITEM(a[5], i * each));
+            if (!param.is_inference()) param.unsafeGetTensorImpl()->bump_version();
+        }
     }
-    Py_RETURN_TRUE;
+    return PyLong_FromLong(status);
     END_HANDLE_TH_ERRORS
 }
 
