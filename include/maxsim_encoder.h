@@ -158,7 +158,8 @@ typedef struct {
  * the gradient's term (g^2 rounded) added with one rounding.  (So a gradient past 1.8e19
  * makes v infinite.)  E4M3 states: the update uses the new m and v in fp32, before they are held
  * in 8 bits again; a second moment that is not 0 is never held as 0 (its root
- * is at least the smallest e4m3 value, 2^-9, times the block's scale).
+ * is at least the smallest e4m3 value, 2^-9, times the block's scale) nor read as 0 (where that
+ * value's square leaves fp32, it is read as the smallest fp32 value, 2^-149).
  * All-zero memory is a valid start for both kinds of state.
  * Up to 56 tensors go into one launch.  After MAXSIM_ERR_HIP some of the tensors may have
  * been stepped: the step is not to be made again from this state.  Requires 0 <= beta1, beta2 < 1.

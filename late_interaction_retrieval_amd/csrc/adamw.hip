@@ -123,7 +123,10 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Table tab, const 
         load_e4m3(t.m, at, n, any ? t.m_scale[at / kQBlock] : 0.f, m);
         load_e4m3(t.v, at, n, any ? t.v_scale[at / kQBlock] : 0.f, v);
 #pragma unroll
-        for (int i = 0; i < kVec; ++i) v[i] *= v[i];
+        for (int i = 0; i < kVec; ++i) {  // a root that is not 0 has a square that is not 0, below 2^-75 too
+            const float sq = v[i] * v[i];
+            v[i] = sq == 0.f && v[i] != 0.f ? __FLT_DENORM_MIN__ : sq;
+        }
     } else {
         load_f<float>(t.m, at, n, m);
         load_f<float>(t.v, at, n, v);

@@ -82,3 +82,23 @@ def test_fp32_states_stay_with_the_plain_form(bd):
         bd.maxsim_adamw(tab, [g], t, 1e-3, B1, B2)
         m, v = moments(m, v, g)
         assert torch.equal(tab.m[0], m) and torch.equal(tab.v[0], v), t
+
+
+@pytest.mark.parametrize("largest", [1.0, 1e-9, 1.85e-16, 1e-18])
+def test_a_second_moment_is_never_lost(bd, largest):
+    """Blocks whose roots reach down to where their squares leave fp32: with eps = 0 a moment read as 0 would be a division
+    by 0.  1.85e-16: the largest root is 5.85e-18, the smallest code's value 2.55e-23 and its square 6.5e-46, less than
+    half of the smallest fp32 value.  The second step's m / sqrt(v) is at most 1.8 times (codes of m and of the root off by
+    half a step each at the smallest, 1.5 and 2 / 3 of them) the first step's, 1: 8 is safe."""
+    small = 1.18e-21   # its square times 1 - beta2 rounds to the smallest fp32 value
+    g = torch.full((256,), small, device=DEV)
+    g[5] = largest
+    g[200] = 0.0
+    tab = bd.AdamWTensors.zeros([torch.zeros(256, device=DEV)], torch.float8_e4m3fn)
+    bd.maxsim_adamw(tab, [g], 1, 2.0 ** -10, B1, B2, 0.0, 0.0)
+    # g[200] gives 0 / 0, as the formula has it; all others move
+    ok = torch.arange(256, device=DEV) != 200
+    first = tab.params[0].clone()
+    assert torch.isnan(first[200]) and torch.isfinite(first[ok]).all() and torch.all(tab.v[0].float()[ok] > 0)
+    bd.maxsim_adamw(tab, [torch.zeros_like(g)], 2, 2.0 ** -10, B1, B2, 0.0, 0.0)
+    assert torch.all((tab.params[0] - first)[ok].abs() <= 8 * 2.0 ** -10)
