@@ -1073,6 +1073,7 @@ class RMSNormFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, weight, residual, eps):
+        ctx.set_materialize_grads(False)  # an output that nothing uses costs no tensor of zeros
         y, _, h, rstd = maxsim_rmsnorm_fwd(x, weight, eps, residual=residual, with_rstd=True)
         ctx.save_for_backward(x if residual is None else h, weight, rstd)
         return y if residual is None else (y, h)
@@ -1081,9 +1082,15 @@ class RMSNormFunction(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy, dsum=None):
         h, weight, rstd = ctx.saved_tensors
-        dx, dw = maxsim_rmsnorm_bwd(dy.contiguous(), h, rstd, weight,
-                                    dsum=None if dsum is None else dsum.contiguous(),
-                                    with_dweight=weight is not None and ctx.needs_input_grad[1])
+        dw = None
+        if dy is None:  # only the sum was used
+            dx = dsum
+            if weight is not None and ctx.needs_input_grad[1]:
+                dw = torch.zeros_like(weight)
+        else:
+            dx, dw = maxsim_rmsnorm_bwd(dy.contiguous(), h, rstd, weight,
+                                        dsum=None if dsum is None else dsum.contiguous(),
+                                        with_dweight=weight is not None and ctx.needs_input_grad[1])
         return (dx if ctx.needs_input_grad[0] else None, None if dw is None else dw.to(weight.dtype),
                 dx if ctx.needs_input_grad[2] else None, None)
 

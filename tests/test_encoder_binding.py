@@ -46,3 +46,51 @@ def test_a_step_that_the_extension_leaves_alone_goes_the_general_way(step, monke
     monkeypatch.setattr(bd._fast, "adamw", lambda *a: None)
     with pytest.raises(ValueError, match="must be on the device"):  # host tensors
         bd.maxsim_adamw(tab, [torch.zeros(5)], 1)
+
+
+@pytest.fixture
+def norm_on_host(monkeypatch):
+    """The norm's two calls by plain torch on the host; what the backward is given is kept."""
+    seen = []
+
+    def fwd(x, weight=None, eps=1e-6, residual=None, with_rstd=False):
+        h = x if residual is None else x + residual
+        rstd = torch.rsqrt(h.square().mean(-1) + eps)
+        return h * rstd[..., None] * (1 if weight is None else weight), None, None if residual is None else h, rstd
+
+    def bwd(dy, h, rstd, weight=None, dsum=None, with_dweight=True):
+        seen.append((dy, dsum))
+        g, xh = dy * (1 if weight is None else weight), h * rstd[..., None]
+        dx = rstd[..., None] * (g - xh * (g * xh).mean(-1, keepdim=True)) + (0 if dsum is None else dsum)
+        return dx, (dy * xh).flatten(0, -2).sum(0) if with_dweight else None
+
+    monkeypatch.setattr(bd, "maxsim_rmsnorm_fwd", fwd)
+    monkeypatch.setattr(bd, "maxsim_rmsnorm_bwd", bwd)
+    return seen
+
+
+@pytest.mark.parametrize("use_y,use_sum", [(True, False), (False, True), (True, True)])
+def test_outputs_of_the_norm_that_nothing_uses(norm_on_host, use_y, use_sum):
+    """An output without a gradient reaches the backward as none, not as zeros; the gradients are the formula's."""
+    g = torch.Generator().manual_seed(1)
+    x, w, r = (torch.randn(s, generator=g, dtype=torch.float64).requires_grad_() for s in ((3, 8), (8,), (3, 8)))
+    dy, ds = (torch.randn(3, 8, generator=g, dtype=torch.float64) for _ in range(2))
+
+    def loss(y, h):
+        if use_y and use_sum:
+            return (y * dy).sum() + (h * ds).sum()
+        return (y * dy if use_y else h * ds).sum()
+
+    loss(*bd.rms_norm(x, w, residual=r)).backward()
+    got = [t.grad for t in (x, w, r)]
+    plain = [t.detach().clone().requires_grad_() for t in (x, w, r)]
+    h = plain[0] + plain[2]
+    loss(h * torch.rsqrt(h.square().mean(-1, keepdim=True) + 1e-6) * plain[1], h).backward()
+    for a, b in zip(got, plain):
+        if b.grad is None:
+            assert torch.all(a == 0)
+        else:
+            assert torch.all((a - b.grad).abs() <= 1e-13 * (1 + b.grad.abs()))  # a few roundings of 1.1e-16 each
+    assert len(norm_on_host) == use_y
+    if use_y:
+        assert (norm_on_host[0][1] is not None) == use_sum
