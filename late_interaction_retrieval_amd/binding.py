@@ -10,6 +10,8 @@ allocated with torch) and streams.
 import ctypes
 import functools
 import os
+import types
+import warnings
 
 import numpy as np
 import torch
@@ -108,7 +110,12 @@ def lib():
 
 
 lib()  # fail loudly at import time if the native library is missing
-from . import _fast  # noqa: E402  the usual calls of the embedding head's operators, natively (fast_binding.cpp)
+try:  # the usual calls of the embedding head's operators, natively (fast_binding.cpp)
+    from . import _fast
+except ImportError as e:  # not built, or built against another torch: all of them go through ctypes
+    warnings.warn("late_interaction_retrieval_amd: no _fast.so (%s): calls take some microseconds more" % e, RuntimeWarning)
+    _fast = types.SimpleNamespace(**{name: lambda *args: None for name in ("rmsnorm_fwd", "rmsnorm_bwd", "quant_fp8",
+                                                                         "gemm_fp8", "adamw")})
 
 
 def _ptr(t):

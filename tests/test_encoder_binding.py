@@ -1,9 +1,15 @@
 """The binding of the embedding head's operators on a host without a GPU: which way a call takes, and what it refuses
 before any device work."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
 from late_interaction_retrieval_amd import binding as bd
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture
@@ -94,3 +100,29 @@ def test_outputs_of_the_norm_that_nothing_uses(norm_on_host, use_y, use_sum):
     assert len(norm_on_host) == use_y
     if use_y:
         assert (norm_on_host[0][1] is not None) == use_sum
+
+
+def test_the_package_does_without_the_extension():
+    """_fast.so missing, or built against another torch: a warning, and every call goes the general way."""
+    code = """
+import sys, warnings
+sys.modules["late_interaction_retrieval_amd._fast"] = None  # an import of it raises ImportError
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    from late_interaction_retrieval_amd import binding as bd
+assert any("_fast.so" in str(w.message) for w in seen)
+import torch
+x, q = torch.zeros(4, 128), torch.zeros(4, 128).to(torch.float8_e4m3fn)
+tab = bd.AdamWTensors.zeros([torch.zeros(5)])
+for f in (lambda: bd.maxsim_rmsnorm_fwd(x), lambda: bd.maxsim_rmsnorm_bwd(x, x, x[:, 0]), lambda: bd.maxsim_quant_fp8(x),
+          lambda: bd.maxsim_gemm_fp8(q, x[:, :1], q, x[:, :1]), lambda: bd.maxsim_adamw(tab, [torch.zeros(5)], 1)):
+    try:
+        f()
+    except ValueError as e:
+        assert "must be on the device" in str(e), e
+    else:
+        raise AssertionError("a host tensor was taken")
+print("all general")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert r.returncode == 0 and "all general" in r.stdout, r.stderr
