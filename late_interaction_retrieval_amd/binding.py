@@ -1137,11 +1137,26 @@ class LinearFP8Function(torch.autograd.Function):
         return dx, dw
 
 
+_MOST_K = 1 << 22  # of maxsim_gemm_fp8
+
+
+def _product_takes(M, N, K):
+    """Sizes within maxsim_gemm_fp8's limits."""
+    return K <= _MOST_K and -(-M // QBLOCK) * -(-N // QBLOCK) < 1 << 22
+
+
 def linear_fp8(x, weight):
     """x [..., K] times weight [N, K] transposed, in 8-bit floating point with a scale for each block of 128, with
-    autograd support (x, weight: fp16, bf16 or fp32; the result has x's type)."""
+    autograd support (x, weight: fp16, bf16 or fp32; the result has x's type).  A gradient's product runs over the
+    tokens (of weight) or over N (of x), of which it takes 2^22 at most."""
     if weight.dim() != 2 or x.shape[-1] != weight.shape[1]:
         raise ValueError("x [..., K] and weight [N, K] must share K")
+    if torch.is_grad_enabled():  # refused here and not by the product in the backward
+        T, (N, K) = _row_count(x.shape), weight.shape
+        if weight.requires_grad and not _product_takes(N, K, T):
+            raise ValueError("linear_fp8: no gradient of a weight [%d, %d] from %d tokens (at most %d)" % (N, K, T, _MOST_K))
+        if x.requires_grad and not _product_takes(T, K, N):
+            raise ValueError("linear_fp8: no gradient of x [%d, %d] through %d columns (at most %d)" % (T, K, N, _MOST_K))
     return LinearFP8Function.apply(x, weight)
 
 

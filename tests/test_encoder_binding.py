@@ -126,3 +126,20 @@ print("all general")
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
     assert r.returncode == 0 and "all general" in r.stdout, r.stderr
+
+
+def test_a_linear_layer_refuses_what_its_backward_could_not_do():
+    """More tokens, or columns, than the gradient's product takes along its sum: refused by the forward, where that
+    gradient is asked for."""
+    many = (1 << 22) + 1
+    flat = lambda rows, grad: torch.zeros(rows, 16, requires_grad=grad)  # noqa: E731
+    with pytest.raises(ValueError, match="no gradient of a weight"):
+        bd.linear_fp8(flat(many, False), flat(3, True))
+    with pytest.raises(ValueError, match="no gradient of x"):
+        bd.linear_fp8(flat(3, True), flat(many, False))
+    # not asked for, or within the limit: on to the call, which refuses host tensors
+    for x, w in ((flat(many, True), flat(3, False)), (flat(3, False), flat(many, True)), (flat(many - 1, True), flat(3, True))):
+        with pytest.raises(ValueError, match="must be on the device"):
+            bd.linear_fp8(x, w)
+    with torch.no_grad(), pytest.raises(ValueError, match="must be on the device"):
+        bd.linear_fp8(flat(many, False), flat(3, True))
