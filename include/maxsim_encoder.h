@@ -170,7 +170,10 @@ typedef struct {
  * value's square leaves fp32, it is read as the smallest fp32 value, 2^-149).
  * All-zero memory is a valid start for both kinds of state.
  * Up to 56 tensors go into one launch.  After MAXSIM_ERR_HIP some of the tensors may have
- * been stepped: the step is not to be made again from this state.  Requires 0 <= beta1, beta2 < 1.
+ * been stepped: the step is not to be made again from this state.  Requires 0 <= beta1, beta2 < 1,
+ * eps >= 0, lr and weight_decay finite.  A gradient that is not finite makes its own values NaN or infinite and,
+ * with E4M3 states, the moments of its whole block of 128 NaN from the next step on: where that may
+ * happen, look at the gradients before the step.
  */
 int maxsim_adamw(const maxsim_adamw_tensor* tensors, int32_t count, int32_t param_dtype, int32_t grad_dtype,
                  int32_t state_dtype, double lr, double beta1, double beta2, double eps, double weight_decay,

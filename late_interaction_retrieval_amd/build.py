@@ -31,8 +31,8 @@ HIPCC_FLAGS = [
 ]
 # inputs are finite: max needs no NaN canonicalisation (infinities are kept)
 FINITE_FLAGS = ["-fno-honor-nans"]
-# these pass NaN and infinity through as their formulas give them
-SOURCE_FLAGS = {s: [] for s in ("rmsnorm.hip", "quant.hip", "gemm_fp8.hip", "adamw.hip")}
+# these pass NaN and infinity through as their formulas give them, or refuse them
+SOURCE_FLAGS = {s: [] for s in ("rmsnorm.hip", "quant.hip", "gemm_fp8.hip", "adamw.hip", "capi_encoder.cpp")}
 
 
 def hipcc():

@@ -4,6 +4,8 @@
 
 #include <hip/hip_runtime_api.h>
 
+#include <cmath>
+
 #include "encoder.h"
 
 namespace {
@@ -173,6 +175,7 @@ int maxsim_adamw(const maxsim_adamw_tensor* tensors, int32_t count, int32_t para
                  int32_t step, const int32_t* step_dev, void* stream) {
     if (count < 0 || (!step_dev && step < 1)) return MAXSIM_ERR_SHAPE;
     if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0)) return MAXSIM_ERR_SHAPE;
+    if (!std::isfinite(lr) || !std::isfinite(weight_decay)) return MAXSIM_ERR_SHAPE;
     if (!is_float(param_dtype) || !is_float(grad_dtype)) return MAXSIM_ERR_UNSUPPORTED;
     if (state_dtype != MAXSIM_F32 && state_dtype != MAXSIM_E4M3) return MAXSIM_ERR_UNSUPPORTED;
     if (count == 0) return MAXSIM_OK;
