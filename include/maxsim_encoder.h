@@ -31,7 +31,8 @@
  * round(v / scale), ties to even:
  *     e4m3  scale = max|v| * c, c the fp32 value next to 1/448 (what torch's division of
  *           a tensor by 448.0 does on the device: scales and codes equal the plain form's);
- *     int8  scale = max|v| / 127, correctly rounded in fp32.
+ *     int8  scale = max|v| / 127, rounded to nearest in fp32.
+ * v / scale is the nearest fp32 value or, in about 1 of 10^7 cases, its neighbour, before it is rounded to 8 bits.
  * A block whose largest magnitude is below 2^-100 is held as zeros with scale 1, so
  * that 1 / scale never overflows.
  * e4m3 is the OCP 8-bit format (4 exponent bits, 3 mantissa bits, largest value 448).

@@ -138,9 +138,11 @@ struct Scale {
     float inv;   // 1 / s to a unit in the last place
     bool zeros;  // the block is held as zeros (too small, or not finite)
 };
-// v / s correctly rounded in 3 operations (a division has ten), given inv =
-// 1 / s to a unit in the last place: the product is within 3 units, its
-// remainder is exact in a fused multiply-add, and the correction rounds once.
+// v / s in 3 operations (a division has ten), given inv = 1 / s to a unit in the
+// last place: the product is within 3 units, and the correction by its remainder leaves
+// the nearest value or, in about 1 of 10^7 pairs, its neighbour (the remainder of a product 3
+// units off need not fit 24 bits).  For s = 127 with inv rounded to nearest all 2^23 mantissas
+// of v give the nearest.
 __device__ __forceinline__ float quotient(float v, float s, float inv) {
     const float q = v * inv;
     return __builtin_fmaf(__builtin_fmaf(-q, s, v), inv, q);
