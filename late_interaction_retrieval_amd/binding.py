@@ -1098,7 +1098,7 @@ class RMSNormFunction(torch.autograd.Function):
             dx, dw = maxsim_rmsnorm_bwd(dy.contiguous(), h, rstd, weight,
                                         dsum=None if dsum is None else dsum.contiguous(),
                                         with_dweight=weight is not None and ctx.needs_input_grad[1])
-        return (dx if ctx.needs_input_grad[0] else None, None if dw is None else dw.to(weight.dtype),
+        return (dx if ctx.needs_input_grad[0] else None, None if dw is None else dw.to(weight.dtype).reshape(weight.shape),
                 dx if ctx.needs_input_grad[2] else None, None)
 
 

@@ -62,11 +62,11 @@ def norm_on_host(monkeypatch):
     def fwd(x, weight=None, eps=1e-6, residual=None, with_rstd=False):
         h = x if residual is None else x + residual
         rstd = torch.rsqrt(h.square().mean(-1) + eps)
-        return h * rstd[..., None] * (1 if weight is None else weight), None, None if residual is None else h, rstd
+        return h * rstd[..., None] * (1 if weight is None else weight.reshape(-1)), None, None if residual is None else h, rstd
 
     def bwd(dy, h, rstd, weight=None, dsum=None, with_dweight=True):
         seen.append((dy, dsum))
-        g, xh = dy * (1 if weight is None else weight), h * rstd[..., None]
+        g, xh = dy * (1 if weight is None else weight.reshape(-1)), h * rstd[..., None]
         dx = rstd[..., None] * (g - xh * (g * xh).mean(-1, keepdim=True)) + (0 if dsum is None else dsum)
         return dx, (dy * xh).flatten(0, -2).sum(0) if with_dweight else None
 
@@ -143,3 +143,13 @@ def test_a_linear_layer_refuses_what_its_backward_could_not_do():
             bd.linear_fp8(x, w)
     with torch.no_grad(), pytest.raises(ValueError, match="must be on the device"):
         bd.linear_fp8(flat(many, False), flat(3, True))
+
+
+@pytest.mark.parametrize("shape", [(8,), (1, 8), (1, 1, 8), (2, 4)])
+def test_a_gain_of_any_shape_gets_its_gradient(norm_on_host, shape):
+    """The forward takes a gain of H contiguous values whatever their shape, and its gradient has that shape."""
+    w = torch.ones(shape, dtype=torch.float64, requires_grad=True)
+    x = torch.arange(24, dtype=torch.float64).reshape(3, 8)
+    bd.rms_norm(x, w).sum().backward()
+    xh = x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6)
+    assert w.grad.shape == shape and torch.all((w.grad.reshape(-1) - xh.sum(0)).abs() <= 1e-13)
