@@ -1020,6 +1020,10 @@ class AdamWTensors:
         if any(this[1] > following[0] for this, following in zip(ends, ends[1:])):
             raise ValueError("two of the tensors share memory")
 
+    def __reduce__(self):
+        # a copy, or one read back from a file, has tensors of its own, and so a table of its own
+        return type(self), (self.params, self.m, self.v, self.m_scales, self.v_scales, self.masters)
+
     def _check_memory(self):
         # a tensor whose .data was replaced, or whose storage was freed, would be updated where it no longer is
         if any(t.data_ptr() != at for t, at in zip(self._held, self._held_at)):

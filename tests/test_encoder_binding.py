@@ -1,5 +1,7 @@
 """The binding of the embedding head's operators on a host without a GPU: which way a call takes, and what it refuses
 before any device work."""
+import copy
+import io
 import os
 import subprocess
 import sys
@@ -153,3 +155,25 @@ def test_a_gain_of_any_shape_gets_its_gradient(norm_on_host, shape):
     bd.rms_norm(x, w).sum().backward()
     xh = x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-6)
     assert w.grad.shape == shape and torch.all((w.grad.reshape(-1) - xh.sum(0)).abs() <= 1e-13)
+
+
+@pytest.mark.parametrize("state", [torch.float32, torch.float8_e4m3fn], ids=str)
+@pytest.mark.parametrize("how", ["deepcopy", "file", "copy"])
+def test_a_copied_optimiser_table_is_one_of_its_own(state, how):
+    """Copied, or written and read back: the table names the copy's tensors, at an address that is its own."""
+    tab = bd.AdamWTensors.zeros([torch.nn.Parameter(torch.ones(5).bfloat16()), torch.ones(300).bfloat16()], state)
+    if how == "file":
+        f = io.BytesIO()
+        torch.save(tab, f)
+        f.seek(0)
+        other = torch.load(f, weights_only=False)  # written just now
+    else:
+        other = copy.deepcopy(tab) if how == "deepcopy" else copy.copy(tab)
+    other._check_memory()
+    assert other._address == other._table.ctypes.data != tab._address
+    assert [int(a) for a in other._table["param"]] == [p.data_ptr() for p in other.params]
+    assert [int(a) for a in other._table["m"]] == [p.data_ptr() for p in other.m]
+    assert (other.params[1].data_ptr() == tab.params[1].data_ptr()) == (how == "copy")
+    assert other.sizes == tab.sizes and (other.state_code, other.param_code) == (tab.state_code, tab.param_code)
+    for a, b in zip(other._held, tab._held):
+        assert a.dtype == b.dtype and torch.equal(a.float(), b.float())
