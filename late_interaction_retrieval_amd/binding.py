@@ -733,13 +733,18 @@ def _empty_e4m3(like, shape):
     return like.new_empty(tuple(shape[:-1]) + (width + pad,), dtype=torch.float8_e4m3fn)[..., :width]
 
 
+def _size(n):
+    """A size or step for the C entry points' 32 bits, to which ctypes would cut it silently."""
+    if not -0x80000000 <= n <= 0x7FFFFFFF:
+        raise ValueError("%d does not fit 32 bits" % n)
+    return n
+
+
 def _row_count(shape):
-    if len(shape) == 2:
-        return shape[0]
     n = 1
     for s in shape[:-1]:
         n *= s
-    return n
+    return _size(n)
 
 
 def _gain(weight, H, dtype, dev):
@@ -769,7 +774,7 @@ def maxsim_rmsnorm_fwd(x, weight=None, eps=1e-6, residual=None, out_dtype=None, 
 @_on_its_device
 def _rmsnorm_fwd(x, weight, eps, residual, out_dtype, with_rstd, y, scale, sum, rstd):
     dev, shape, dtype = x.device, x.shape, x.dtype
-    H, R = shape[-1], _row_count(shape)
+    H, R = _size(shape[-1]), _row_count(shape)
     code = _code(dtype, _FLOATS, "x")
     out_dtype = dtype if out_dtype is None else out_dtype
     out = _code(out_dtype, _ALL, "out_dtype")
@@ -833,7 +838,7 @@ def maxsim_rmsnorm_bwd(dy, h, rstd, weight=None, dsum=None, with_dweight=True, d
 @_on_its_device
 def _rmsnorm_bwd(dy, h, rstd, weight, dsum, with_dweight, dx, dweight, workspace):
     dev, shape, dtype = h.device, h.shape, h.dtype
-    H, R = shape[-1], _row_count(shape)
+    H, R = _size(shape[-1]), _row_count(shape)
     code = _code(dtype, _FLOATS, "h")
     ldh = _rows(h, "h", shape, dtype, dev)
     lddy = _rows(dy, "dy", shape, dtype, dev)
@@ -882,7 +887,7 @@ def _quant_fp8(x, block_rows, rows, transposed):
     if x.dim() != 2:
         raise ValueError("x must be [R, C]")
     dev = x.device
-    R, C = x.shape
+    R, C = map(_size, x.shape)
     code = _code(x.dtype, _FLOATS, "x")
     ldx = _rows(x, "x", x.shape, x.dtype, dev)
     if not rows and not transposed:
@@ -938,8 +943,8 @@ def _gemm_fp8(A, a_scale, B, b_scale, out_dtype, out, workspace):
     dev = A.device
     if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
         raise ValueError("A [M, K] and B [N, K] must share K")
-    M, K = A.shape
-    N = B.shape[0]
+    M, K = map(_size, A.shape)
+    N = _size(B.shape[0])
     lda, ldb = _operand(A, "A", dev), _operand(B, "B", dev)
     kb = -(-K // QBLOCK)
     _flat(a_scale, "a_scale", M * kb, torch.float32, dev)
@@ -1069,6 +1074,7 @@ def _adamw(tensors, grads, step, lr, beta1, beta2, eps, weight_decay, step_dev):
             raise ValueError("gradients must be contiguous, of one type, on %s and of their parameters' sizes" % dev)
     if step_dev is not None:
         _flat(step_dev, "step_dev", 1, torch.int32, dev)
+    _size(step)
     table = tensors._table.copy()
     table["grad"] = [g.data_ptr() for g in grads]
     st = _lib.maxsim_adamw(table.ctypes.data, len(grads), tensors.param_code, code, tensors.state_code, lr, beta1,

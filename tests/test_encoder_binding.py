@@ -177,3 +177,28 @@ def test_a_copied_optimiser_table_is_one_of_its_own(state, how):
     assert other.sizes == tab.sizes and (other.state_code, other.param_code) == (tab.state_code, tab.param_code)
     for a, b in zip(other._held, tab._held):
         assert a.dtype == b.dtype and torch.equal(a.float(), b.float())
+
+
+def test_sizes_past_32_bits_are_refused():
+    """2^32 + 5 rows would be 5 of them in the C call.  (Tensors without memory: the refusal comes before any use.)"""
+    big = (1 << 32) + 5
+    empty = lambda *shape, dtype=torch.bfloat16: torch.empty(shape, dtype=dtype, device="meta")  # noqa: E731
+    e4m3 = torch.float8_e4m3fn
+    x, wide = empty(big, 16), empty(2, big)
+    q, few = empty(big, 16, dtype=e4m3), empty(4, 16, dtype=e4m3)
+    one = empty(1, 1, dtype=torch.float32)
+    raw = {n: getattr(bd, n).__wrapped__ for n in ("_rmsnorm_fwd", "_rmsnorm_bwd", "_quant_fp8", "_gemm_fp8")}
+    for t in (x, wide):
+        calls = [lambda: raw["_rmsnorm_fwd"](t, None, 1e-6, None, None, False, None, None, None, None),
+                 lambda: raw["_rmsnorm_bwd"](t, t, t, None, None, False, None, None, None),
+                 lambda: raw["_quant_fp8"](t, 1, True, False)]
+        for call in calls:
+            with pytest.raises(ValueError, match="32 bits"):
+                call()
+    for a, b in ((q, few), (few, q), (empty(4, big, dtype=e4m3), empty(4, big, dtype=e4m3))):
+        with pytest.raises(ValueError, match="32 bits"):
+            raw["_gemm_fp8"](a, one, b, one, torch.bfloat16, None, None)
+    tab = bd.AdamWTensors.zeros([torch.zeros(5)])
+    for step in (big, -big):
+        with pytest.raises(ValueError, match="32 bits"):
+            bd._adamw.__wrapped__(tab, [torch.zeros(5)], step, 1e-3, 0.9, 0.99, 1e-8, 0.0, None)
