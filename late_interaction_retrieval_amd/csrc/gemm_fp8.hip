@@ -19,7 +19,7 @@
 //     straight to registers and a workgroup's waves split K.
 //
 // Measured (bf16 results, scales of 128 x 128 for B): 16384 x 8192 x 4096
-// 505-547 us, 2.0-2.2 PFLOP/s; the matrix pipes are busy 54 % of the cycles at
+// 505-553 us, 2.0-2.2 PFLOP/s; the matrix pipes are busy 54 % of the cycles at
 // the 1.9 GHz that the card holds under this load, and what they wait for is
 // the scaling (16 multiply-adds beside two MFMAs of 64 cycles), the issue of
 // the direct loads, and 9 us a tile before its first product and after its last.

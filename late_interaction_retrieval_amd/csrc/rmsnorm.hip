@@ -12,10 +12,11 @@
 // an e4m3 block's scale is a 16-lane maximum.
 //
 // Measured (bf16, the times of the kernels alone): forward 32768 x 2048 with a
-// residual, its sum and e4m3 out 95 us, 472 MB at 5.0 TB/s; backward 16384 x
+// residual, its sum and e4m3 out 92-100 us, 472 MB at 4.7-5.1 TB/s; backward 16384 x
 // 2048 with a gradient of the sum 54 us + 5 us for the gains, 268 MB at 4.6
-// TB/s; a copy of 1 GiB reaches 5.2.  32 x 128 fp32 to int8 2.8 us, 1003 x 769
-// fp16 backward 7.5 us: launches and the chain load, sum, store.
+// TB/s; a copy of 1 GiB reaches 5.2.  32 x 128 fp32 to int8 2.7 us, a launch.  1003 x 769
+// fp16 backward 7.7 us, inputs in cache 6.1: dx alone is 4.1 there, as for 64 rows, the rest
+// the dweight workgroups' way over the rows.
 #include <algorithm>
 #include <type_traits>
 
