@@ -61,7 +61,8 @@ enum { MAXSIM_F32 = 2, MAXSIM_I8 = 3, MAXSIM_E4M3 = 4 };
  *   y         [R, H] of out_dtype, pitch ldy:
  *               F16, BF16, F32: rounded to nearest;
  *               I8:   one scale per row, scale [R] -- the operand and scales of
- *                     maxsim_fwd_i8 when H = 128;
+ *                     maxsim_fwd_i8 when H = 128 (which takes finite scales only: not
+ *                     a row whose values were not finite);
  *               E4M3: one scale per 128 columns, scale [R, ceil(H/128)] -- the
  *                     operand of maxsim_gemm_fp8 (ldy a multiple of 16 there).
  *   scale     fp32 out for I8 and E4M3, NULL otherwise

@@ -1174,7 +1174,8 @@ def encode_tokens(hidden, gain, proj, proj_scale, residual=None, out_dtype=torch
     """Token rows for the MaxSim entry points from an encoder's last hidden rows [..., H]: their RMS norm (of
     hidden + residual where one is given) in 8 bits, the projection to 128 columns, and rows of length 1 --
     (rows int8 [..., 128], scale [...]) for maxsim_fwd_i8, or (rows fp16 / bf16, None) for the other forwards.
-    proj [128, H] and proj_scale: maxsim_quant_fp8(weight, block_rows=128)."""
+    proj [128, H] and proj_scale: maxsim_quant_fp8(weight, block_rows=128).  hidden has to be finite: the forwards take
+    no NaN."""
     if proj.shape[0] != QBLOCK:
         raise ValueError("proj must have 128 rows, got %d" % proj.shape[0])
     q, s, _, _ = maxsim_rmsnorm_fwd(hidden, gain, eps, residual=residual, out_dtype=torch.float8_e4m3fn)
