@@ -34,7 +34,7 @@ MAXSIM_I8 = 3
 MAXSIM_E4M3 = 4
 QBLOCK = 128  # values that share a scale
 
-# name -> (restype, argtypes); must match include/maxsim.h and include/maxsim_encoder.h
+# name -> (restype, argtypes); must match include/maxsim.h, maxsim_encoder.h and maxsim_layers.h
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
 _I64 = ctypes.c_int64
@@ -80,6 +80,14 @@ SIGNATURES = {
     "maxsim_gemm_fp8": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _P, _I32, _I32, _I32, _I32, _I32, _P, _I64, _P,
                                        ctypes.c_size_t, _P]),
     "maxsim_adamw": (ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _F64, _F64, _F64, _F64, _F64, _I32, _P, _P]),
+    "maxsim_rope": (ctypes.c_int, [_P, _P, _I32, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _F32, _I32, _P]),
+    "maxsim_attn_fwd_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "maxsim_attn_bwd_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "maxsim_attn_fwd": (ctypes.c_int, [_P, _P, _P, ctypes.c_size_t, _P]),
+    "maxsim_attn_bwd": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "maxsim_distill_workspace_bytes": (ctypes.c_size_t, [_I32, _I32]),
+    "maxsim_distill_fwd": (ctypes.c_int, [_P, _I64, _P, _P, _I32, _I32, _I32, _I32, _F32, _P, _P, _P, ctypes.c_size_t, _P]),
+    "maxsim_distill_bwd": (ctypes.c_int, [_P, _P, _I64, _P, _P, _P, _I32, _I32, _I32, _I32, _F32, _P, _I64, _P]),
 }
 
 
@@ -1188,3 +1196,377 @@ def encode_tokens(hidden, gain, proj, proj_scale, residual=None, out_dtype=torch
     rows, scale, _, _ = maxsim_rmsnorm_fwd(rows, gain1, 1e-12, out_dtype=out_dtype)
     shape = hidden.shape[:-1]
     return rows.reshape(shape + (QBLOCK,)), None if scale is None else scale.reshape(shape)
+
+
+# ---------------------------------------------------------------- the attention layer's operators and the distillation loss
+# (include/maxsim_layers.h)
+
+
+class _View(ctypes.Structure):
+    _fields_ = [("data", _P), ("batch", _I64), ("token", _I64), ("head", _I64)]
+
+
+class _Attn(ctypes.Structure):
+    _fields_ = [("q", _View), ("k", _View), ("v", _View), ("out", _View), ("cu_q", _P), ("cu_k", _P), ("q_lens", _P),
+                ("k_lens", _P), ("rows_q", _I64), ("rows_k", _I64), ("B", _I32), ("max_q", _I32), ("max_k", _I32),
+                ("Hq", _I32), ("Hk", _I32), ("D", _I32), ("dtype", _I32), ("left", _I32), ("right", _I32), ("sinks", _I32),
+                ("zero_rest", _I32), ("scale", _F32), ("lse_step", _I32)]
+
+
+_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def _view(t, name, shape, dtype, dev):
+    """t [..., heads, width] of `shape`, `dtype` and device, as a view; steps along dimensions of one row are the widths."""
+    if t.device != dev:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    steps, sizes = t.stride(), t.shape
+    width = sizes[-1]
+    if steps[-1] != 1 and width > 1:
+        raise ValueError("%s: the values of a row must be neighbours" % name)
+    head = steps[-2] if sizes[-2] > 1 else width
+    token = steps[-3] if sizes[-3] > 1 else width * sizes[-2]
+    batch = steps[0] if len(sizes) == 4 and sizes[0] > 1 else 0
+    return _View(t.data_ptr(), batch, token, head)
+
+
+def rope_frequencies(rotary, base=10000.0, stretch=1.0, kind="parts", length=4096, fast=32.0, slow=1.0, device="cuda"):
+    """(inv_freq [rotary / 2] fp64, scale) for rope: base^(-2 i / rotary), stretched for contexts `stretch` times as long as
+    the `length` that the weights were trained on.  kind "linear": every frequency is divided by stretch; "base": the base
+    grows so that the slowest is; "parts": pairs that make fewer than `slow` turns over `length` are divided, those
+    with more than `fast` stay, and those between are mixed, with scale 1 + 0.1 ln(stretch)."""
+    if rotary < 2 or rotary % 2:
+        raise ValueError("rotary must be even, got %d" % rotary)
+    if kind not in ("linear", "base", "parts"):
+        raise ValueError("kind must be linear, base or parts, got %r" % (kind,))
+    if not (stretch >= 1.0 and base > 0.0 and fast > slow):
+        raise ValueError("stretch must be at least 1, base positive and fast above slow")
+    i = np.arange(rotary // 2, dtype=np.float64)
+    scale = 1.0
+    if kind == "base" and rotary > 2:
+        base = base * stretch ** (rotary / (rotary - 2))
+    f = base ** (-2.0 * i / rotary)
+    if kind == "linear" or (kind == "base" and rotary == 2):
+        f = f / stretch
+    elif kind == "parts" and stretch > 1.0:
+        part = np.clip((fast - length * f / (2 * np.pi)) / (fast - slow), 0.0, 1.0)  # of the divided frequency
+        f = f * (1.0 - part + part / stretch)
+        scale = 1.0 + 0.1 * float(np.log(stretch))
+    return torch.from_numpy(f).to(device), scale
+
+
+def maxsim_rope(x, inv_freq, positions=None, offsets=None, layout="half", scale=1.0, inverse=False, out=None, stream=None):
+    """Rotary positions: pair i of the first 2 * len(inv_freq) columns of each head of x [B, L, H, D] or [T, H, D] (fp16,
+    bf16, fp32) turned by position * inv_freq[i] and multiplied by scale; the other columns are copied.
+
+    layout "half": columns (i, i + rotary / 2) are a pair; "interleaved": (2i, 2i + 1).  positions [B, L] or [T] int32; or
+    offsets [B] int32, the position of each sequence's first token; or neither: from 0 on.  inverse: turned back (the
+    gradient of x from that of the result).  out may be x.  Returns out.
+    """
+    return _rope(x, inv_freq, positions, offsets, layout, scale, inverse, out, stream=stream)
+
+
+@_on_its_device
+def _rope(x, inv_freq, positions, offsets, layout, scale, inverse, out):
+    dev, shape = x.device, x.shape
+    if x.dim() not in (3, 4):
+        raise ValueError("x must be [B, L, H, D] or [T, H, D]")
+    if layout not in _LAYOUTS:
+        raise ValueError("layout must be half or interleaved, got %r" % (layout,))
+    code = _code(x.dtype, _FLOATS, "x")
+    B, L = (shape[0], shape[1]) if x.dim() == 4 else (1, shape[0])
+    H, D = map(_size, shape[-2:])
+    rotary = 2 * inv_freq.numel()
+    _flat(inv_freq, "inv_freq", rotary // 2, torch.float64, dev)
+    if positions is not None:
+        _flat(positions, "positions", B * L, torch.int32, dev)
+    if offsets is not None:
+        _flat(offsets, "offsets", B, torch.int32, dev)
+    xv = _view(x, "x", shape, x.dtype, dev)
+    if out is None:
+        out = x.new_empty(shape)
+    ov = xv if out is x else _view(out, "out", shape, x.dtype, dev)
+    st = _lib.maxsim_rope(ctypes.byref(xv), ctypes.byref(ov), _size(B), _size(L), H, D, rotary, _LAYOUTS[layout], code,
+                          inv_freq.data_ptr(), None if positions is None else positions.data_ptr(),
+                          None if offsets is None else offsets.data_ptr(), scale, inverse, _raw_stream(dev))
+    if st:
+        _check(st, "maxsim_rope")
+    return out
+
+
+class RopeFunction(torch.autograd.Function):
+    """Rotary positions as an autograd op: the gradient is turned back."""
+
+    @staticmethod
+    def forward(ctx, x, inv_freq, positions, offsets, layout, scale):
+        ctx.save_for_backward(inv_freq, positions, offsets)
+        ctx.how = layout, scale
+        return maxsim_rope(x, inv_freq, positions, offsets, layout, scale)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        inv_freq, positions, offsets = ctx.saved_tensors
+        layout, scale = ctx.how
+        if dy.stride(-1) != 1:
+            dy = dy.contiguous()
+        return maxsim_rope(dy, inv_freq, positions, offsets, layout, scale, inverse=True), None, None, None, None, None
+
+
+def rope(x, inv_freq, positions=None, offsets=None, layout="half", scale=1.0):
+    """maxsim_rope with autograd support (of x)."""
+    return RopeFunction.apply(x, inv_freq, positions, offsets, layout, scale)
+
+
+def _lengths(t, name, n, dev):
+    if t is None:
+        return None
+    _flat(t, name, n, torch.int32, dev)
+    return t.data_ptr()
+
+
+def _attn(q, k, v, out, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k):
+    """The call's struct; q [B, Lq, Hq, D] (or packed [Tq, Hq, D] with cu_q and max_q), k and v likewise."""
+    dev, dtype = q.device, q.dtype
+    a = _Attn()
+    a.dtype = _code(dtype, (MAXSIM_F16, MAXSIM_BF16), "q")
+    for t, name, cu, most in ((q, "q", cu_q, max_q), (k, "k", cu_k, max_k)):
+        if t.dim() != (4 if cu is None else 3):
+            raise ValueError("%s must be [B, L, H, D], or packed [T, H, D] with cu_%s" % (name, name))
+        if cu is not None and most is None:
+            raise ValueError("max_%s goes with cu_%s" % (name, name))
+    if q_lens is not None and cu_q is not None or k_lens is not None and cu_k is not None:
+        raise ValueError("lengths go with padded sequences, cu_q and cu_k with packed ones")
+    a.B = _size(q.shape[0] if cu_q is None else cu_q.numel() - 1)
+    if a.B != (k.shape[0] if cu_k is None else cu_k.numel() - 1) or a.B < 0:
+        raise ValueError("q and k must have as many sequences")
+    if k.shape[-1] != q.shape[-1]:
+        raise ValueError("q and k must share the width")
+    a.q, a.k, a.v = _view(q, "q", q.shape, dtype, dev), _view(k, "k", k.shape, dtype, dev), _view(v, "v", k.shape, dtype, dev)
+    if out is not None:
+        a.out = _view(out, "out", q.shape, dtype, dev)
+    a.cu_q, a.cu_k = _lengths(cu_q, "cu_q", a.B + 1, dev), _lengths(cu_k, "cu_k", a.B + 1, dev)
+    a.q_lens, a.k_lens = _lengths(q_lens, "q_lens", a.B, dev), _lengths(k_lens, "k_lens", a.B, dev)
+    a.rows_q, a.rows_k = (0 if cu_q is None else q.shape[0]), (0 if cu_k is None else k.shape[0])
+    a.max_q = _size(q.shape[1] if cu_q is None else int(max_q))
+    a.max_k = _size(k.shape[1] if cu_k is None else int(max_k))
+    a.Hq, a.Hk, a.D = map(_size, (q.shape[-2], k.shape[-2], q.shape[-1]))
+    a.left, a.right, a.sinks = _size(window[0]), _size(window[1]), _size(sinks)
+    a.scale = q.shape[-1] ** -0.5 if scale is None else scale
+    a.lse_step = 1
+    return a
+
+
+def _lse_step(lse, q):
+    """The step of lse, a number for each row of q: 1, or that of maxsim_attn_fwd's, behind whose numbers more is kept."""
+    if lse.device != q.device or lse.dtype != torch.float32 or lse.shape != q.shape[:-1]:
+        raise ValueError("lse must be %s float32 on %s" % (tuple(q.shape[:-1]), q.device))
+    if lse.is_contiguous() or lse.numel() == 0:
+        return 1
+    step = lse.stride(-1) if lse.shape[-1] > 1 else 1 + q.shape[-1] // 2
+    want = [step]
+    for n in reversed(lse.shape[1:]):
+        want.insert(0, want[0] * n)
+    end = lse.storage_offset() + lse.numel() * step
+    if step < 1 + q.shape[-1] // 2 or any(n > 1 and s != w for n, s, w in zip(lse.shape, lse.stride(), want)) or \
+            4 * end > lse.untyped_storage().nbytes():
+        raise ValueError("lse must be contiguous, or as maxsim_attn_fwd made it")
+    return step
+
+
+def _workspace(like, given, nbytes):
+    if given is not None:
+        _need(given, "workspace", device=like.device)
+        return given, given.numel() * given.element_size()
+    return (like.new_empty(nbytes, dtype=torch.uint8) if nbytes else None), nbytes
+
+
+def maxsim_attn_fwd(q, k, v, scale=None, window=(-1, -1), sinks=0, q_lens=None, k_lens=None, cu_q=None, cu_k=None,
+                    max_q=None, max_k=None, with_lse=False, out=None, lse=None, workspace=None, stream=None):
+    """Attention with a sliding window and first tokens that stay visible.
+
+    q [B, Lq, Hq, D], k and v [B, Lk, Hk, D] (fp16, bf16; D a multiple of 8 up to 128; Hq a multiple of Hk), with q_lens and
+    k_lens [B] int32 where sequences are shorter; or packed [T, H, D] with cu_q, cu_k [B + 1] int32 and bounds max_q,
+    max_k of the lengths.  Query i stands at p = i + Lk - Lq of its sequence and sees key j where j <= p + window[1] and
+    (j >= p - window[0] or j < sinks); -1 is no bound, so window (-1, 0) is causal.  scale: of q k, 1 / sqrt(D) if None.
+    Returns (out as q, lse [..., Hq] fp32 or None).  The lse made here is a view whose memory also keeps, for the backward,
+    what rounding left off out; a contiguous one does for it too, with a less exact rowsum(dO * out).  Rows of no sequence are zeros in outputs made here, and left as
+    they were in those that are given.
+    """
+    return _attn_fwd(q, k, v, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k, with_lse, out, lse, workspace,
+                     stream=stream)
+
+
+@_on_its_device
+def _attn_fwd(q, k, v, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k, with_lse, out, lse, workspace):
+    given = out is not None or lse is not None
+    rest = given and (out is None or (lse is None and with_lse))  # some made here, some given
+    make = torch.zeros if rest else torch.empty
+    if out is None:
+        out = make(q.shape, dtype=q.dtype, device=q.device)
+    a = _attn(q, k, v, out, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k)
+    if lse is not None:
+        _flat(lse, "lse", q.numel() // max(1, q.shape[-1]), torch.float32, q.device)
+    elif with_lse:
+        a.lse_step = 1 + q.shape[-1] // 2
+        lse = make(q.shape[:-1] + (a.lse_step,), dtype=torch.float32, device=q.device)[..., 0]
+    a.zero_rest = not given and (cu_q is not None or q_lens is not None)
+    if a.B == 0 and a.zero_rest:
+        out.zero_()
+    workspace, nbytes = _workspace(q, workspace, _lib.maxsim_attn_fwd_workspace_bytes(ctypes.byref(a)))
+    st = _lib.maxsim_attn_fwd(ctypes.byref(a), None if lse is None else lse.data_ptr(),
+                              None if workspace is None else workspace.data_ptr(), nbytes, _raw_stream(q.device))
+    if st:
+        _check(st, "maxsim_attn_fwd")
+    return out, lse
+
+
+def maxsim_attn_bwd(dout, q, k, v, out, lse, scale=None, window=(-1, -1), sinks=0, q_lens=None, k_lens=None, cu_q=None,
+                    cu_k=None, max_q=None, max_k=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """Backward of maxsim_attn_fwd, whose out and lse it takes with the same arguments.  Returns (dq, dk, dv); what queries
+    give to a shared head of k and v is summed in fp32.  Rows of no sequence are zeros in gradients made here, and left
+    as they were where all three are given."""
+    return _attn_bwd(dout, q, k, v, out, lse, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k, dq, dk, dv,
+                     workspace, stream=stream)
+
+
+@_on_its_device
+def _attn_bwd(dout, q, k, v, out, lse, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k, dq, dk, dv, workspace):
+    dev, dtype = q.device, q.dtype
+    a = _attn(q, k, v, out, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k)
+    given = [t is not None for t in (dq, dk, dv)]
+    make = torch.zeros if any(given) and not all(given) else torch.empty
+    dq, dk, dv = (make(t.shape, dtype=dtype, device=dev) if d is None else d for d, t in ((dq, q), (dk, k), (dv, v)))
+    a.zero_rest = not any(given) and any(t is not None for t in (cu_q, cu_k, q_lens, k_lens))
+    if a.B == 0 and a.zero_rest:
+        for t in (dq, dk, dv):
+            t.zero_()
+    a.lse_step = _lse_step(lse, q)
+    views = [_view(t, n, s.shape, dtype, dev) for t, n, s in ((dout, "dout", q), (dq, "dq", q), (dk, "dk", k), (dv, "dv", k))]
+    workspace, nbytes = _workspace(q, workspace, _lib.maxsim_attn_bwd_workspace_bytes(ctypes.byref(a)))
+    st = _lib.maxsim_attn_bwd(ctypes.byref(a), lse.data_ptr(), *[ctypes.byref(w) for w in views],
+                              None if workspace is None else workspace.data_ptr(), nbytes, _raw_stream(dev))
+    if st:
+        _check(st, "maxsim_attn_bwd")
+    return dq, dk, dv
+
+
+def _loadable(t):
+    """t itself where tiles of its rows can be loaded, or a copy."""
+    steps = t.stride()
+    ok = steps[-1] == 1 and t.data_ptr() % 16 == 0 and all(s % 8 == 0 for s in steps[:-1]) and \
+        (t.shape[-3] <= 1 or t.shape[-1] <= steps[-3] <= 1 << 20)
+    return t if ok else t.contiguous()
+
+
+class AttentionFunction(torch.autograd.Function):
+    """Attention as an autograd op: of the forward only the output and a number for each row are kept."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, cu_q, cu_k, q_lens, k_lens, how):
+        q, k, v = _loadable(q), _loadable(k), _loadable(v)
+        lengths = dict(cu_q=cu_q, cu_k=cu_k, q_lens=q_lens, k_lens=k_lens)
+        out, lse = maxsim_attn_fwd(q, k, v, with_lse=any(ctx.needs_input_grad[:3]), **lengths, **how)
+        ctx.save_for_backward(q, k, v, out, lse, cu_q, cu_k, q_lens, k_lens)
+        ctx.how = how
+        return out
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        q, k, v, out, lse, cu_q, cu_k, q_lens, k_lens = ctx.saved_tensors
+        grads = maxsim_attn_bwd(_loadable(dout), q, k, v, out, lse, cu_q=cu_q, cu_k=cu_k, q_lens=q_lens, k_lens=k_lens, **ctx.how)
+        return tuple(g if need else None for g, need in zip(grads, ctx.needs_input_grad)) + (None,) * 5
+
+
+def attention(q, k, v, scale=None, window=(-1, -1), sinks=0, q_lens=None, k_lens=None, cu_q=None, cu_k=None, max_q=None,
+              max_k=None):
+    """maxsim_attn_fwd's output with autograd support (of q, k and v, which may be views of any layout)."""
+    return AttentionFunction.apply(q, k, v, cu_q, cu_k, q_lens, k_lens,
+                                   dict(scale=scale, window=window, sinks=sinks, max_q=max_q, max_k=max_k))
+
+
+def maxsim_distill_fwd(scores, index, teacher, temperature=1.0, loss=None, stat=None, workspace=None, stream=None):
+    """A loss for each row of scores [N, V] (fp16, bf16, fp32) from a teacher's top scores: with
+    q = softmax(teacher / T) over the row's entries and p = softmax(scores / T) over its columns,
+    T^2 sum_k q_k (log q_k - log p[index_k]).  index [N, K] int32 (an index outside [0, V) is no entry), teacher [N, K]
+    fp32, K <= 1024.  Returns (loss [N], stat [N, 2]) fp32; the backward takes stat."""
+    return _distill_fwd(scores, index, teacher, temperature, loss, stat, workspace, stream=stream)
+
+
+def _distill_sizes(scores, index, teacher):
+    if scores.dim() != 2 or index.dim() != 2:
+        raise ValueError("scores must be [N, V] and index [N, K]")
+    (N, V), K, dev = map(_size, scores.shape), _size(index.shape[1]), scores.device
+    _flat(index, "index", N * K, torch.int32, dev)
+    _flat(teacher, "teacher", N * K, torch.float32, dev)
+    return N, V, K, _code(scores.dtype, _FLOATS, "scores"), _rows(scores, "scores", scores.shape, scores.dtype, dev)
+
+
+@_on_its_device
+def _distill_fwd(scores, index, teacher, temperature, loss, stat, workspace):
+    dev = scores.device
+    N, V, K, code, ld = _distill_sizes(scores, index, teacher)
+    if loss is None:
+        loss = scores.new_empty(N, dtype=torch.float32)
+    if stat is None:
+        stat = scores.new_empty((N, 2), dtype=torch.float32)
+    _flat(loss, "loss", N, torch.float32, dev)
+    _flat(stat, "stat", 2 * N, torch.float32, dev)
+    workspace, nbytes = _workspace(scores, workspace, _lib.maxsim_distill_workspace_bytes(N, V))
+    st = _lib.maxsim_distill_fwd(scores.data_ptr(), ld, index.data_ptr(), teacher.data_ptr(), N, V, K, code, temperature,
+                                 loss.data_ptr(), stat.data_ptr(), None if workspace is None else workspace.data_ptr(),
+                                 nbytes, _raw_stream(dev))
+    if st:
+        _check(st, "maxsim_distill_fwd")
+    return loss, stat
+
+
+def maxsim_distill_bwd(dloss, scores, stat, index, teacher, temperature=1.0, dscores=None, stream=None):
+    """The gradient of scores from that of the rows' losses, dloss [N] fp32, with maxsim_distill_fwd's stat:
+    dloss T (p - the entries' q).  dscores may be scores.  Returns dscores [N, V] of scores' type."""
+    return _distill_bwd(dloss, scores, stat, index, teacher, temperature, dscores, stream=stream)
+
+
+@_on_its_device
+def _distill_bwd(dloss, scores, stat, index, teacher, temperature, dscores):
+    dev = scores.device
+    N, V, K, code, ld = _distill_sizes(scores, index, teacher)
+    _flat(dloss, "dloss", N, torch.float32, dev)
+    _flat(stat, "stat", 2 * N, torch.float32, dev)
+    ldd = V
+    if dscores is None:
+        dscores = scores.new_empty((N, V))
+    else:
+        ldd = _rows(dscores, "dscores", scores.shape, scores.dtype, dev)
+    st = _lib.maxsim_distill_bwd(dloss.data_ptr(), scores.data_ptr(), ld, stat.data_ptr(), index.data_ptr(),
+                                 teacher.data_ptr(), N, V, K, code, temperature, dscores.data_ptr(), ldd, _raw_stream(dev))
+    if st:
+        _check(st, "maxsim_distill_bwd")
+    return dscores
+
+
+class DistillFunction(torch.autograd.Function):
+    """The distillation loss of each row as an autograd op (of the scores)."""
+
+    @staticmethod
+    def forward(ctx, scores, index, teacher, temperature):
+        loss, stat = maxsim_distill_fwd(scores, index, teacher, temperature)
+        ctx.save_for_backward(scores, stat, index, teacher)
+        ctx.temperature = temperature
+        return loss
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss):
+        scores, stat, index, teacher = ctx.saved_tensors
+        return maxsim_distill_bwd(dloss.contiguous(), scores, stat, index, teacher, ctx.temperature), None, None, None
+
+
+def distill_loss(scores, index, teacher, temperature=1.0):
+    """maxsim_distill_fwd's loss [N] with autograd support (of scores, MaxSim's [Nq, B] among them)."""
+    return DistillFunction.apply(scores.contiguous(), index.contiguous(), teacher.contiguous(), temperature)

@@ -16,7 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmaxsim.so")
 FAST = os.path.join(HERE, "_fast.so")
 SOURCES = ["fwd.hip", "bwd.hip", "topk.hip", "ooc.hip", "chamfer.hip", "noalloc.hip", "capi.cpp",
-           "rmsnorm.hip", "quant.hip", "gemm_fp8.hip", "adamw.hip", "capi_encoder.cpp"]
+           "rmsnorm.hip", "quant.hip", "gemm_fp8.hip", "adamw.hip", "capi_encoder.cpp",
+           "rope.hip", "attn_fwd.hip", "attn_bwd.hip", "distill.hip", "capi_layers.cpp"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
@@ -29,10 +30,12 @@ HIPCC_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wno-unused-command-line-argument",
 ]
-# inputs are finite: max needs no NaN canonicalisation (infinities are kept)
+# inputs are finite: max needs no NaN canonicalisation (infinities are kept).  Attention's files, which take these
+# flags too, test sums of exponentials by their bits, so that a NaN there still reaches the output.
 FINITE_FLAGS = ["-fno-honor-nans"]
 # these pass NaN and infinity through as their formulas give them, or refuse them
-SOURCE_FLAGS = {s: [] for s in ("rmsnorm.hip", "quant.hip", "gemm_fp8.hip", "adamw.hip", "capi_encoder.cpp")}
+SOURCE_FLAGS = {s: [] for s in ("rmsnorm.hip", "quant.hip", "gemm_fp8.hip", "adamw.hip", "capi_encoder.cpp",
+                                   "rope.hip", "distill.hip", "capi_layers.cpp")}
 
 
 def hipcc():

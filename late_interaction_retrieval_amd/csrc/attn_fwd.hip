@@ -1,0 +1,443 @@
+// attn_fwd.hip -- attention with a sliding window and first tokens that stay
+// visible, forward, for gfx950 (MI355X).
+//
+//     S = scale q k^T over the keys a query sees;  P = softmax(S);  out = P v;  lse = log sum exp S
+//
+// One pass over the keys with the running maximum and sum.  The products run with the
+// queries as columns: S^T = K Q^T leaves a query's scores in one lane pair, so its maximum
+// and sum need one exchange between lanes and the factors of a new maximum are the lane's own; P^T goes
+// from the registers it was made in to out^T = V^T P^T as it stands.
+#include <algorithm>
+
+#include "attn_dev.h"
+
+namespace maxsim {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kRowsWave = 32;                  // rows (a token's query head each) of a wave
+constexpr int kRows = kWaves * kRowsWave;      // of a workgroup
+constexpr int kKeys = 64;                      // of a tile
+constexpr int kKeysFew = 32;                   // of a wave's own tile, with few rows
+
+// A wave's state for its 32 rows: out^T and, for the lane's row, the reference of the exponents in
+// units of the scores and the sum of this lane's keys.
+template <typename T, int DP>
+struct Rows {
+    static constexpr int KS = DP / 16, DB = DP / 32;
+    typename Vec8<T>::V q[KS];
+    f32x16 o[DB];
+    float ref, sum;
+    int lo, hi;  // the lane's row sees keys [lo, hi] (and those below `sinks` that are at most hi)
+
+    __device__ __forceinline__ void start(const T* row, int lane, int D, int pos, int lk, const maxsim_attn& a) {
+#pragma unroll
+        for (int kk = 0; kk < KS; ++kk) q[kk] = row8<T>(row, 16 * kk + 8 * (lane >> 5), D);
+#pragma unroll
+        for (int db = 0; db < DB; ++db) o[db] = zero16();
+        ref = -INFINITY;
+        sum = 0.f;
+        lo = pos - a.left;
+        hi = min(pos + a.right, lk - 1);
+    }
+
+    // NB blocks of 32 keys from key j0 on; those from `end` on are no keys.  whole: all of them are seen by all rows.
+    // The reference stays while the maximum passes it by less than 2^8: P grows to 256 at most, which both types hold,
+    // and relative to the row's sum nothing is lost.
+    template <int NB>
+    __device__ __forceinline__ void step(const uint8_t* kt, const uint8_t* vt, int lane, int j0, int end, bool whole, int sinks,
+                                         float c, float slack) {
+        f32x16 s[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+            s[nb] = zero16();
+#pragma unroll
+            for (int kk = 0; kk < KS; ++kk) s[nb] = mma<T>(rows_at<T, DP>(kt + nb * 32 * Tile<DP>::ROW, lane, kk), q[kk], s[nb]);
+        }
+        if (!whole) {
+            const int j = j0 + 4 * (lane >> 5);
+            const int top = min(hi, end - 1) - j, low = lo - j, sink = sinks - j;
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int at = 32 * nb + slot(i);
+                    s[nb][i] = at <= top && (at >= low || at < sink) ? s[nb][i] : -INFINITY;
+                }
+        }
+        float m = s[0][0];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m = fmaxf(m, s[nb][i]);
+        m = swap_max(m);
+        if (__any(m > ref + slack)) {  // -infinity + slack is -infinity
+            const float now = fmaxf(ref, m);
+            const float f = ref == now ? 1.f : __builtin_amdgcn_exp2f((ref - now) * c);
+            ref = now;
+            sum *= f;
+#pragma unroll
+            for (int db = 0; db < DB; ++db)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[db][i] *= f;
+        }
+        const float base = ref == -INFINITY ? 0.f : -ref * c;  // a row that has seen nothing yet
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[nb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nb][i], c, base));
+                sum += s[nb][i];
+            }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const typename Vec8<T>::V p = pack8<T>(s[nb], 8 * t);
+#pragma unroll
+                for (int db = 0; db < DB; ++db) o[db] = mma<T>(cols_at<T, DP>(vt, lane, 2 * nb + t, db), p, o[db]);
+            }
+    }
+};
+
+// What a workgroup works on.
+struct Item {
+    int b, h, split, tile;  // sequence, key head
+};
+__device__ __forceinline__ Item item_of(int id, int tiles, int splits, int heads) {
+    Item w;
+    w.tile = tiles - 1 - id % tiles;  // with a causal bound the last rows see the most keys: first
+    id /= tiles;
+    w.split = id % splits;
+    id /= splits;
+    w.h = id % heads;
+    w.b = id / heads;
+    return w;
+}
+
+// Row r of a sequence and key head: query token r / group, head r % group of those that share the key head.
+template <typename TT, int DP>
+__global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnArgs p, int tiles) {
+    typedef typename TT::type T;
+    typedef Rows<T, DP> R;
+    constexpr int BYTES = kKeys * Tile<DP>::ROW;
+    // separate arrays: the compiler then sees that a tile's reads and the next one's loads touch different memory
+    __shared__ __align__(16) uint8_t k_0[BYTES], v_0[BYTES], k_1[BYTES], v_1[BYTES];
+    const maxsim_attn& a = p.a;
+    const int id = item_of_block();
+    const Item w = item_of(id, tiles, p.splits, a.Hk);
+    const Seq s = sequence(a, w.b);
+    const int G = p.group, D = a.D, rows = s.lq * G;
+    if (a.zero_rest && p.splits == 1)
+        zero_rest<T>(a.out, p.lse, a.lse_step, a.cu_q, a.B, a.rows_q, w.b, s.q0, s.lq, s.all_q, a.Hq, D, w.h * tiles + w.tile,
+                     a.Hk * tiles, id, (int)gridDim.x);
+    const int r0 = w.tile * kRows;
+    if (r0 >= rows) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int shift = s.lk - s.lq;
+    const int last = min(r0 + kRows, rows) - 1;
+    const Span span = span_of(a, s.lk, r0 / G + shift, last / G + shift, kKeys);
+    const int t0 = (int)((int64_t)span.tiles * w.split / p.splits), t1 = (int)((int64_t)span.tiles * (w.split + 1) / p.splits);
+
+    const int wr = r0 + wave * kRowsWave;
+    const int r = min(wr + (lane & 31), rows - 1), token = r / G, head = w.h * G + r % G;
+    const T* qs = first<T>(a.q, a.cu_q != nullptr, w.b, s.q0, 0);
+    R row;
+    row.start(qs + (int64_t)token * a.q.token + (int64_t)head * a.q.head, lane, D, token + shift, s.lk, a);
+    // the wave's rows: the positions between which they lie
+    const int p_lo = min(wr, rows - 1) / G + shift, p_hi = min(wr + kRowsWave - 1, rows - 1) / G + shift;
+    const float c = a.scale * kLog2e, slack = 8.f / c;
+
+    const T* ks = first<T>(a.k, a.cu_k != nullptr, w.b, s.k0, w.h);
+    const T* vs = first<T>(a.v, a.cu_k != nullptr, w.b, s.k0, w.h);
+    Loader<DP, kKeys, kWaves> lk, lv;
+    lk.init(wave, lane, a.k.token, D);
+    lv.init(wave, lane, a.v.token, D);
+    const auto load = [&](int t, uint8_t* kt, uint8_t* vt) {
+        const int j = span.at(t, kKeys);
+        lk.load(ks + (int64_t)j * a.k.token, s.lk - j, a.k.token, D, kt, wave);
+        lv.load(vs + (int64_t)j * a.v.token, s.lk - j, a.v.token, D, vt, wave);
+    };
+    const auto work = [&](int t, const uint8_t* kt, const uint8_t* vt) {
+        const int j = span.at(t, kKeys), end = span.end(t), j_last = j + kKeys - 1;
+        if (wr >= rows || j > p_hi + a.right || (j_last < p_lo - a.left && j >= a.sinks)) return;  // nothing to see
+        const bool whole = j_last < end && j_last <= min(p_lo + a.right, s.lk - 1) && (j >= p_hi - a.left || j_last < a.sinks);
+        row.template step<kKeys / 32>(kt, vt, lane, j, end, whole, a.sinks, c, slack);
+    };
+    if (t0 < t1) load(t0, k_0, v_0);
+    for (int t = t0; t < t1; t += 2) {
+        tile_ready();
+        if (t + 1 < t1) load(t + 1, k_1, v_1);
+        work(t, k_0, v_0);
+        if (t + 1 >= t1) break;
+        tile_ready();
+        if (t + 2 < t1) load(t + 2, k_0, v_0);
+        work(t + 1, k_1, v_1);
+    }
+
+    const float sum = swap_sum(row.sum), top = row.ref == -INFINITY ? 0.f : row.ref * c;
+    const bool mine = wr + (lane & 31) < rows;
+    const int64_t at = (first_row(a, s, w.b) + token) * a.Hq + head;
+    if (p.splits == 1) {
+        T* out = first<T>(a.out, a.cu_q != nullptr, w.b, s.q0, 0) + (int64_t)token * a.out.token + (int64_t)head * a.out.head;
+        const float inv = is_zero(sum) ? 0.f : 1.f / sum;
+        store_row<T, R::DB>(out, mine, row.o, inv, lane, D);
+        if (p.lse && a.lse_step > 1) store_row<T, R::DB, true>(rest_of<T>(p, at), mine, row.o, inv, lane, D);
+        if (p.lse && mine && lane < 32)
+            p.lse[at * a.lse_step] = is_zero(sum) ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
+    } else if (mine) {
+        const int64_t part = (int64_t)w.split * p.rows * a.Hq + at;
+        if (lane < 32) {
+            p.part_ml[2 * part] = top;
+            p.part_ml[2 * part + 1] = sum;
+        }
+        float* o = p.part_o + part * D;
+#pragma unroll
+        for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int d = 32 * db + 8 * q + 4 * (lane >> 5);
+                if (d < D) {
+                    f32x4 v = {row.o[db][4 * q], row.o[db][4 * q + 1], row.o[db][4 * q + 2], row.o[db][4 * q + 3]};
+                    *reinterpret_cast<f32x4*>(o + d) = v;
+                }
+            }
+    }
+}
+
+// Few rows of a key head (32 at most: a sequence's next token, a short query): the four waves take the same rows
+// and every fourth tile of 32 keys each, in buffers of their own that no barrier orders; they are joined in LDS at the end.
+template <typename TT, int DP>
+__global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_few_kernel(AttnArgs p) {
+    typedef typename TT::type T;
+    typedef Rows<T, DP> R;
+    constexpr int BYTES = kKeysFew * Tile<DP>::ROW;
+    __shared__ __align__(16) uint8_t k_0[kWaves * BYTES], v_0[kWaves * BYTES], k_1[kWaves * BYTES], v_1[kWaves * BYTES];
+    __shared__ __align__(16) float joined[kWaves][32][2];
+    const maxsim_attn& a = p.a;
+    const int id = item_of_block();
+    const Item w = item_of(id, 1, p.splits, a.Hk);
+    const Seq s = sequence(a, w.b);
+    const int G = p.group, D = a.D, rows = s.lq * G;
+    if (a.zero_rest && p.splits == 1)
+        zero_rest<T>(a.out, p.lse, a.lse_step, a.cu_q, a.B, a.rows_q, w.b, s.q0, s.lq, s.all_q, a.Hq, D, w.h, a.Hk, id, (int)gridDim.x);
+    if (rows <= 0) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int shift = s.lk - s.lq;
+    const int p_lo = shift, p_hi = (rows - 1) / G + shift;
+    const Span span = span_of(a, s.lk, p_lo, p_hi, kKeysFew);
+    const int t0 = (int)((int64_t)span.tiles * w.split / p.splits), t1 = (int)((int64_t)span.tiles * (w.split + 1) / p.splits);
+    const int r = min(lane & 31, rows - 1), token = r / G, head = w.h * G + r % G;
+    R row;
+    row.start(first<T>(a.q, a.cu_q != nullptr, w.b, s.q0, 0) + (int64_t)token * a.q.token + (int64_t)head * a.q.head, lane, D,
+              token + shift, s.lk, a);
+    const float c = a.scale * kLog2e, slack = 8.f / c;
+    const T* ks = first<T>(a.k, a.cu_k != nullptr, w.b, s.k0, w.h);
+    const T* vs = first<T>(a.v, a.cu_k != nullptr, w.b, s.k0, w.h);
+    Loader<DP, kKeysFew, 1> lk, lv;
+    lk.init(0, lane, a.k.token, D);
+    lv.init(0, lane, a.v.token, D);
+    constexpr int LOADS = 2 * Loader<DP, kKeysFew, 1>::N;  // on their way for the next tile
+    const auto load = [&](int t, uint8_t* kt, uint8_t* vt) {
+        const int j = span.at(t, kKeysFew);
+        lk.load(ks + (int64_t)j * a.k.token, s.lk - j, a.k.token, D, kt + wave * BYTES, 0);
+        lv.load(vs + (int64_t)j * a.v.token, s.lk - j, a.v.token, D, vt + wave * BYTES, 0);
+    };
+    const auto work = [&](int t, const uint8_t* kt, const uint8_t* vt) {
+        const int j = span.at(t, kKeysFew), end = span.end(t), j_last = j + kKeysFew - 1;
+        const bool whole = j_last < end && j_last <= min(p_lo + a.right, s.lk - 1) && (j >= p_hi - a.left || j_last < a.sinks);
+        row.template step<1>(kt + wave * BYTES, vt + wave * BYTES, lane, j, end, whole, a.sinks, c, slack);
+    };
+    const auto landed = [&](bool ahead) {  // the tile's loads; those of the next one may stay on their way
+        asm volatile("" ::: "memory");
+        if (ahead) __builtin_amdgcn_s_waitcnt((LOADS & 15) | ((LOADS >> 4) << 14) | 0x0F70);
+        else __builtin_amdgcn_s_waitcnt(0x0F70);
+        asm volatile("" ::: "memory");
+    };
+    int t = t0 + wave;
+    if (t < t1) load(t, k_0, v_0);
+    for (; t < t1; t += 2 * kWaves) {
+        const bool one = t + kWaves < t1, two = t + 2 * kWaves < t1;
+        if (one) load(t + kWaves, k_1, v_1);
+        landed(one);
+        work(t, k_0, v_0);
+        if (!one) break;
+        if (two) load(t + 2 * kWaves, k_0, v_0);
+        landed(two);
+        work(t + kWaves, k_1, v_1);
+    }
+
+    // the waves' parts: references and sums first, then out^T, scaled to the largest reference, added in order
+    const float sum = swap_sum(row.sum), top = row.ref == -INFINITY ? -INFINITY : row.ref * c;
+    if (lane < 32) {
+        joined[wave][lane][0] = top;
+        joined[wave][lane][1] = sum;
+    }
+    __syncthreads();  // all tiles are read: their memory takes the parts
+    float most = -INFINITY, total = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) most = fmaxf(most, joined[i][lane & 31][0]);
+    const float f = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - most);
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i)
+        total += joined[i][lane & 31][0] == -INFINITY ? 0.f : joined[i][lane & 31][1] * __builtin_amdgcn_exp2f(joined[i][lane & 31][0] - most);
+    constexpr int BLOCK = 16 * 64 * 4;  // bytes of a block of 32 columns: register by register, 64 lanes each
+    static_assert(R::DB * BLOCK <= 2 * kWaves * BYTES, "a wave's part fits two arrays' share");
+    // wave i's part in array i
+    uint8_t* const mem = wave == 0 ? k_0 : wave == 1 ? v_0 : wave == 2 ? k_1 : v_1;
+    static_assert(R::DB * BLOCK <= kWaves * BYTES, "a wave's part fits an array");
+#pragma unroll
+    for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) reinterpret_cast<float*>(mem)[(db * 16 + i) * 64 + lane] = row.o[db][i] * f;
+    __syncthreads();
+    // each wave sums DB / 4 blocks: registers of 8 columns at a time are spread over the waves
+    const bool mine = (lane & 31) < rows;
+    const int64_t at = (first_row(a, s, w.b) + token) * a.Hq + head;
+    if (wave == 0 && mine && lane < 32) {
+        if (p.splits == 1) {
+            if (p.lse) p.lse[at * a.lse_step] = is_zero(total) ? -INFINITY : (most + __builtin_amdgcn_logf(total)) * kLn2;
+        } else {
+            const int64_t part = (int64_t)w.split * p.rows * a.Hq + at;
+            p.part_ml[2 * part] = most == -INFINITY ? 0.f : most;
+            p.part_ml[2 * part + 1] = total;
+        }
+    }
+    const float inv = is_zero(total) ? 0.f : 1.f / total;
+    for (int q = wave; q < R::DB * 4; q += kWaves) {  // 4 registers: columns 8 q + 4 (l / 32) on
+        f32x4 v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int e = (4 * q + i) * 64 + lane;
+            v[i] = ((reinterpret_cast<const float*>(k_0)[e] + reinterpret_cast<const float*>(v_0)[e]) +
+                    reinterpret_cast<const float*>(k_1)[e]) + reinterpret_cast<const float*>(v_1)[e];
+        }
+        const int d = 8 * q + 4 * (lane >> 5);
+        if (!mine || d >= D) continue;
+        if (p.splits == 1) {
+            v *= inv;
+            T* rest = rest_of<T>(p, at);
+            store4<T>(first<T>(a.out, a.cu_q != nullptr, w.b, s.q0, 0) + (int64_t)token * a.out.token +
+                          (int64_t)head * a.out.head + d,
+                      rest ? rest + d : nullptr, v);
+        } else {
+            *reinterpret_cast<f32x4*>(p.part_o + ((int64_t)w.split * p.rows * a.Hq + at) * D + d) = v;
+        }
+    }
+}
+
+// Rows whose keys were split: their parts, joined in order.  32 threads to a row (of one head), 4 columns each.
+template <typename TT>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p, int groups) {
+    typedef typename TT::type T;
+    const maxsim_attn& a = p.a;
+    const int b = blockIdx.x / groups, g = blockIdx.x % groups;
+    const Seq s = sequence(a, b);
+    if (a.zero_rest)
+        zero_rest<T>(a.out, p.lse, a.lse_step, a.cu_q, a.B, a.rows_q, b, s.q0, s.lq, s.all_q, a.Hq, a.D, g, groups, (int)blockIdx.x,
+                     (int)gridDim.x);
+    const int64_t r = (int64_t)g * 8 + (threadIdx.x >> 5);
+    if (r >= (int64_t)s.lq * a.Hq) return;
+    const int d = (threadIdx.x & 31) * 4, token = (int)(r / a.Hq), head = (int)(r % a.Hq);
+    const int64_t at = (first_row(a, s, b) + token) * a.Hq + head, step = p.rows * a.Hq;
+    float most = -INFINITY;
+    for (int i = 0; i < p.splits; ++i)
+        if (!is_zero(p.part_ml[2 * (at + i * step) + 1])) most = fmaxf(most, p.part_ml[2 * (at + i * step)]);
+    float total = 0.f;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int i = 0; i < p.splits; ++i) {
+        const float l = p.part_ml[2 * (at + i * step) + 1];
+        const float f = is_zero(l) ? 0.f : __builtin_amdgcn_exp2f(p.part_ml[2 * (at + i * step)] - most);
+        total += l * f;
+        if (d < a.D) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(p.part_o + (at + i * step) * a.D + d);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] += v[q] * f;
+        }
+    }
+    const float inv = is_zero(total) ? 0.f : 1.f / total;
+    if (d < a.D) {
+        o *= inv;
+        T* rest = rest_of<T>(p, at);
+        store4<T>(first<T>(a.out, a.cu_q != nullptr, b, s.q0, 0) + (int64_t)token * a.out.token + (int64_t)head * a.out.head + d,
+                  rest ? rest + d : nullptr, o);
+    }
+    if (p.lse && (threadIdx.x & 31) == 0)
+        p.lse[at * a.lse_step] = is_zero(total) ? -INFINITY : (most + __builtin_amdgcn_logf(total)) * kLn2;
+}
+
+struct Plan {
+    bool few;
+    int tiles, splits;
+    int64_t blocks;
+};
+int64_t rows_in_memory(const maxsim_attn& a) { return a.cu_q ? a.rows_q : (int64_t)a.B * a.max_q; }
+
+// Keys are split where the rows alone do not fill the chip.
+Plan plan_of(const maxsim_attn& a) {
+    Plan p;
+    const int64_t group = a.Hq / a.Hk, rows = (int64_t)a.max_q * group;
+    p.few = rows <= kRowsWave;
+    p.tiles = p.few ? 1 : (int)((rows + kRows - 1) / kRows);
+    const int64_t base = (int64_t)p.tiles * a.Hk * a.B;
+    // keys that a workgroup's rows may see
+    int64_t keys = a.max_k;
+    if (a.left >= 0 && a.right >= 0)
+        keys = std::min<int64_t>(keys, (int64_t)a.left + a.right + std::min<int64_t>(rows, kRows) / group + 2 + a.sinks);
+    const int64_t wanted = p.few ? 512 : 512, least = 256;  // workgroups; keys of a split
+    int64_t splits = base > 0 ? wanted / base : 1;
+    splits = std::min(splits, keys / least);
+    p.splits = rows > 0 ? (int)std::max<int64_t>(1, std::min<int64_t>(splits, 64)) : 1;
+    p.blocks = base * p.splits;
+    return p;
+}
+int64_t join_groups(const maxsim_attn& a) { return ((int64_t)a.max_q * a.Hq + 7) / 8; }
+
+template <typename TT, int DP>
+void launch(const AttnArgs& p, const Plan& plan, hipStream_t stream) {
+    if (plan.few)
+        attn_fwd_few_kernel<TT, DP><<<(unsigned)plan.blocks, 64 * kWaves, 0, stream>>>(p);
+    else
+        attn_fwd_kernel<TT, DP><<<(unsigned)plan.blocks, 64 * kWaves, 0, stream>>>(p, plan.tiles);
+}
+
+}  // namespace
+
+size_t attn_fwd_workspace_bytes(const maxsim_attn& a) {
+    const Plan plan = plan_of(a);
+    if (plan.splits == 1) return 0;
+    return (size_t)plan.splits * (size_t)rows_in_memory(a) * a.Hq * (a.D + 2) * sizeof(float);
+}
+
+bool attn_grid_ok(const maxsim_attn& a) {
+    const int64_t most = (int64_t)1 << 23;
+    const int64_t q_tiles = ((int64_t)a.max_q * (a.Hq / a.Hk) + kRows - 1) / kRows, k_tiles = ((int64_t)a.max_k + 127) / 128;
+    return (std::max(q_tiles, k_tiles) + 1) * a.Hk < most && (std::max(q_tiles, k_tiles) + 1) * a.Hk * a.B < most &&
+           join_groups(a) * a.B < most;
+}
+
+hipError_t launch_attn_fwd(const maxsim_attn& a, float* lse, void* workspace, hipStream_t stream) {
+    const Plan plan = plan_of(a);
+    AttnArgs p{};
+    p.a = a;
+    if (a.left < 0 || a.left > kNoBound) p.a.left = kNoBound;
+    if (a.right < 0 || a.right > kNoBound) p.a.right = kNoBound;
+    p.lse = lse;
+    p.group = a.Hq / a.Hk;
+    p.splits = plan.splits;
+    p.rows = rows_in_memory(a);
+    p.part_o = static_cast<float*>(workspace);
+    p.part_ml = p.part_o + (size_t)plan.splits * p.rows * a.Hq * a.D;
+    const bool half = a.dtype == MAXSIM_F16;
+    if (a.D <= 64) half ? launch<F16, 64>(p, plan, stream) : launch<BF16, 64>(p, plan, stream);
+    else half ? launch<F16, 128>(p, plan, stream) : launch<BF16, 128>(p, plan, stream);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || plan.splits == 1) return e;
+    const int groups = (int)join_groups(a);
+    if (half) attn_join_kernel<F16><<<groups * a.B, 256, 0, stream>>>(p, groups);
+    else attn_join_kernel<BF16><<<groups * a.B, 256, 0, stream>>>(p, groups);
+    return hipGetLastError();
+}
+
+}  // namespace maxsim

@@ -1,0 +1,301 @@
+// distill.hip -- distillation from a teacher's top scores, forward and backward,
+// for gfx950 (MI355X).
+//
+//     q = softmax(teacher / T) over a row's entries;  p = softmax(z / T) over its columns
+//     loss = T^2 sum_k q_k (log q_k - log p_{i_k});  dz_v = dloss T (p_v - sum_{k: i_k = v} q_k)
+//
+// Bound by HBM: the forward reads z once, with a running maximum and sum in each thread; the
+// backward reads it once and writes dz.  The entries touch a few columns only: the backward first writes
+// dloss T p over the whole row and then the entries' columns again.  Few long rows are split over
+// workgroups.  Differences z - max are formed before they are multiplied by 1 / T, and the backward gets
+// the maximum and the sum's logarithm apart, so that large scores at a low temperature lose nothing.
+#include <algorithm>
+
+#include "encoder_dev.h"
+#include "layers.h"
+
+namespace maxsim {
+namespace {
+
+constexpr int kMostEntries = 1024;
+constexpr int kThreads = 256;
+constexpr int kShortRow = 1024;  // columns that one wave takes by itself
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+
+// The largest z and the sum of exp((z - largest) / T).
+struct Soft {
+    float top, sum;
+};
+__device__ __forceinline__ Soft join(Soft a, Soft b, float c) {
+    const float top = fmaxf(a.top, b.top), at = top == -INFINITY ? 0.f : top;
+    return {top, a.sum * __builtin_amdgcn_exp2f((a.top - at) * c) + b.sum * __builtin_amdgcn_exp2f((b.top - at) * c)};
+}
+__device__ __forceinline__ Soft join64(Soft s, float c) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) s = join(s, {__shfl_xor(s.top, d), __shfl_xor(s.sum, d)}, c);
+    return s;
+}
+// Over TPR threads of a row: a wave, or the workgroup, whose waves meet in `part`.
+template <int TPR>
+__device__ __forceinline__ Soft join_row(Soft s, float c, Soft* part) {
+    s = join64(s, c);
+    if constexpr (TPR > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+        __syncthreads();
+        s = part[0];
+#pragma unroll
+        for (int i = 1; i < TPR / 64; ++i) s = join(s, part[i], c);
+    }
+    return s;
+}
+template <int TPR>
+__device__ __forceinline__ float add_row(float v, float* part) {
+    v = sum64(v);
+    if constexpr (TPR > 64) {
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = part[0];
+#pragma unroll
+        for (int i = 1; i < TPR / 64; ++i) v += part[i];
+    }
+    return v;
+}
+
+// A row's threads have read and written what comes before: one wave's, or the workgroup's.
+template <int TPR>
+__device__ __forceinline__ void row_sync() {
+    if constexpr (TPR > 64) {
+        __syncthreads();
+    } else {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0): the row's stores are made
+        asm volatile("" ::: "memory");
+    }
+}
+
+// A row's columns [from, to) by its threads.
+template <typename T, int TPR>
+__device__ __forceinline__ Soft soft_of(const T* z, int from, int to, int lane, float c) {
+    constexpr int AHEAD = 4;
+    Soft s = {-INFINITY, 0.f};
+    for (int at = from + lane * kVec; at < to; at += AHEAD * TPR * kVec) {
+        typename Pack8<T>::V v[AHEAD];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const int col = at + a * TPR * kVec;
+            if (col < to) v[a] = load8<T>(z, col, to);
+        }
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const int col = at + a * TPR * kVec;
+            if (col >= to) continue;
+            float f[kVec], top = s.top;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                f[i] = col + i < to ? (float)v[a][i] : -INFINITY;
+                top = fmaxf(top, f[i]);
+            }
+            const float base = top == -INFINITY ? 0.f : top;
+            s.sum *= __builtin_amdgcn_exp2f((s.top - base) * c);
+            s.top = top;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) s.sum += __builtin_amdgcn_exp2f((f[i] - base) * c);
+        }
+    }
+    return s;
+}
+
+// The teacher's softmax over a row's entries: the largest score and the sum, 0 where there are none.
+template <int TPR>
+__device__ __forceinline__ Soft teacher_of(const DistillArgs& p, const int32_t* index, const float* teacher, int lane, float c,
+                                           Soft* part) {
+    Soft s = {-INFINITY, 0.f};
+    for (int k = lane; k < p.K; k += TPR)
+        if ((uint32_t)index[k] < (uint32_t)p.V) s = join(s, {teacher[k], teacher[k] == -INFINITY ? 0.f : 1.f}, c);
+    return join_row<TPR>(s, c, part);
+}
+
+// A row's loss from its largest score and the logarithm of its sum.
+template <typename T, int TPR>
+__device__ __forceinline__ void finish(const DistillArgs& p, int64_t row, Soft z, int lane, float c, Soft* part, float* parts) {
+    const int32_t* index = p.index + row * p.K;
+    const float* teacher = p.teacher + row * p.K;
+    const T* scores = (const T*)p.scores + row * p.ld;
+    const float log_sum = __builtin_amdgcn_logf(z.sum) * kLn2, t = p.temperature;
+    const Soft q = teacher_of<TPR>(p, index, teacher, lane, c, part);
+    float loss = 0.f;
+    if (q.sum != 0.f) {
+        const float log_q = __builtin_amdgcn_logf(q.sum) * kLn2, inv = 1.f / t;
+        for (int k = lane; k < p.K; k += TPR) {
+            const int v = index[k];
+            if ((uint32_t)v >= (uint32_t)p.V) continue;
+            const float lq = (teacher[k] - q.top) * inv - log_q, w = __builtin_amdgcn_exp2f(lq * kLog2e);
+            const float s = (float)scores[v];
+            const float lp = s == -INFINITY ? -INFINITY : (s - z.top) * inv - log_sum;
+            if (w != 0.f) loss += w * (lq - lp);
+        }
+    }
+    loss = add_row<TPR>(loss, parts);
+    if (lane == 0) {
+        p.loss[row] = loss * (t * t);
+        p.stat[2 * row] = z.top;
+        p.stat[2 * row + 1] = log_sum;
+    }
+}
+
+template <typename TT, int TPR>
+__global__ __launch_bounds__(kThreads) void distill_fwd_kernel(DistillArgs p) {
+    typedef typename TT::type T;
+    __shared__ Soft part[kThreads / 64];
+    __shared__ float parts[kThreads / 64];
+    const int lane = threadIdx.x % TPR;
+    const float c = kLog2e / p.temperature;
+    const int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
+    if (row >= p.N) return;  // whole waves, and whole workgroups where they meet
+    const Soft z = join_row<TPR>(soft_of<T, TPR>((const T*)p.scores + row * p.ld, 0, p.V, lane, c), c, part);
+    finish<T, TPR>(p, row, z, lane, c, part, parts);
+}
+
+// Split rows: a part of a row to a workgroup, and the rest of the work when all are there.
+template <typename TT>
+__global__ __launch_bounds__(kThreads) void distill_part_kernel(DistillArgs p, int splits, int width) {
+    typedef typename TT::type T;
+    __shared__ Soft part[kThreads / 64];
+    const int64_t row = blockIdx.x / splits;
+    const int n = blockIdx.x % splits, from = n * width, to = min(p.V, from + width);
+    const float c = kLog2e / p.temperature;
+    const Soft z =
+        join_row<kThreads>(soft_of<T, kThreads>((const T*)p.scores + row * p.ld, from, to, threadIdx.x, c), c, part);
+    if (threadIdx.x == 0) {
+        p.partial[2 * blockIdx.x] = z.top;
+        p.partial[2 * blockIdx.x + 1] = z.sum;
+    }
+}
+template <typename TT>
+__global__ __launch_bounds__(64) void distill_finish_kernel(DistillArgs p, int splits) {
+    const int64_t row = blockIdx.x;
+    const int lane = threadIdx.x;
+    const float c = kLog2e / p.temperature;
+    Soft z = {-INFINITY, 0.f};
+    for (int i = lane; i < splits; i += 64)
+        z = join(z, {p.partial[2 * (row * splits + i)], p.partial[2 * (row * splits + i) + 1]}, c);
+    finish<typename TT::type, 64>(p, row, join64(z, c), lane, c, nullptr, nullptr);
+}
+
+// dz over columns [from, to) of a row by TPR threads, and the entries among them.
+template <typename TT, int TPR>
+__global__ __launch_bounds__(kThreads) void distill_bwd_kernel(DistillArgs p, int splits, int width) {
+    typedef typename TT::type T;
+    constexpr int PER = kThreads / TPR, AHEAD = 4;
+    __shared__ Soft part[kThreads / 64];
+    extern __shared__ __align__(16) float entries[];  // for each row: columns, q, then p of the entries in the range
+    const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+    const int64_t row = (int64_t)(blockIdx.x / splits) * PER + sub;
+    const int from = (int)(blockIdx.x % splits) * width, to = min(p.V, from + width);
+    if (row >= p.N) return;
+    int* col = (int*)entries + sub * 3 * p.K;
+    float *q = (float*)col + p.K, *prob = q + p.K;
+    const T* z = (const T*)p.scores + row * p.ld;
+    T* dz = (T*)p.dscores + row * p.ldd;
+    const float c = kLog2e / p.temperature, top = p.stat[2 * row] == -INFINITY ? 0.f : p.stat[2 * row];
+    const float log_sum = p.stat[2 * row + 1] * kLog2e;
+    const bool nothing = p.stat[2 * row] == -INFINITY;  // no column is there: p = 0
+    const int32_t* index = p.index + row * p.K;
+    const Soft t = teacher_of<TPR>(p, index, p.teacher + row * p.K, lane, c, part);
+    // no entries: no gradient
+    const float k = t.sum == 0.f ? 0.f : p.dloss[row] * p.temperature;
+    const auto p_of = [&](float s) {
+        return nothing ? 0.f : __builtin_amdgcn_exp2f(__builtin_fmaf(s - top, c, -log_sum));
+    };
+    for (int i = lane; i < p.K; i += TPR) {  // before anything of the row is written: it may be in place
+        const int v = index[i];
+        const bool here = v >= from && v < to;
+        col[i] = (uint32_t)v < (uint32_t)p.V ? v : -1;
+        q[i] = t.sum == 0.f ? 0.f : __builtin_amdgcn_exp2f((p.teacher[row * p.K + i] - t.top) * c) / t.sum;
+        prob[i] = here ? p_of((float)z[v]) : 0.f;
+    }
+    row_sync<TPR>();
+    for (int at = from + lane * kVec; at < to; at += AHEAD * TPR * kVec) {
+        typename Pack8<T>::V v[AHEAD];
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const int cl = at + a * TPR * kVec;
+            if (cl < to) v[a] = load8<T>(z, cl, to);
+        }
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) {
+            const int cl = at + a * TPR * kVec;
+            if (cl >= to) continue;
+            float f[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) f[i] = k == 0.f ? 0.f : p_of((float)v[a][i]) * k;
+            store8<T>(dz, cl, to, f);
+        }
+    }
+    row_sync<TPR>();  // the row is written: its entries' columns come after
+    for (int i = lane; i < p.K; i += TPR) {
+        const int v = col[i];
+        if (v < from || v >= to) continue;
+        float all = 0.f;  // a column may be listed more than once: the same value from each
+        for (int j = 0; j < p.K; ++j) all += col[j] == v ? q[j] : 0.f;
+        dz[v] = (T)(k == 0.f ? 0.f : (prob[i] - all) * k);
+    }
+}
+
+struct DistillPlan {
+    int splits, width;
+};
+// Rows over workgroups while there are fewer than 4 for each CU, a part of at least 4096 columns.
+DistillPlan plan_of(int N, int V) {
+    DistillPlan d{1, V};
+    if (N <= 0 || V <= kShortRow) return d;
+    const int64_t splits = std::min<int64_t>(1024 / N, V / 4096);
+    if (splits <= 1) return d;
+    d.width = (int)(ceil_div(ceil_div(V, splits), 64) * 64);
+    d.splits = (int)ceil_div(V, d.width);
+    return d;
+}
+
+template <typename TT>
+hipError_t fwd(const DistillArgs& a, hipStream_t stream) {
+    const DistillPlan d = plan_of(a.N, a.V);
+    if (d.splits > 1) {
+        distill_part_kernel<TT><<<(unsigned)(a.N * d.splits), kThreads, 0, stream>>>(a, d.splits, d.width);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        distill_finish_kernel<TT><<<(unsigned)a.N, 64, 0, stream>>>(a, d.splits);
+    } else if (a.V <= kShortRow) {
+        distill_fwd_kernel<TT, 64><<<(unsigned)ceil_div(a.N, kThreads / 64), kThreads, 0, stream>>>(a);
+    } else {
+        distill_fwd_kernel<TT, kThreads><<<(unsigned)a.N, kThreads, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+}
+template <typename TT>
+hipError_t bwd(const DistillArgs& a, hipStream_t stream) {
+    const DistillPlan d = plan_of(a.N, a.V);
+    if (a.V <= kShortRow)
+        distill_bwd_kernel<TT, 64><<<(unsigned)ceil_div(a.N, kThreads / 64), kThreads, (size_t)a.K * 12 * (kThreads / 64), stream>>>(
+            a, 1, a.V);
+    else
+        distill_bwd_kernel<TT, kThreads><<<(unsigned)(a.N * d.splits), kThreads, (size_t)a.K * 12, stream>>>(a, d.splits, d.width);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+size_t distill_workspace_bytes(int N, int V) {
+    const DistillPlan d = plan_of(N, V);
+    return d.splits > 1 ? (size_t)N * d.splits * 2 * sizeof(float) : 0;
+}
+hipError_t launch_distill_fwd(const DistillArgs& a, hipStream_t stream) {
+    return a.dtype == MAXSIM_F32 ? fwd<F32>(a, stream) : a.dtype == MAXSIM_BF16 ? fwd<BF16>(a, stream) : fwd<F16>(a, stream);
+}
+hipError_t launch_distill_bwd(const DistillArgs& a, hipStream_t stream) {
+    return a.dtype == MAXSIM_F32 ? bwd<F32>(a, stream) : a.dtype == MAXSIM_BF16 ? bwd<BF16>(a, stream) : bwd<F16>(a, stream);
+}
+
+}  // namespace maxsim

@@ -1,0 +1,116 @@
+// rope.hip -- rotary positions for gfx950 (MI355X).
+//
+//     (u, w) -> scale * (u cos a - w sin a, w cos a + u sin a),   a = position * inv_freq[pair]
+//
+// Bound by HBM: a read and a write of each value.  A workgroup takes some tokens: it forms their
+// sines and cosines once, into LDS (an angle serves all heads), and then streams their heads' rows, 8 columns of a
+// row (8 of either half) to a thread.
+//
+// The angle is a product in fp64 in turns, whose whole part is dropped before it becomes fp32: at position 2^20 a
+// product in fp32 would be off by up to 0.06 radians.
+#include <algorithm>
+
+#include "encoder_dev.h"
+#include "layers.h"
+
+namespace maxsim {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTable = 2048;  // angles of a workgroup, 16 KB of LDS
+
+struct RopePlan {
+    int tokens;     // of a workgroup
+    int heads;      // of a workgroup; the others in further ones
+    int splits;     // of the heads
+    int turn_units, units;  // pieces of a row: of the turned columns, and in all
+    int pitch;      // angles of a token in the table
+};
+
+template <typename TT>
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs p, RopePlan plan) {
+    typedef typename TT::type T;
+    __shared__ __align__(16) float cosine[kTable], sine[kTable];
+    const int half = p.rotary / 2;
+    const int64_t all = (int64_t)p.B * p.L, t0 = (int64_t)(blockIdx.x / plan.splits) * plan.tokens;
+    const int h0 = (int)(blockIdx.x % plan.splits) * plan.heads;
+    const int tokens = (int)min((int64_t)plan.tokens, all - t0), heads = min(plan.heads, p.H - h0);
+    for (int e = threadIdx.x; e < tokens * plan.pitch; e += kThreads) {
+        const int k = e / plan.pitch, i = e - k * plan.pitch;
+        const int64_t t = t0 + k;
+        const int b = (int)(t / p.L), l = (int)(t - (int64_t)b * p.L);
+        const double at = p.positions ? (double)p.positions[t] : (double)l + (p.offsets ? (double)p.offsets[b] : 0.0);
+        const double turns = i < half ? at * (p.inv_freq[i] * 0.15915494309189533577) : 0.0;
+        float s, c;
+        sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
+        cosine[e] = c * p.scale;
+        sine[e] = (p.inverse ? -s : s) * p.scale;
+    }
+    __syncthreads();
+    const int rows = kThreads / plan.units, unit = (int)threadIdx.x % plan.units;
+    if ((int)threadIdx.x >= rows * plan.units) return;
+    const bool turned = unit < plan.turn_units, in_place = p.x.data == p.y.data;
+    if (!turned && in_place) return;
+    const int c = (turned ? unit : unit - plan.turn_units) * kVec;
+    int k = 0, h = (int)threadIdx.x / plan.units;
+    while (h >= heads) h -= heads, ++k;
+    for (; k < tokens;) {
+        const int64_t t = t0 + k;
+        const int b = (int)(t / p.L), l = (int)(t - (int64_t)b * p.L);
+        const T* x = (const T*)p.x.data + b * p.x.batch + l * p.x.token + (int64_t)(h0 + h) * p.x.head;
+        T* y = (T*)p.y.data + b * p.y.batch + l * p.y.token + (int64_t)(h0 + h) * p.y.head;
+        const float *cs = cosine + k * plan.pitch, *sn = sine + k * plan.pitch;
+        if (!turned) {
+            put8<T>(y + p.rotary, c, p.D - p.rotary, load8<T>(x + p.rotary, c, p.D - p.rotary));
+        } else if (p.interleaved) {
+            const auto v = load8<T>(x, c, p.rotary);
+            float f[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec; i += 2) {
+                const float u = (float)v[i], w = (float)v[i + 1], co = cs[(c + i) >> 1], si = sn[(c + i) >> 1];
+                f[i] = __builtin_fmaf(u, co, -(w * si));
+                f[i + 1] = __builtin_fmaf(w, co, u * si);
+            }
+            store8<T>(y, c, p.rotary, f);
+        } else {
+            const auto a = load8<T>(x, c, half), d = load8<T>(x + half, c, half);
+            float f[kVec], g[kVec];
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const float u = (float)a[i], w = (float)d[i], co = cs[c + i], si = sn[c + i];
+                f[i] = __builtin_fmaf(u, co, -(w * si));
+                g[i] = __builtin_fmaf(w, co, u * si);
+            }
+            store8<T>(y, c, half, f);
+            store8<T>(y + half, c, half, g);
+        }
+        h += rows;
+        while (h >= heads) h -= heads, ++k;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_rope(const RopeArgs& a, hipStream_t stream) {
+    RopePlan plan;
+    const int half = a.rotary / 2, rest = a.D - a.rotary;
+    plan.turn_units = a.interleaved ? (int)ceil_div(a.rotary, kVec) : (int)ceil_div(half, kVec);
+    plan.units = plan.turn_units + (int)ceil_div(rest, kVec);
+    plan.pitch = (int)ceil_div(half, kVec) * kVec;
+    const int64_t all = (int64_t)a.B * a.L;
+    // as many tokens to a workgroup as fill the table, fewer where that leaves CUs without work; then fewer heads
+    int64_t tokens = std::min<int64_t>({kTable / plan.pitch, 16, std::max<int64_t>(1, all / 1024)});
+    plan.tokens = (int)std::max<int64_t>(1, tokens);
+    const int64_t groups = ceil_div(all, plan.tokens);
+    const int per_pass = std::max(1, kThreads / plan.units);
+    plan.splits = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.H, per_pass), 1024 / std::max<int64_t>(1, groups)));
+    plan.heads = (int)ceil_div(a.H, plan.splits);
+    plan.splits = (int)ceil_div(a.H, plan.heads);
+    const unsigned blocks = (unsigned)(groups * plan.splits);
+    if (a.dtype == MAXSIM_F32) rope_kernel<F32><<<blocks, kThreads, 0, stream>>>(a, plan);
+    else if (a.dtype == MAXSIM_BF16) rope_kernel<BF16><<<blocks, kThreads, 0, stream>>>(a, plan);
+    else rope_kernel<F16><<<blocks, kThreads, 0, stream>>>(a, plan);
+    return hipGetLastError();
+}
+
+}  // namespace maxsim

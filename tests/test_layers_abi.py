@@ -1,0 +1,165 @@
+"""C ABI of the attention layer's operators and of the distillation loss (include/maxsim_layers.h) on a host without a
+GPU: every declared function is exported with the binding's argument count, and every refusal comes back before any
+device work."""
+import ctypes
+import os
+import re
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "maxsim_layers.h")
+LIB = os.path.join(ROOT, "late_interaction_retrieval_amd", "libmaxsim.so")
+
+if not os.path.exists(LIB):
+    from late_interaction_retrieval_amd import build
+    build.build()
+from late_interaction_retrieval_amd import binding as bd  # noqa: E402
+
+L = bd.lib()
+A = 0x10000  # aligned non-null fake pointers: never dereferenced
+M = 0x10001  # misaligned
+OK, NULL, SHAPE, UNSUPPORTED, ALIGN, WORKSPACE = 0, 1, 2, 3, 4, 5
+F16, BF16, F32, I8 = 0, 1, 2, 3
+
+
+def test_every_declared_symbol_is_exported_with_binding_arity():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    decl = {m.group(1): len([p for p in m.group(2).split(",") if p.strip() and p.strip() != "void"])
+            for m in re.finditer(r"^[A-Za-z_][\w \*]*?\b(maxsim_\w+)\s*\(([^)]*)\)\s*;", text, flags=re.M)}
+    assert set(decl) == {"maxsim_rope", "maxsim_attn_fwd", "maxsim_attn_bwd", "maxsim_attn_fwd_workspace_bytes",
+                         "maxsim_attn_bwd_workspace_bytes", "maxsim_distill_fwd", "maxsim_distill_bwd",
+                         "maxsim_distill_workspace_bytes"}
+    raw = ctypes.CDLL(LIB)
+    for name, nargs in decl.items():
+        assert hasattr(raw, name), name
+        assert len(bd.SIGNATURES[name][1]) == nargs, name
+
+
+def test_the_struct_has_the_headers_fields_in_order():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    body = re.search(r"typedef struct \{([^}]*)\} maxsim_attn;", text).group(1)
+    names = [n.strip(" *\n") for line in body.split(";") for n in re.sub(r"^\s*(const )?\w+", "", line).split(",") if n.strip()]
+    assert names == [f[0] for f in bd._Attn._fields_]
+
+
+def view(data=A, batch=4096, token=128, head=64):
+    return bd._View(data, batch, token, head)
+
+
+def rope(xv=None, yv=None, **kw):
+    a = dict(B=2, L=3, H=2, D=64, rotary=64, layout=0, dt=BF16, f=A, pos=None, off=None, scale=1.0, inverse=0, stream=None)
+    a.update(kw)
+    x, y = xv or view(), yv or view(data=2 * A)
+    return L.maxsim_rope(ctypes.byref(x) if xv != 0 else None, ctypes.byref(y), *a.values())
+
+
+@pytest.mark.parametrize("want,kw", [
+    (SHAPE, dict(B=-1)), (SHAPE, dict(L=-1)), (SHAPE, dict(H=0)), (SHAPE, dict(D=0)), (SHAPE, dict(rotary=0)),
+    (SHAPE, dict(rotary=63)), (SHAPE, dict(rotary=66)), (SHAPE, dict(scale=float("nan"))), (SHAPE, dict(scale=float("inf"))),
+    (SHAPE, dict(B=1 << 13, L=1 << 13)), (SHAPE, dict(pos=A, off=A)), (UNSUPPORTED, dict(dt=I8)), (UNSUPPORTED, dict(layout=2)),
+    (UNSUPPORTED, dict(D=1026, yv=view(token=4096, head=2048))), (SHAPE, dict(yv=view(head=63))), (SHAPE, dict(yv=view(token=63))),
+    (SHAPE, dict(yv=view(batch=63))), (SHAPE, dict(xv=view(token=-1))), (SHAPE, dict(yv=view(batch=1 << 41))),
+    (SHAPE, dict(yv=view(head=128))),  # x's memory with other steps
+    (NULL, dict(xv=view(data=0))), (NULL, dict(yv=view(data=0))), (NULL, dict(f=None)), (ALIGN, dict(xv=view(data=M))),
+    (ALIGN, dict(yv=view(data=M))), (ALIGN, dict(f=A + 4)), (ALIGN, dict(pos=M)), (ALIGN, dict(off=M)), (OK, dict(B=0)), (OK, dict(L=0)),
+], ids=str)
+def test_rope_refusals(want, kw):
+    if kw.get("yv") is not None and kw["yv"].head == 128:
+        kw = dict(xv=view(), yv=view(head=128))
+    assert rope(**kw) == want
+
+
+def attn(**kw):
+    a = bd._Attn()
+    for n in ("q", "k", "v", "out"):
+        setattr(a, n, kw.pop(n, None) or view())
+    d = dict(B=2, max_q=5, max_k=9, Hq=2, Hk=2, D=64, dtype=BF16, left=-1, right=-1, sinks=0, zero_rest=0, scale=0.125, lse_step=1,
+             rows_q=10, rows_k=18, cu_q=None, cu_k=None, q_lens=None, k_lens=None)
+    d.update(kw)
+    for n, v in d.items():
+        setattr(a, n, v)
+    return a
+
+
+SIZES = [
+    (SHAPE, dict(B=-1)), (SHAPE, dict(max_q=-1)), (SHAPE, dict(max_k=-1)), (SHAPE, dict(Hq=0)), (SHAPE, dict(Hk=0)),
+    (SHAPE, dict(Hq=3)), (SHAPE, dict(sinks=-1)), (SHAPE, dict(scale=0.0)), (SHAPE, dict(scale=-1.0)),
+    (SHAPE, dict(scale=float("nan"))), (SHAPE, dict(scale=float("inf"))), (SHAPE, dict(max_q=1 << 29)),
+    (SHAPE, dict(max_q=1 << 28, Hq=4)), (SHAPE, dict(max_k=1 << 29)), (SHAPE, dict(cu_q=A, rows_q=-1)),
+    (SHAPE, dict(cu_k=A, rows_k=1 << 31)), (SHAPE, dict(B=1 << 20, Hq=64, Hk=64, max_q=1)), (SHAPE, dict(lse_step=0)),
+    (SHAPE, dict(lse_step=32)), (UNSUPPORTED, dict(D=0)), (UNSUPPORTED, dict(D=12)), (UNSUPPORTED, dict(D=136)),
+    (UNSUPPORTED, dict(dtype=F32)), (UNSUPPORTED, dict(dtype=I8)),
+]
+VIEWS = [(SHAPE, dict(token=63)), (SHAPE, dict(token=(1 << 20) + 8)), (SHAPE, dict(batch=-8)), (SHAPE, dict(head=1 << 41)),
+         (NULL, dict(data=0)), (ALIGN, dict(data=A + 8)), (ALIGN, dict(token=132)), (ALIGN, dict(head=68)), (ALIGN, dict(batch=4100))]
+
+
+@pytest.mark.parametrize("want,kw", SIZES + [(w, {n: view(**v)}) for n in ("q", "k", "v", "out") for w, v in VIEWS] + [
+    (SHAPE, dict(out=view(head=0))), (SHAPE, dict(out=view(batch=0))), (ALIGN, dict(cu_q=M)), (ALIGN, dict(cu_k=M)),
+    (ALIGN, dict(q_lens=M)), (ALIGN, dict(k_lens=M)), (OK, dict(B=0))], ids=str)
+def test_attention_forward_refusals(want, kw):
+    a = attn(**kw)
+    assert L.maxsim_attn_fwd(ctypes.byref(a), None, None, 0, None) == want
+
+
+def test_attention_forward_pointers_and_workspace():
+    assert L.maxsim_attn_fwd(None, None, None, 0, None) == NULL
+    a = attn()
+    assert L.maxsim_attn_fwd(ctypes.byref(a), M, None, 0, None) == ALIGN
+    assert L.maxsim_attn_fwd(ctypes.byref(a), None, M, 0, None) == ALIGN
+    long = attn(B=1, max_q=1, max_k=1 << 16, k_lens=A)
+    need = L.maxsim_attn_fwd_workspace_bytes(ctypes.byref(long))
+    assert need > 0
+    assert L.maxsim_attn_fwd(ctypes.byref(long), None, None, 0, None) == NULL
+    assert L.maxsim_attn_fwd(ctypes.byref(long), None, A, need - 1, None) == WORKSPACE
+    assert L.maxsim_attn_fwd_workspace_bytes(None) == 0 and L.maxsim_attn_bwd_workspace_bytes(None) == 0
+    for _, bad in SIZES:
+        assert L.maxsim_attn_fwd_workspace_bytes(ctypes.byref(attn(**bad))) == 0
+        assert L.maxsim_attn_bwd_workspace_bytes(ctypes.byref(attn(**bad))) == 0
+
+
+def bwd(a, lse=A, ws=A, nbytes=1 << 20, **kw):
+    v = {n: kw.get(n) or view() for n in ("dout", "dq", "dk", "dv")}
+    return L.maxsim_attn_bwd(ctypes.byref(a), lse, *[ctypes.byref(x) for x in v.values()], ws, nbytes, None)
+
+
+@pytest.mark.parametrize("want,kw", SIZES + [(w, {n: view(**v)}) for n in ("q", "out", "dout", "dq", "dk", "dv") for w, v in VIEWS] + [
+    (SHAPE, dict(dq=view(head=0))), (SHAPE, dict(dk=view(batch=0))), (NULL, dict(lse=None)), (NULL, dict(ws=None)),
+    (ALIGN, dict(lse=M)), (ALIGN, dict(ws=A + 8)), (WORKSPACE, dict(nbytes=8)), (OK, dict(B=0))], ids=str)
+def test_attention_backward_refusals(want, kw):
+    mine = {n: kw[n] for n in ("dout", "dq", "dk", "dv", "lse", "ws", "nbytes") if n in kw}
+    assert bwd(attn(**{n: v for n, v in kw.items() if n not in mine}), **mine) == want
+
+
+def distill(fwd, **kw):
+    a = dict(z=A, ld=64, i=A, t=A, N=3, V=64, K=5, dt=F32, T=1.0, loss=A, stat=A, ws=None, nbytes=0, dloss=A, d=A, ldd=64)
+    a.update(kw)
+    if fwd:
+        names = ("z", "ld", "i", "t", "N", "V", "K", "dt", "T", "loss", "stat", "ws", "nbytes")
+        return L.maxsim_distill_fwd(*[a[n] for n in names], None)
+    names = ("dloss", "z", "ld", "stat", "i", "t", "N", "V", "K", "dt", "T", "d", "ldd")
+    return L.maxsim_distill_bwd(*[a[n] for n in names], None)
+
+
+@pytest.mark.parametrize("fwd", [True, False])
+@pytest.mark.parametrize("want,kw", [
+    (SHAPE, dict(N=-1)), (SHAPE, dict(V=-1)), (SHAPE, dict(K=-1)), (SHAPE, dict(T=0.0)), (SHAPE, dict(T=-1.0)),
+    (SHAPE, dict(T=float("nan"))), (SHAPE, dict(T=float("inf"))), (SHAPE, dict(ld=63)), (SHAPE, dict(ld=1 << 32)),
+    (SHAPE, dict(N=1 << 24)), (SHAPE, dict(V=1 << 30, ld=1 << 30, ldd=1 << 30)), (UNSUPPORTED, dict(K=1025)),
+    (UNSUPPORTED, dict(dt=I8)), (NULL, dict(z=None)), (NULL, dict(i=None)), (NULL, dict(t=None)), (NULL, dict(stat=None)),
+    (ALIGN, dict(z=M)), (ALIGN, dict(i=M)), (ALIGN, dict(t=M)), (ALIGN, dict(stat=M)), (OK, dict(N=0)), (OK, dict(N=0, z=None)),
+], ids=str)
+def test_distill_refusals(want, kw, fwd):
+    assert distill(fwd, **kw) == want
+
+
+def test_distill_refusals_of_one_direction():
+    assert distill(True, loss=None) == NULL and distill(True, loss=M) == ALIGN and distill(True, ws=M) == ALIGN
+    assert distill(False, dloss=None) == NULL and distill(False, d=None) == NULL and distill(False, dloss=M) == ALIGN
+    assert distill(False, d=M) == ALIGN and distill(False, ldd=63) == SHAPE and distill(False, ldd=65) == SHAPE
+    assert distill(False, V=0, ld=0, ldd=0) == OK
+    need = L.maxsim_distill_workspace_bytes(4, 1 << 20)
+    big = dict(N=4, V=1 << 20, ld=1 << 20)
+    assert need > 0 and distill(True, **big) == NULL and distill(True, ws=A, nbytes=need - 1, **big) == WORKSPACE
+    assert L.maxsim_distill_workspace_bytes(-1, 5) == 0 and L.maxsim_distill_workspace_bytes(4, 1 << 30) == 0
