@@ -77,7 +77,8 @@ int maxsim_rope(const maxsim_view* x, const maxsim_view* y, int32_t B, int32_t L
  * the matrix cores take it; each output is rounded once.  Values of one sequence have to be finite: a NaN or an
  * infinity reaches all rows that see it and may reach rows near them that do not.
  * Requires data 16-byte aligned and steps multiples of 8, token steps of at least D and at most 2^20; D a multiple of 8 from 8 to 128;
- * Hq a multiple of Hk; 0 <= max_q * (Hq / Hk), max_k < 2^29; scale finite and > 0; sinks >= 0.
+ * Hq a multiple of Hk; 0 <= max_q * (Hq / Hk), max_k < 2^29; scale finite and > 0; sinks >= 0; and tiles of
+ * 128 rows, of queries (max_q * (Hq / Hk)) or keys, of which B * Hk times one more than there are stay below 2^21.
  */
 typedef struct {
     maxsim_view q, k, v, out;

@@ -7,6 +7,8 @@
 // second over the queries for each tile of keys (dK and dV, summed over the query heads of the key
 // head).  Each makes S and dP anew: 7 products of a pair for the 5 of a single pass, whose dQ would have to be
 // added up in memory by all workgroups in an order of chance.
+#include <algorithm>
+
 #include "attn_dev.h"
 
 namespace maxsim {
@@ -29,6 +31,15 @@ __device__ __forceinline__ float lift_of(float top) {
     return e == 0 || e == 255 ? 1.f : __uint_as_float((uint32_t)(254 - e) << 23);
 }
 
+// The first token past the window of all of a key tile's keys.
+__device__ __forceinline__ int far_from(const maxsim_attn& a, const Seq& s, int j0) {
+    return max(0, min(s.lq, min(j0 + kRows, s.lk) + a.left - (s.lk - s.lq)));
+}
+__device__ __forceinline__ float* far_row(const AttnArgs& p, int b, int h, int tile, int slot, int row) {
+    const int64_t block = (((int64_t)b * p.a.Hk + h) * p.far_tiles + tile) * (p.far_chunks + 1) + slot;
+    return p.part_far + (block * 2 * p.far_rows + row) * p.a.D;
+}
+
 template <typename TT, int DP>
 __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int tiles) {
     typedef typename TT::type T;
@@ -36,15 +47,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
     constexpr int KS = DP / 16, DB = DP / 32, BYTES = kTile * Tile<DP>::ROW;
     __shared__ __align__(16) uint8_t k_0[BYTES], v_0[BYTES], k_1[BYTES], v_1[BYTES];
     const maxsim_attn& a = p.a;
-    int id = item_of_block();
-    const int item = id, tile = tiles - 1 - id % tiles;
-    id /= tiles;
-    const int h = id % a.Hk, b = id / a.Hk;
+    Work w;
+    if (!work_of(w, a.B, a.Hk, tiles)) return;
+    const int b = w.b, h = w.h, tile = tiles - 1 - w.part;
     const Seq s = sequence(a, b);
     const int G = p.group, D = a.D, rows = s.lq * G;
     if (a.zero_rest)
-        zero_rest<T>(p.dq, nullptr, 1, a.cu_q, a.B, a.rows_q, b, s.q0, s.lq, s.all_q, a.Hq, D, h * tiles + tile, a.Hk * tiles, item,
-                     (int)gridDim.x);
+        zero_rest<T>(p.dq, nullptr, 1, a.cu_q, a.B, a.rows_q, b, s.q0, s.lq, s.all_q, a.Hq, D, h * tiles + tile, a.Hk * tiles,
+                     w.item(tiles, a.Hk), w.items);
     const int r0 = tile * kRows;
     if (r0 >= rows) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -109,11 +119,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
         lv.load(vs + (int64_t)j * a.v.token, s.lk - j, a.v.token, D, vt, wave);
     };
     const auto work = [&](int t, const uint8_t* kt, const uint8_t* vt) {
-        const int j0 = span.at(t, kTile), end = span.end(t), j_last = j0 + kTile - 1;
-        if (wr >= rows || j0 > p_hi + a.right || (j_last < p_lo - a.left && j0 >= a.sinks)) return;
-        const bool whole = j_last < end && j_last <= min(p_lo + a.right, s.lk - 1) && (j0 >= p_hi - a.left || j_last < a.sinks);
+        const int j0 = span.at(t, kTile), end = span.end(t);
+        if (wr >= rows) return;
 #pragma unroll
         for (int nb = 0; nb < kTile / 32; ++nb) {
+            const int jb = j0 + 32 * nb;
+            if (jb >= end || jb > p_hi + a.right || (jb + 31 < p_lo - a.left && jb >= a.sinks)) continue;  // no row sees any
+            const bool whole = jb + 32 <= end && jb + 31 <= min(p_lo + a.right, s.lk - 1) && (jb >= p_hi - a.left || jb + 32 <= a.sinks);
             const uint8_t *kb = kt + nb * 32 * Tile<DP>::ROW, *vb = vt + nb * 32 * Tile<DP>::ROW;
             f32x16 x = zero16(), dp = zero16();
 #pragma unroll
@@ -123,13 +135,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -lse));
             if (!whole) {
-                const int j = j0 + 32 * nb + 4 * (lane >> 5);
-                const int upto = min(hi, end - 1) - j, low = lo - j, sink = a.sinks - j;
+                const int j = jb + 4 * (lane >> 5);
+                const uint32_t bits = slots_seen(lo - j, min(hi, end - 1) - j, a.sinks - j);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] = slot(i) <= upto && (slot(i) >= low || slot(i) < sink) ? x[i] : 0.f;
+                for (int i = 0; i < 16; ++i) x[i] = keep(bits, i, x[i], 0u);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] *= (dp[i] - delta) * lift;
+            for (int i = 0; i < 16; ++i) x[i] *= is_f16<T>() ? (dp[i] - delta) * lift : dp[i] - delta;
 #pragma unroll
             for (int t2 = 0; t2 < 2; ++t2) {
                 const V8 ds = pack8<T>(x, 8 * t2);
@@ -152,51 +164,70 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
     store_row<T, DB>(out, mine, acc, a.scale / lift, lane, D);
 }
 
-// A workgroup's 128 keys of one key head; the query heads that share it one after the other, 64 tokens at a
-// time.  The queries are the rows of S here, the keys its columns, so P and dS are the B operands of dV^T = dO^T P and
-// dK^T = Q^T dS, and a lane's two result rows stay in registers.
-template <typename TT, int DP>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_dkv_kernel(AttnArgs p, int tiles) {
+// A workgroup's 128 keys of one key head, 32 of a wave; the query heads that share it one after the other, TR tokens
+// at a time.  The queries are the rows of S here, the keys its columns, so P and dS are the B operands of dV^T = dO^T P and
+// dK^T = Q^T dS, and a lane's result rows stay in registers.  WAVES to a SIMD: two leave a wave 256 registers, which do
+// not hold k's operands beside the sums at a width of 128 (they stay in LDS), one leaves 512.
+template <typename TT, int DP, int WAVES>
+__global__ __launch_bounds__(64 * kWaves, WAVES) void attn_dkv_kernel(AttnArgs p, int tiles) {
     typedef typename TT::type T;
     typedef typename Vec8<T>::V V8;
-    constexpr int KS = DP / 16, DB = DP / 32, BYTES = kTile * Tile<DP>::ROW, STATS = is_f16<T>() ? 3 : 2;
+    constexpr int TR = DP == 128 && WAVES == 2 ? 32 : 64;
+    constexpr bool K_IN_LDS = DP == 128 && WAVES == 2;
+    constexpr int KS = DP / 16, DB = DP / 32, BYTES = TR * Tile<DP>::ROW, STATS = is_f16<T>() ? 3 : 2;
     __shared__ __align__(16) uint8_t q_0[BYTES], g_0[BYTES], q_1[BYTES], g_1[BYTES];
-    __shared__ __align__(16) float stat_0[4 * 64], stat_1[4 * 64];
+    __shared__ __align__(16) float stat_0[STATS * 64], stat_1[STATS * 64];
+    __shared__ __align__(16) uint8_t k_lds[K_IN_LDS ? kWaves * KS * 1024 : 16];  // 64 lanes x 16 bytes for each step
     const maxsim_attn& a = p.a;
-    int id = item_of_block();
-    const int item = id, tile = id % tiles;
-    id /= tiles;
-    const int h = id % a.Hk, b = id / a.Hk;
+    Work w;
+    const int fars = p.far_tiles * p.far_chunks;
+    if (!work_of(w, a.B, a.Hk, tiles + fars)) return;
+    const int b = w.b, h = w.h;
+    const bool far = w.part < fars;
+    const int tile = far ? w.part / p.far_chunks : w.part - fars, chunk = far ? w.part % p.far_chunks : 0;
     const Seq s = sequence(a, b);
     const int G = p.group, D = a.D;
-    if (a.zero_rest) {
-        zero_rest<T>(p.dk, nullptr, 1, a.cu_k, a.B, a.rows_k, b, s.k0, s.lk, s.all_k, a.Hk, D, h * tiles + tile, a.Hk * tiles, item,
-                     (int)gridDim.x);
-        zero_rest<T>(p.dv, nullptr, 1, a.cu_k, a.B, a.rows_k, b, s.k0, s.lk, s.all_k, a.Hk, D, h * tiles + tile, a.Hk * tiles, item,
-                     (int)gridDim.x);
+    if (a.zero_rest && !far) {
+        const int part = h * tiles + tile, parts = a.Hk * tiles, item = (b * a.Hk + h) * tiles + tile, items = a.B * a.Hk * tiles;
+        zero_rest<T>(p.dk, nullptr, 1, a.cu_k, a.B, a.rows_k, b, s.k0, s.lk, s.all_k, a.Hk, D, part, parts, item, items);
+        zero_rest<T>(p.dv, nullptr, 1, a.cu_k, a.B, a.rows_k, b, s.k0, s.lk, s.all_k, a.Hk, D, part, parts, item, items);
     }
     const int j0 = tile * kRows;
     if (j0 >= s.lk) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int shift = s.lk - s.lq;
-    // tokens that see any of the keys
-    const int i_lo = max(0, j0 - a.right - shift);
-    const int i_hi = j0 < a.sinks ? s.lq : min(s.lq, min(j0 + kRows, s.lk) - 1 + a.left - shift + 1);
-    const int steps = (max(i_hi - i_lo, 0) + kTile - 1) / kTile, total = steps * G;
+    // tokens [i_lo, i_hi) see any of the keys; where first tokens' keys are worked on apart, those past the window do not count
+    const bool apart = tile < p.far_tiles;
+    const int i_far = far_from(a, s, j0);
+    int i_lo = max(0, j0 - a.right - shift), i_hi = j0 < a.sinks && !apart ? s.lq : i_far;
+    if (far) {
+        i_lo = i_far + chunk * p.far_tokens;
+        i_hi = min(s.lq, i_lo + p.far_tokens);
+        if (i_lo >= i_hi) return;
+    }
+    const int steps = (max(i_hi - i_lo, 0) + TR - 1) / TR, total = steps * G;
 
-    const int wj = j0 + wave * 32, j = min(wj + (lane & 31), s.lk - 1);
+    const int wj = j0 + wave * 32, j_hi = min(wj + 31, s.lk - 1);  // the wave's keys
+    const int j = min(wj + (lane & 31), s.lk - 1);
     const bool mine = wj + (lane & 31) < s.lk, packed = a.cu_k != nullptr;
-    V8 k[KS], v[KS];
+    V8 k[K_IN_LDS ? 1 : KS], v[KS];
+    const int k_at = wave * KS * 1024 + lane * 16;
     const T* kr = first<T>(a.k, packed, b, s.k0, h) + (int64_t)j * a.k.token;
     const T* vr = first<T>(a.v, packed, b, s.k0, h) + (int64_t)j * a.v.token;
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk) {
-        k[kk] = row8<T>(kr, 16 * kk + 8 * (lane >> 5), D);
+        const V8 x = row8<T>(kr, 16 * kk + 8 * (lane >> 5), D);
+        if constexpr (K_IN_LDS) *reinterpret_cast<V8*>(k_lds + k_at + kk * 1024) = x;
+        else k[kk] = x;
         v[kk] = row8<T>(vr, 16 * kk + 8 * (lane >> 5), D);
     }
-    // the lane's key is seen by tokens [lo, hi]
-    const int lo = j - a.right - shift, hi = j < a.sinks ? s.lq - 1 : min(s.lq - 1, j + a.left - shift);
-    const int j_hi = min(wj + 31, s.lk - 1);  // the wave's last key
+    // the lane's key is seen by tokens [lo, hi] of these
+    const int hi_first = i_hi - 1, hi_plain = far ? -1 : min(i_hi - 1, j + a.left - shift);
+    const int lo = max(i_lo, j - a.right - shift), hi = j < a.sinks ? hi_first : hi_plain;
+    // all of the wave's keys by tokens [all_lo, all_hi], any of them by [any_lo, any_hi]
+    const int all_lo = max(i_lo, j_hi - a.right - shift), any_lo = max(i_lo, wj - a.right - shift);
+    const int all_hi = j_hi < a.sinks ? hi_first : far ? -1 : min(i_hi - 1, wj + a.left - shift);
+    const int any_hi = wj < a.sinks ? hi_first : far ? -1 : min(i_hi - 1, j_hi + a.left - shift);
     const float c = a.scale * kLog2e;
     f32x16 dk[DB], dv[DB];
 #pragma unroll
@@ -206,30 +237,34 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dkv_kernel(AttnArgs p, in
     const T* qs = first<T>(a.q, a.cu_q != nullptr, b, s.q0, h * G);
     const T* gs = first<T>(p.dout, a.cu_q != nullptr, b, s.q0, h * G);
     const int64_t row0 = first_row(a, s, b);
-    Loader<DP, kTile, kWaves> lq, lg;
+    Loader<DP, TR, kWaves> lq, lg;
     lq.init(wave, lane, a.q.token, D);
     lg.init(wave, lane, p.dout.token, D);
-    const auto load = [&](int t, uint8_t* qt, uint8_t* gt, float* stat) {
-        const int g = t / steps, i = i_lo + (t - g * steps) * kTile;
-        lq.load(qs + (int64_t)g * a.q.head + (int64_t)i * a.q.token, s.lq - i, a.q.token, D, qt, wave);
-        lg.load(gs + (int64_t)g * p.dout.head + (int64_t)i * p.dout.token, s.lq - i, p.dout.token, D, gt, wave);
-        if (wave < STATS) {  // 64 rows' values of one kind; zeros past the last row, whose q and dO are zeros too
-            const uint64_t at = (uint64_t)(p.row_stat + ((int64_t)wave * a.Hq + h * G + g) * p.rows + row0 + i);
-            const uint32_t first_ = __builtin_amdgcn_readfirstlane((uint32_t)at), second = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+    int g_next = 0, i_next = i_lo;  // the head and the token that the next tile starts with
+    const auto load = [&](uint8_t* qt, uint8_t* gt, float* stat) {
+        lq.load(qs + (int64_t)g_next * a.q.head + (int64_t)i_next * a.q.token, s.lq - i_next, a.q.token, D, qt, wave);
+        lg.load(gs + (int64_t)g_next * p.dout.head + (int64_t)i_next * p.dout.token, s.lq - i_next, p.dout.token, D, gt, wave);
+        if (wave < STATS) {  // the rows' values of one kind; zeros past the last row, whose q and dO are zeros too
+            const uint64_t at = (uint64_t)(p.row_stat + ((int64_t)wave * a.Hq + h * G + g_next) * p.rows + row0 + i_next);
+            const uint32_t low = __builtin_amdgcn_readfirstlane((uint32_t)at), high = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
             const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(((uint64_t)second << 32) | first_), (short)0, min(s.lq - i, kTile) * 4, 0x00020000);
+                (void*)(((uint64_t)high << 32) | low), (short)0, min(s.lq - i_next, TR) * 4, 0x00020000);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lptr_t)(stat + wave * 64), 4, lane * 4, 0, 0, 0);
         }
+        i_next += TR;
+        if (i_next >= i_hi) i_next = i_lo, ++g_next;
     };
-    const auto work = [&](int t, const uint8_t* qt, const uint8_t* gt, const float* stat) {
-        const int i0 = i_lo + (t % steps) * kTile;
+    int i_now = i_lo;  // the token that the tile at hand starts with
+    const auto work = [&](const uint8_t* qt, const uint8_t* gt, const float* stat) {
+        const int at = i_now;
+        i_now = i_now + TR >= i_hi ? i_lo : i_now + TR;
         if (wj >= s.lk) return;
         float f = 1.f;
         if constexpr (is_f16<T>()) {
             // rows in the scale of the largest dO seen so far, what is there already brought to it
-            const float now = lift_of(fmaxf(__uint_as_float(max64(fbits(stat[128 + lane]))), 0.f));
-            const bool any = max64(fbits(stat[128 + lane])) != 0;
-            if (any && (lift == 0.f || now < lift)) {
+            const uint32_t top = max64(fbits(stat[128 + lane]));
+            const float now = lift_of(__uint_as_float(top));
+            if (top != 0 && (lift == 0.f || now < lift)) {
                 const float down = lift == 0.f ? 1.f : now / lift;
 #pragma unroll
                 for (int db = 0; db < DB; ++db)
@@ -237,18 +272,25 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dkv_kernel(AttnArgs p, in
                     for (int i = 0; i < 16; ++i) dk[db][i] *= down;
                 lift = now;
             }
-            f = lift == 0.f ? 1.f : lift;
+            f = (lift == 0.f ? 1.f : lift) * (1.f / 256.f);  // P is lifted by 2^8
         }
 #pragma unroll
-        for (int nb = 0; nb < kTile / 32; ++nb) {
-            const int ib = i0 + 32 * nb;
-            // all of the block's tokens before, or behind, those that see the wave's keys
-            if (ib > (wj < a.sinks ? s.lq - 1 : j_hi + a.left - shift) || ib + 31 < wj - a.right - shift || ib >= s.lq) continue;
-            const bool whole = ib >= j_hi - a.right - shift && ib + 31 < s.lq && (j_hi < a.sinks || ib + 31 <= wj + a.left - shift);
+        for (int nb = 0; nb < TR / 32; ++nb) {
+            const int ib = at + 32 * nb;
+            if (ib > any_hi || ib + 31 < any_lo) continue;
+            const bool whole = ib >= all_lo && ib + 31 <= all_hi;
             const uint8_t *qb = qt + nb * 32 * Tile<DP>::ROW, *gb = gt + nb * 32 * Tile<DP>::ROW;
+            // (the compiler is not to see that k's operands are the same in each step: it would keep them in registers)
+            int ka = k_at;
+            asm volatile("" : "+v"(ka));
             f32x16 x = zero16(), dp = zero16();
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk) x = mma<T>(rows_at<T, DP>(qb, lane, kk), k[kk], x);
+            for (int kk = 0; kk < KS; ++kk) {
+                V8 kx;
+                if constexpr (K_IN_LDS) kx = *reinterpret_cast<const V8*>(k_lds + ka + kk * 1024);
+                else kx = k[kk];
+                x = mma<T>(rows_at<T, DP>(qb, lane, kk), kx, x);
+            }
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) dp = mma<T>(rows_at<T, DP>(gb, lane, kk), v[kk], dp);
 #pragma unroll
@@ -259,72 +301,145 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dkv_kernel(AttnArgs p, in
             }
             if (!whole) {
                 const int i = ib + 4 * (lane >> 5);
-                const int low = lo - i, upto = hi - i;
+                const uint32_t bits = slots_seen(lo - i, hi - i, 0);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = slot(e) >= low && slot(e) <= upto ? x[e] : 0.f;
+                for (int e = 0; e < 16; ++e) x[e] = keep(bits, e, x[e], 0u);
             }
 #pragma unroll
-            for (int t2 = 0; t2 < 2; ++t2) {
-                const V8 pt = pack8<T>(x, 8 * t2);
+            for (int t = 0; t < 2; ++t) {
+                const V8 pt = pack8<T>(x, 8 * t);
 #pragma unroll
-                for (int db = 0; db < DB; ++db) dv[db] = mma<T>(cols_at<T, DP>(gb, lane, t2, db), pt, dv[db]);
+                for (int db = 0; db < DB; ++db) dv[db] = mma<T>(cols_at<T, DP>(gb, lane, t, db), pt, dv[db]);
             }
-            if constexpr (is_f16<T>()) f *= 1.f / 256.f;  // P is lifted by 2^8
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const f32x4 d = *reinterpret_cast<const f32x4*>(stat + 64 + 32 * nb + 8 * q + 4 * (lane >> 5));
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[4 * q + i] *= is_f16<T>() ? (dp[4 * q + i] - d[i]) * f : dp[4 * q + i] - d[i];
             }
-            if constexpr (is_f16<T>()) f *= 256.f;
 #pragma unroll
-            for (int t2 = 0; t2 < 2; ++t2) {
-                const V8 ds = pack8<T>(x, 8 * t2);
+            for (int t = 0; t < 2; ++t) {
+                const V8 ds = pack8<T>(x, 8 * t);
 #pragma unroll
-                for (int db = 0; db < DB; ++db) dk[db] = mma<T>(cols_at<T, DP>(qb, lane, t2, db), ds, dk[db]);
+                for (int db = 0; db < DB; ++db) dk[db] = mma<T>(cols_at<T, DP>(qb, lane, t, db), ds, dk[db]);
             }
         }
     };
-    if (total > 0) load(0, q_0, g_0, stat_0);
+    if (total > 0) load(q_0, g_0, stat_0);
     for (int t = 0; t < total; t += 2) {
         tile_ready();
-        if (t + 1 < total) load(t + 1, q_1, g_1, stat_1);
-        work(t, q_0, g_0, stat_0);
+        if (t + 1 < total) load(q_1, g_1, stat_1);
+        work(q_0, g_0, stat_0);
         if (t + 1 >= total) break;
         tile_ready();
-        if (t + 2 < total) load(t + 2, q_0, g_0, stat_0);
-        work(t + 1, q_1, g_1, stat_1);
+        if (t + 2 < total) load(q_0, g_0, stat_0);
+        work(q_1, g_1, stat_1);
     }
-    T* dkr = first<T>(p.dk, packed, b, s.k0, h) + (int64_t)j * p.dk.token;
-    T* dvr = first<T>(p.dv, packed, b, s.k0, h) + (int64_t)j * p.dv.token;
-    store_row<T, DB>(dkr, mine, dk, is_f16<T>() && lift != 0.f ? a.scale / lift : a.scale, lane, D);
-    store_row<T, DB>(dvr, mine, dv, is_f16<T>() ? 1.f / 256.f : 1.f, lane, D);
+    const float kf = is_f16<T>() && lift != 0.f ? a.scale / lift : a.scale, vf = is_f16<T>() ? 1.f / 256.f : 1.f;
+    const bool part = apart && j < a.sinks;
+    if (!far) {
+        T* dkr = first<T>(p.dk, packed, b, s.k0, h) + (int64_t)j * p.dk.token;
+        T* dvr = first<T>(p.dv, packed, b, s.k0, h) + (int64_t)j * p.dv.token;
+        store_row<T, DB>(dkr, mine && !part, dk, kf, lane, D);
+        store_row<T, DB>(dvr, mine && !part, dv, vf, lane, D);
+    }
+    if (part && mine) {
+        float* to = far_row(p, b, h, tile, far ? chunk + 1 : 0, j - j0);
+        const int64_t other = (int64_t)p.far_rows * D;
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int d = 32 * db + 8 * q + 4 * (lane >> 5);
+                if (d >= D) continue;
+                f32x4 x, y;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = dk[db][4 * q + i] * kf;
+                    y[i] = dv[db][4 * q + i] * vf;
+                }
+                *reinterpret_cast<f32x4*>(to + d) = x;
+                *reinterpret_cast<f32x4*>(to + other + d) = y;
+            }
+    }
+}
+
+// The first tokens' rows of dK and dV: the parts of the tokens near and far, added in order.  32 threads to a row, 4 columns each.
+template <typename TT>
+__global__ __launch_bounds__(64) void attn_far_kernel(AttnArgs p) {
+    typedef typename TT::type T;
+    typedef T V4 __attribute__((ext_vector_type(4)));
+    const maxsim_attn& a = p.a;
+    const int keys = min(a.sinks, a.max_k), j = blockIdx.x % keys, pair = blockIdx.x / keys, h = pair % a.Hk, b = pair / a.Hk;
+    const Seq s = sequence(a, b);
+    const int d = (threadIdx.x & 31) * 4, tile = j / kRows, j0 = tile * kRows;
+    if (j >= s.lk || d >= a.D) return;
+    const bool of_v = threadIdx.x >= 32;
+    const int chunks = (max(s.lq - far_from(a, s, j0), 0) + p.far_tokens - 1) / p.far_tokens;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    for (int n = 0; n <= chunks; ++n)
+        sum += *reinterpret_cast<const f32x4*>(far_row(p, b, h, tile, n, j - j0) + (of_v ? (int64_t)p.far_rows * a.D : 0) + d);
+    const maxsim_view& out = of_v ? p.dv : p.dk;
+    V4 y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = (T)sum[i];
+    *reinterpret_cast<V4*>(first<T>(out, a.cu_k != nullptr, b, s.k0, h) + (int64_t)j * out.token + d) = y;
+}
+
+// Where first tokens stay visible past the window, their key tile would go over all queries and the others over a
+// window's worth.  With more than two such stretches of queries the far ones get workgroups of their own.
+void plan_far(const maxsim_attn& a, AttnArgs& p) {
+    p.far_tiles = p.far_chunks = p.far_tokens = p.far_rows = 0;
+    if (a.sinks == 0 || a.left < 0 || a.max_k == 0 || a.sinks > 2 * kRows) return;
+    const int64_t right = a.right < 0 ? 0 : a.right, stretch = ((int64_t)kRows + a.left + right + 63) / 64 * 64;
+    if (a.max_q <= 2 * stretch) return;
+    p.far_tokens = (int)stretch;
+    p.far_chunks = (int)((a.max_q + stretch - 1) / stretch);
+    const int keys = a.sinks < a.max_k ? a.sinks : a.max_k;
+    p.far_tiles = (keys + kRows - 1) / kRows;
+    p.far_rows = keys < kRows ? keys : kRows;
+}
+int64_t far_floats(const maxsim_attn& a, const AttnArgs& p) {
+    return (int64_t)a.B * a.Hk * p.far_tiles * (p.far_chunks + 1) * 2 * p.far_rows * a.D;
 }
 
 template <typename TT, int DP>
 hipError_t launch(const AttnArgs& p, hipStream_t stream) {
     const maxsim_attn& a = p.a;
-    const int64_t q_tiles = ((int64_t)a.max_q * p.group + kRows - 1) / kRows, k_tiles = ((int64_t)a.max_k + kRows - 1) / kRows;
+    const int64_t pairs = (int64_t)a.B * a.Hk;
     // (of no queries, or no keys, the rows of no sequence are still to be made 0)
-    const int q_blocks = (int)(q_tiles > 0 ? q_tiles : 1), k_blocks = (int)(k_tiles > 0 ? k_tiles : 1);
-    attn_dq_kernel<TT, DP><<<(unsigned)(q_blocks * a.Hk * a.B), 64 * kWaves, 0, stream>>>(p, q_blocks);
-    const hipError_t e = hipGetLastError();
+    const int q_tiles = (int)std::max<int64_t>(1, ((int64_t)a.max_q * p.group + kRows - 1) / kRows);
+    const int k_tiles = std::max(1, (a.max_k + kRows - 1) / kRows), each = k_tiles + p.far_tiles * p.far_chunks;
+    attn_dq_kernel<TT, DP><<<(unsigned)blocks_for(pairs, q_tiles), 64 * kWaves, 0, stream>>>(p, q_tiles);
+    hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    attn_dkv_kernel<TT, DP><<<(unsigned)(k_blocks * a.Hk * a.B), 64 * kWaves, 0, stream>>>(p, k_blocks);
+    const int64_t blocks = blocks_for(pairs, each);
+    // a width of 128: two workgroups to a CU where there are so many
+    const auto dkv = DP == 128 && blocks <= 384 ? attn_dkv_kernel<TT, DP, DP == 128 ? 1 : 2> : attn_dkv_kernel<TT, DP, 2>;
+    dkv<<<(unsigned)blocks, 64 * kWaves, 0, stream>>>(p, k_tiles);
+    e = hipGetLastError();
+    if (e != hipSuccess || p.far_chunks == 0) return e;
+    attn_far_kernel<TT><<<(unsigned)(pairs * std::min(a.sinks, a.max_k)), 64, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 int64_t rows_in_memory(const maxsim_attn& a) { return a.cu_q ? a.rows_q : (int64_t)a.B * a.max_q; }
+int64_t stat_floats(const maxsim_attn& a) {  // the parts after them start at a multiple of 16 bytes
+    return ((a.dtype == MAXSIM_F16 ? 3 : 2) * rows_in_memory(a) * a.Hq + 3) / 4 * 4;
+}
 
 }  // namespace
 
 size_t attn_bwd_workspace_bytes(const maxsim_attn& a) {
-    return (size_t)(a.dtype == MAXSIM_F16 ? 3 : 2) * (size_t)rows_in_memory(a) * a.Hq * sizeof(float);
+    AttnArgs p{};
+    plan_far(a, p);
+    return (size_t)(stat_floats(a) + far_floats(a, p)) * sizeof(float);
 }
 
 hipError_t launch_attn_bwd(const maxsim_attn& a, const float* lse, const maxsim_view& dout, const maxsim_view& dq,
                            const maxsim_view& dk, const maxsim_view& dv, void* workspace, hipStream_t stream) {
     AttnArgs p{};
+    plan_far(a, p);
     p.a = a;
     if (a.left < 0 || a.left > kNoBound) p.a.left = kNoBound;
     if (a.right < 0 || a.right > kNoBound) p.a.right = kNoBound;
@@ -337,6 +452,7 @@ hipError_t launch_attn_bwd(const maxsim_attn& a, const float* lse, const maxsim_
     p.splits = 1;
     p.rows = rows_in_memory(a);
     p.row_stat = static_cast<float*>(workspace);
+    p.part_far = p.row_stat + stat_floats(a);
     const bool half = a.dtype == MAXSIM_F16;
     if (a.D <= 64) return half ? launch<F16, 64>(p, stream) : launch<BF16, 64>(p, stream);
     return half ? launch<F16, 128>(p, stream) : launch<BF16, 128>(p, stream);

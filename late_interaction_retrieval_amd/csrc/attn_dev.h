@@ -125,12 +125,52 @@ __device__ __forceinline__ Span span_of(const maxsim_attn& a, int lk, int p_lo, 
     return s;
 }
 
-// Work items in order of their blocks' dispatch: blocks go round-robin over the 8 XCDs, and each
-// XCD gets a run of neighbouring items, which share keys in its L2.
-__device__ __forceinline__ int item_of_block() {
-    const int total = gridDim.x, xcd = blockIdx.x & 7, each = total >> 3, more = total & 7;
-    return xcd * each + min(xcd, more) + (int)(blockIdx.x >> 3);
+// What a block works on: sequence b, key head h, and one of the `each` parts of their work.  Blocks go round-robin over
+// the 8 XCDs; the parts of one (b, h) read the same keys and go to one XCD, whose L2 holds them.  Many (b, h), of
+// lengths that differ, are dealt out in turn; few of them in runs, which leave no XCD without work (16 sequences of
+// 700 to 1024 tokens and 4 key heads: TODO).
+struct Work {
+    int b, h, part;
+    int items;  // in all: B * Hk * each
+    __device__ __forceinline__ int item(int each, int Hk) const { return (b * Hk + h) * each + part; }
+};
+inline __host__ __device__ bool dealt(int64_t pairs) { return pairs % 8 == 0 || pairs >= 64; }
+// Blocks to launch for that.
+inline int64_t blocks_for(int64_t pairs, int64_t each) { return (dealt(pairs) ? ceil_div(pairs, 8) * 8 : pairs) * each; }
+// False: nothing for this block.
+__device__ __forceinline__ bool work_of(Work& w, int B, int Hk, int each) {
+    const int pairs = B * Hk, xcd = blockIdx.x & 7, at = (int)(blockIdx.x >> 3);
+    int pair;
+    if (dealt(pairs)) {
+        pair = at / each * 8 + xcd;
+        w.part = at % each;
+    } else {
+        const int total = gridDim.x, run = total >> 3, more = total & 7;
+        const int id = xcd * run + min(xcd, more) + at;
+        pair = id / each;
+        w.part = id % each;
+    }
+    w.b = pair / Hk;
+    w.h = pair % Hk;
+    w.items = pairs * each;
+    return pair < pairs;
 }
+
+// A lane's values of a block of 32 keys (or rows), in the slots' order, as bits: those from `low` up to `top`, and those
+// below `sink`, all counted from the lane's first slot.
+__device__ __forceinline__ uint32_t slots_below(int n) {  // n slots' worth of bits below place n
+    n = max(0, min(n, 32));
+    const uint32_t count = 4 * (n >> 3) + min(n & 7, 4);
+    return (1u << count) - 1;  // 16 at most
+}
+__device__ __forceinline__ uint32_t slots_seen(int low, int top, int sink) {
+    return slots_below(top + 1) & (~slots_below(low) | slots_below(sink));
+}
+__device__ __forceinline__ float keep(uint32_t bits, int i, float v, uint32_t other) {
+    const uint32_t m = (uint32_t)((int)(bits << (31 - i)) >> 31);
+    return __uint_as_float((fbits(v) & m) | (other & ~m));
+}
+constexpr uint32_t kMinusInfinity = 0xff800000u;
 
 // A tile in LDS: rows of DP values (DP * 2 bytes = NCH chunks of 16 bytes), chunk c of row r at
 // place c ^ turn(r) of its row.  16 rows that follow each other, read at one chunk, lie in 16 different
@@ -175,10 +215,14 @@ struct Loader {
 };
 
 // A operand from a tile's rows: row l % 32 of a block of 32, values 16 kk + 8 (l / 32) on.
+template <int DP>
+__device__ __forceinline__ int row_place(int lane, int kk) {
+    const int r = lane & 31, c = 2 * kk + (lane >> 5);
+    return r * Tile<DP>::ROW + ((c ^ Tile<DP>::turn(r)) << 4);
+}
 template <typename T, int DP>
 __device__ __forceinline__ typename Vec8<T>::V rows_at(const uint8_t* block, int lane, int kk) {
-    const int r = lane & 31, c = 2 * kk + (lane >> 5);
-    return *reinterpret_cast<const typename Vec8<T>::V*>(block + r * Tile<DP>::ROW + ((c ^ Tile<DP>::turn(r)) << 4));
+    return *reinterpret_cast<const typename Vec8<T>::V*>(block + row_place<DP>(lane, kk));
 }
 // A operand from a tile transposed: column 32 db + l % 32 of its rows slot(l / 32, 0 .. 7) from row 16 t of `block` on.
 template <typename T, int DP>

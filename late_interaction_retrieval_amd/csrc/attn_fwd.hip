@@ -41,12 +41,19 @@ struct Rows {
         hi = min(pos + a.right, lk - 1);
     }
 
-    // NB blocks of 32 keys from key j0 on; those from `end` on are no keys.  whole: all of them are seen by all rows.
+    // Which of a block's keys from j0 on, before `end`, the lane's row sees.
+    __device__ __forceinline__ uint32_t bits(int j0, int end, int sinks, int lane) const {
+        const int j = j0 + 4 * (lane >> 5);
+        return slots_seen(lo - j, min(hi, end - 1) - j, sinks - j);
+    }
+
+    // NB blocks of 32 keys.  all: every row sees all of them; else bits[nb] are the lane's.  (Leaving out a block that no
+    // row sees, by a branch, was slower: 88 -> 98 us over ragged documents, 284 -> 300 over whole rows of 4096 keys.)
     // The reference stays while the maximum passes it by less than 2^8: P grows to 256 at most, which both types hold,
     // and relative to the row's sum nothing is lost.
     template <int NB>
-    __device__ __forceinline__ void step(const uint8_t* kt, const uint8_t* vt, int lane, int j0, int end, bool whole, int sinks,
-                                         float c, float slack) {
+    __device__ __forceinline__ void step(const uint8_t* kt, const uint8_t* vt, int lane, bool all, const uint32_t* bits, float c,
+                                         float slack) {
         f32x16 s[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
@@ -54,16 +61,11 @@ struct Rows {
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) s[nb] = mma<T>(rows_at<T, DP>(kt + nb * 32 * Tile<DP>::ROW, lane, kk), q[kk], s[nb]);
         }
-        if (!whole) {
-            const int j = j0 + 4 * (lane >> 5);
-            const int top = min(hi, end - 1) - j, low = lo - j, sink = sinks - j;
+        if (!all) {
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int at = 32 * nb + slot(i);
-                    s[nb][i] = at <= top && (at >= low || at < sink) ? s[nb][i] : -INFINITY;
-                }
+                for (int i = 0; i < 16; ++i) s[nb][i] = keep(bits[nb], i, s[nb][i], kMinusInfinity);
         }
         float m = s[0][0];
 #pragma unroll
@@ -82,62 +84,52 @@ struct Rows {
                 for (int i = 0; i < 16; ++i) o[db][i] *= f;
         }
         const float base = ref == -INFINITY ? 0.f : -ref * c;  // a row that has seen nothing yet
+        float part[4] = {0.f, 0.f, 0.f, 0.f};  // chains that do not wait for each other
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 s[nb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[nb][i], c, base));
-                sum += s[nb][i];
+                part[i & 3] += s[nb][i];
             }
+        sum += (part[0] + part[1]) + (part[2] + part[3]);
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const typename Vec8<T>::V p = pack8<T>(s[nb], 8 * t);
 #pragma unroll
                 for (int db = 0; db < DB; ++db) o[db] = mma<T>(cols_at<T, DP>(vt, lane, 2 * nb + t, db), p, o[db]);
             }
+        }
     }
 };
 
-// What a workgroup works on.
-struct Item {
-    int b, h, split, tile;  // sequence, key head
-};
-__device__ __forceinline__ Item item_of(int id, int tiles, int splits, int heads) {
-    Item w;
-    w.tile = tiles - 1 - id % tiles;  // with a causal bound the last rows see the most keys: first
-    id /= tiles;
-    w.split = id % splits;
-    id /= splits;
-    w.h = id % heads;
-    w.b = id / heads;
-    return w;
-}
-
 // Row r of a sequence and key head: query token r / group, head r % group of those that share the key head.
 template <typename TT, int DP>
-__global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnArgs p, int tiles) {
+__global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : 2) void attn_fwd_kernel(AttnArgs p, int tiles) {
     typedef typename TT::type T;
     typedef Rows<T, DP> R;
     constexpr int BYTES = kKeys * Tile<DP>::ROW;
     // separate arrays: the compiler then sees that a tile's reads and the next one's loads touch different memory
     __shared__ __align__(16) uint8_t k_0[BYTES], v_0[BYTES], k_1[BYTES], v_1[BYTES];
     const maxsim_attn& a = p.a;
-    const int id = item_of_block();
-    const Item w = item_of(id, tiles, p.splits, a.Hk);
+    Work w;
+    if (!work_of(w, a.B, a.Hk, tiles * p.splits)) return;
+    // with a causal bound the last rows see the most keys: first
+    const int split = w.part / tiles, tile = tiles - 1 - w.part % tiles;
     const Seq s = sequence(a, w.b);
     const int G = p.group, D = a.D, rows = s.lq * G;
     if (a.zero_rest && p.splits == 1)
-        zero_rest<T>(a.out, p.lse, a.lse_step, a.cu_q, a.B, a.rows_q, w.b, s.q0, s.lq, s.all_q, a.Hq, D, w.h * tiles + w.tile,
-                     a.Hk * tiles, id, (int)gridDim.x);
-    const int r0 = w.tile * kRows;
+        zero_rest<T>(a.out, p.lse, a.lse_step, a.cu_q, a.B, a.rows_q, w.b, s.q0, s.lq, s.all_q, a.Hq, D, w.h * tiles + tile,
+                     a.Hk * tiles, w.item(tiles, a.Hk), w.items);
+    const int r0 = tile * kRows;
     if (r0 >= rows) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int shift = s.lk - s.lq;
     const int last = min(r0 + kRows, rows) - 1;
     const Span span = span_of(a, s.lk, r0 / G + shift, last / G + shift, kKeys);
-    const int t0 = (int)((int64_t)span.tiles * w.split / p.splits), t1 = (int)((int64_t)span.tiles * (w.split + 1) / p.splits);
+    const int t0 = (int)((int64_t)span.tiles * split / p.splits), t1 = (int)((int64_t)span.tiles * (split + 1) / p.splits);
 
     const int wr = r0 + wave * kRowsWave;
     const int r = min(wr + (lane & 31), rows - 1), token = r / G, head = w.h * G + r % G;
@@ -147,6 +139,10 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnArgs p, in
     // the wave's rows: the positions between which they lie
     const int p_lo = min(wr, rows - 1) / G + shift, p_hi = min(wr + kRowsWave - 1, rows - 1) / G + shift;
     const float c = a.scale * kLog2e, slack = 8.f / c;
+
+    const auto all_see = [&](int j, int end) {
+        return j + kKeys <= end && j + kKeys - 1 <= min(p_lo + a.right, s.lk - 1) && (j >= p_hi - a.left || j + kKeys <= a.sinks);
+    };
 
     const T* ks = first<T>(a.k, a.cu_k != nullptr, w.b, s.k0, w.h);
     const T* vs = first<T>(a.v, a.cu_k != nullptr, w.b, s.k0, w.h);
@@ -159,10 +155,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnArgs p, in
         lv.load(vs + (int64_t)j * a.v.token, s.lk - j, a.v.token, D, vt, wave);
     };
     const auto work = [&](int t, const uint8_t* kt, const uint8_t* vt) {
-        const int j = span.at(t, kKeys), end = span.end(t), j_last = j + kKeys - 1;
-        if (wr >= rows || j > p_hi + a.right || (j_last < p_lo - a.left && j >= a.sinks)) return;  // nothing to see
-        const bool whole = j_last < end && j_last <= min(p_lo + a.right, s.lk - 1) && (j >= p_hi - a.left || j_last < a.sinks);
-        row.template step<kKeys / 32>(kt, vt, lane, j, end, whole, a.sinks, c, slack);
+        const int j = span.at(t, kKeys), end = span.end(t);
+        if (wr >= rows) return;
+        if (j > p_hi + a.right || (j + kKeys - 1 < p_lo - a.left && j >= a.sinks)) return;  // none sees any
+        const bool all = all_see(j, end);
+        uint32_t bits[kKeys / 32] = {};
+        if (!all) {
+#pragma unroll
+            for (int nb = 0; nb < kKeys / 32; ++nb) bits[nb] = row.bits(j + 32 * nb, end, a.sinks, lane);
+        }
+        row.template step<kKeys / 32>(kt, vt, lane, all, bits, c, slack);
     };
     if (t0 < t1) load(t0, k_0, v_0);
     for (int t = t0; t < t1; t += 2) {
@@ -186,7 +188,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_fwd_kernel(AttnArgs p, in
         if (p.lse && mine && lane < 32)
             p.lse[at * a.lse_step] = is_zero(sum) ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * kLn2;
     } else if (mine) {
-        const int64_t part = (int64_t)w.split * p.rows * a.Hq + at;
+        const int64_t part = (int64_t)split * p.rows * a.Hq + at;
         if (lane < 32) {
             p.part_ml[2 * part] = top;
             p.part_ml[2 * part + 1] = sum;
@@ -215,18 +217,19 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_few_kernel(AttnArgs p
     __shared__ __align__(16) uint8_t k_0[kWaves * BYTES], v_0[kWaves * BYTES], k_1[kWaves * BYTES], v_1[kWaves * BYTES];
     __shared__ __align__(16) float joined[kWaves][32][2];
     const maxsim_attn& a = p.a;
-    const int id = item_of_block();
-    const Item w = item_of(id, 1, p.splits, a.Hk);
+    Work w;
+    if (!work_of(w, a.B, a.Hk, p.splits)) return;
+    const int split = w.part;
     const Seq s = sequence(a, w.b);
     const int G = p.group, D = a.D, rows = s.lq * G;
     if (a.zero_rest && p.splits == 1)
-        zero_rest<T>(a.out, p.lse, a.lse_step, a.cu_q, a.B, a.rows_q, w.b, s.q0, s.lq, s.all_q, a.Hq, D, w.h, a.Hk, id, (int)gridDim.x);
+        zero_rest<T>(a.out, p.lse, a.lse_step, a.cu_q, a.B, a.rows_q, w.b, s.q0, s.lq, s.all_q, a.Hq, D, w.h, a.Hk, w.item(1, a.Hk), w.items);
     if (rows <= 0) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int shift = s.lk - s.lq;
     const int p_lo = shift, p_hi = (rows - 1) / G + shift;
     const Span span = span_of(a, s.lk, p_lo, p_hi, kKeysFew);
-    const int t0 = (int)((int64_t)span.tiles * w.split / p.splits), t1 = (int)((int64_t)span.tiles * (w.split + 1) / p.splits);
+    const int t0 = (int)((int64_t)span.tiles * split / p.splits), t1 = (int)((int64_t)span.tiles * (split + 1) / p.splits);
     const int r = min(lane & 31, rows - 1), token = r / G, head = w.h * G + r % G;
     R row;
     row.start(first<T>(a.q, a.cu_q != nullptr, w.b, s.q0, 0) + (int64_t)token * a.q.token + (int64_t)head * a.q.head, lane, D,
@@ -244,9 +247,10 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_few_kernel(AttnArgs p
         lv.load(vs + (int64_t)j * a.v.token, s.lk - j, a.v.token, D, vt + wave * BYTES, 0);
     };
     const auto work = [&](int t, const uint8_t* kt, const uint8_t* vt) {
-        const int j = span.at(t, kKeysFew), end = span.end(t), j_last = j + kKeysFew - 1;
-        const bool whole = j_last < end && j_last <= min(p_lo + a.right, s.lk - 1) && (j >= p_hi - a.left || j_last < a.sinks);
-        row.template step<1>(kt + wave * BYTES, vt + wave * BYTES, lane, j, end, whole, a.sinks, c, slack);
+        const int j = span.at(t, kKeysFew), end = span.end(t);
+        const bool whole = j + 32 <= end && j + 31 <= min(p_lo + a.right, s.lk - 1) && (j >= p_hi - a.left || j + 32 <= a.sinks);
+        const uint32_t bits = whole ? 0u : row.bits(j, end, a.sinks, lane);
+        row.template step<1>(kt + wave * BYTES, vt + wave * BYTES, lane, whole, &bits, c, slack);
     };
     const auto landed = [&](bool ahead) {  // the tile's loads; those of the next one may stay on their way
         asm volatile("" ::: "memory");
@@ -298,7 +302,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_few_kernel(AttnArgs p
         if (p.splits == 1) {
             if (p.lse) p.lse[at * a.lse_step] = is_zero(total) ? -INFINITY : (most + __builtin_amdgcn_logf(total)) * kLn2;
         } else {
-            const int64_t part = (int64_t)w.split * p.rows * a.Hq + at;
+            const int64_t part = (int64_t)split * p.rows * a.Hq + at;
             p.part_ml[2 * part] = most == -INFINITY ? 0.f : most;
             p.part_ml[2 * part + 1] = total;
         }
@@ -321,7 +325,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_few_kernel(AttnArgs p
                           (int64_t)head * a.out.head + d,
                       rest ? rest + d : nullptr, v);
         } else {
-            *reinterpret_cast<f32x4*>(p.part_o + ((int64_t)w.split * p.rows * a.Hq + at) * D + d) = v;
+            *reinterpret_cast<f32x4*>(p.part_o + ((int64_t)split * p.rows * a.Hq + at) * D + d) = v;
         }
     }
 }
@@ -389,7 +393,7 @@ Plan plan_of(const maxsim_attn& a) {
     int64_t splits = base > 0 ? wanted / base : 1;
     splits = std::min(splits, keys / least);
     p.splits = rows > 0 ? (int)std::max<int64_t>(1, std::min<int64_t>(splits, 64)) : 1;
-    p.blocks = base * p.splits;
+    p.blocks = blocks_for((int64_t)a.Hk * a.B, (int64_t)p.tiles * p.splits);
     return p;
 }
 int64_t join_groups(const maxsim_attn& a) { return ((int64_t)a.max_q * a.Hq + 7) / 8; }
@@ -411,10 +415,9 @@ size_t attn_fwd_workspace_bytes(const maxsim_attn& a) {
 }
 
 bool attn_grid_ok(const maxsim_attn& a) {
-    const int64_t most = (int64_t)1 << 23;
-    const int64_t q_tiles = ((int64_t)a.max_q * (a.Hq / a.Hk) + kRows - 1) / kRows, k_tiles = ((int64_t)a.max_k + 127) / 128;
-    return (std::max(q_tiles, k_tiles) + 1) * a.Hk < most && (std::max(q_tiles, k_tiles) + 1) * a.Hk * a.B < most &&
-           join_groups(a) * a.B < most;
+    const int64_t most = (int64_t)1 << 21, pairs = (int64_t)a.Hk * a.B;
+    const int64_t q_tiles = ((int64_t)a.max_q * (a.Hq / a.Hk) + kRows - 1) / kRows, k_tiles = ((int64_t)a.max_k + kRows - 1) / kRows;
+    return pairs < most && (std::max(q_tiles, k_tiles) + 1) * pairs < most;
 }
 
 hipError_t launch_attn_fwd(const maxsim_attn& a, float* lse, void* workspace, hipStream_t stream) {

@@ -32,7 +32,12 @@ struct AttnArgs {
     float* part_o;   // [splits][rows][Hq][D]
     float* part_ml;  // [splits][rows][Hq][2]
     int64_t rows;    // of q in memory
-    float* row_stat; // backward: [2][Hq][rows]: lse in powers of 2 (+infinity where it is -infinity), rowsum(dO * out)
+    float* row_stat; // backward: [2][Hq][rows]: lse in powers of 2 (+infinity where it is -infinity), rowsum(dO * out);
+                     // fp16: a third, the rows' largest |dO|
+    // Backward: queries past the window see the first tokens' keys alone.  They are worked on apart, `far_tokens` at a
+    // time, and their sums joined: part_far [B * Hk][key tiles with first tokens][far_chunks + 1][dk, dv][far_rows][D].
+    int far_tiles, far_chunks, far_tokens, far_rows;
+    float* part_far;
 };
 constexpr int kNoBound = 1 << 29;  // past every position
 
