@@ -118,12 +118,13 @@ def lib():
 
 
 lib()  # fail loudly at import time if the native library is missing
-try:  # the usual calls of the embedding head's operators, natively (fast_binding.cpp)
+try:  # the usual calls of the operators around MaxSim, natively (fast_binding.cpp)
     from . import _fast
 except ImportError as e:  # not built, or built against another torch: all of them go through ctypes
     warnings.warn("late_interaction_retrieval_amd: no _fast.so (%s): calls take some microseconds more" % e, RuntimeWarning)
     _fast = types.SimpleNamespace(**{name: lambda *args: None for name in ("rmsnorm_fwd", "rmsnorm_bwd", "quant_fp8",
-                                                                         "gemm_fp8", "adamw")})
+                                                                         "gemm_fp8", "adamw", "rope", "attn_fwd", "attn_bwd",
+                                                                         "distill_fwd", "distill_bwd")})
 
 
 def _ptr(t):
@@ -1267,6 +1268,10 @@ def maxsim_rope(x, inv_freq, positions=None, offsets=None, layout="half", scale=
     offsets [B] int32, the position of each sequence's first token; or neither: from 0 on.  inverse: turned back (the
     gradient of x from that of the result).  out may be x.  Returns out.
     """
+    if out is None and stream is None:
+        got = _fast.rope(x, inv_freq, positions, offsets, layout, scale, inverse)
+        if got is not None:
+            return got
     return _rope(x, inv_freq, positions, offsets, layout, scale, inverse, out, stream=stream)
 
 
@@ -1397,6 +1402,10 @@ def maxsim_attn_fwd(q, k, v, scale=None, window=(-1, -1), sinks=0, q_lens=None, 
     what rounding left off out; a contiguous one does for it too, with a less exact rowsum(dO * out).  Rows of no sequence are zeros in outputs made here, and left as
     they were in those that are given.
     """
+    if out is None and lse is None and workspace is None and stream is None:
+        got = _fast.attn_fwd(q, k, v, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k, with_lse)
+        if got is not None:
+            return got
     return _attn_fwd(q, k, v, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k, with_lse, out, lse, workspace,
                      stream=stream)
 
@@ -1430,6 +1439,10 @@ def maxsim_attn_bwd(dout, q, k, v, out, lse, scale=None, window=(-1, -1), sinks=
     """Backward of maxsim_attn_fwd, whose out and lse it takes with the same arguments.  Returns (dq, dk, dv); what queries
     give to a shared head of k and v is summed in fp32.  Rows of no sequence are zeros in gradients made here, and left
     as they were where all three are given."""
+    if dq is None and dk is None and dv is None and workspace is None and stream is None:
+        got = _fast.attn_bwd(dout, q, k, v, out, lse, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k)
+        if got is not None:
+            return got
     return _attn_bwd(dout, q, k, v, out, lse, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k, dq, dk, dv,
                      workspace, stream=stream)
 
@@ -1495,6 +1508,10 @@ def maxsim_distill_fwd(scores, index, teacher, temperature=1.0, loss=None, stat=
     q = softmax(teacher / T) over the row's entries and p = softmax(scores / T) over its columns,
     T^2 sum_k q_k (log q_k - log p[index_k]).  index [N, K] int32 (an index outside [0, V) is no entry), teacher [N, K]
     fp32, K <= 1024.  Returns (loss [N], stat [N, 2]) fp32; the backward takes stat."""
+    if loss is None and stat is None and workspace is None and stream is None:
+        got = _fast.distill_fwd(scores, index, teacher, temperature)
+        if got is not None:
+            return got
     return _distill_fwd(scores, index, teacher, temperature, loss, stat, workspace, stream=stream)
 
 
@@ -1529,6 +1546,10 @@ def _distill_fwd(scores, index, teacher, temperature, loss, stat, workspace):
 def maxsim_distill_bwd(dloss, scores, stat, index, teacher, temperature=1.0, dscores=None, stream=None):
     """The gradient of scores from that of the rows' losses, dloss [N] fp32, with maxsim_distill_fwd's stat:
     dloss T (p - the entries' q).  dscores may be scores.  Returns dscores [N, V] of scores' type."""
+    if dscores is None and stream is None:
+        got = _fast.distill_bwd(dloss, scores, stat, index, teacher, temperature)
+        if got is not None:
+            return got
     return _distill_bwd(dloss, scores, stat, index, teacher, temperature, dscores, stream=stream)
 
 

@@ -1,6 +1,6 @@
-// fast_binding.cpp -- the usual calls of binding.py's embedding-head operators
-// as a Python extension (_fast.so): on small tensors the interpreter's share of a
-// call (6 us) was more than the kernel's.
+// fast_binding.cpp -- the usual calls of binding.py's operators of the embedding head, the attention layer and
+// the distillation loss as a Python extension (_fast.so): on small tensors the interpreter's share of a
+// call (6 us and more) was more than the kernel's.
 //
 // Each function takes its binding function's main arguments.  It makes the call where
 // they are plain -- contiguous tensors of the right types and sizes on the
@@ -18,9 +18,11 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <cmath>
 #include <vector>
 
 #include "maxsim_encoder.h"
+#include "maxsim_layers.h"
 
 namespace {
 
@@ -286,8 +288,219 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// Rows of heads [.., heads, width] of these sizes and type on this device, as the library's view.
+bool view_of(const Tensor& t, at::IntArrayRef sizes, at::ScalarType type, at::Device dev, maxsim_view& v) {
+    if (t.scalar_type() != type || t.device() != dev || t.sizes() != sizes) return false;
+    const int64_t n = t.dim(), width = t.size(n - 1);
+    if (width > 1 && t.stride(n - 1) != 1) return false;
+    v.data = t.data_ptr();
+    v.head = t.size(n - 2) > 1 ? t.stride(n - 2) : width;
+    v.token = t.size(n - 3) > 1 ? t.stride(n - 3) : width * t.size(n - 2);
+    v.batch = n == 4 && t.size(0) > 1 ? t.stride(0) : 0;
+    return true;
+}
+bool int32s(const Tensor* t, int64_t n, at::Device dev, const int32_t** to) {
+    *to = nullptr;
+    if (!t) return true;
+    if (!good(*t, at::kInt, dev) || t->numel() != n) return false;
+    *to = t->data_ptr<int32_t>();
+    return true;
+}
+// An int that fits 32 bits; None where `none` is given.
+bool int_of(PyObject* o, int32_t& to, const int64_t* none = nullptr) {
+    if (none && o == Py_None) {
+        if (!fits(*none)) return false;
+        to = (int32_t)*none;
+        return true;
+    }
+    if (!PyLong_Check(o)) return false;
+    const long v = PyLong_AsLong(o);
+    if (v == -1 && PyErr_Occurred()) PyErr_Clear();
+    to = (int32_t)v;
+    return v == to;
+}
+
+// (x, inv_freq, positions, offsets, layout, scale, inverse) -> out
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    bool plain = n == 7 && PyUnicode_Check(a[4]) && PyFloat_Check(a[5]);
+    if (!plain) Py_RETURN_NONE;
+    const Tensor *x = tensor(a[0], plain), *f = tensor(a[1], plain), *pos = tensor(a[2], plain), *off = tensor(a[3], plain);
+    const int inverse = PyObject_IsTrue(a[6]);
+    if (inverse < 0) return nullptr;
+    const bool half = PyUnicode_CompareWithASCIIString(a[4], "half") == 0;
+    if (!plain || !x || !f || (!half && PyUnicode_CompareWithASCIIString(a[4], "interleaved") != 0) || !on_current(*x) ||
+        (x->dim() != 3 && x->dim() != 4))
+        Py_RETURN_NONE;
+    const at::Device dev = x->device();
+    const int code = code_of(x->scalar_type());
+    const int64_t B = x->dim() == 4 ? x->size(0) : 1, L = x->size(x->dim() - 3), H = x->size(x->dim() - 2), D = x->size(x->dim() - 1);
+    maxsim_view xv, yv;
+    const int32_t *p, *o;
+    if (!is_float(code) || !fits(B) || !fits(L) || !fits(H) || !fits(D) || !good(*f, at::kDouble, dev) || !fits(2 * f->numel()) ||
+        !int32s(pos, B * L, dev, &p) || !int32s(off, B, dev, &o) || !view_of(*x, x->sizes(), x->scalar_type(), dev, xv))
+        Py_RETURN_NONE;
+    Tensor y = empty(x->sizes(), *x, x->scalar_type());
+    view_of(y, x->sizes(), x->scalar_type(), dev, yv);
+    if (maxsim_rope(&xv, &yv, (int32_t)B, (int32_t)L, (int32_t)H, (int32_t)D, (int32_t)(2 * f->numel()), half ? 0 : 1, code,
+                    f->data_ptr<double>(), p, o, (float)PyFloat_AS_DOUBLE(a[5]), inverse, stream_of(*x)) != MAXSIM_OK)
+        Py_RETURN_NONE;
+    return wrap(y);
+    END_HANDLE_TH_ERRORS
+}
+
+// The ten arguments that attention's two directions share (scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q,
+// max_k from a[0] on) with q, k and v, as the library's struct.  False: not a plain call.
+bool attn_of(const Tensor& q, const Tensor& k, const Tensor& v, PyObject* const* a, maxsim_attn& s) {
+    bool plain = PyTuple_Check(a[1]) && PyTuple_GET_SIZE(a[1]) == 2 && (a[0] == Py_None || PyFloat_Check(a[0]));
+    if (!plain) return false;
+    const Tensor *ql = tensor(a[3], plain), *kl = tensor(a[4], plain), *cq = tensor(a[5], plain), *ck = tensor(a[6], plain);
+    if (!plain || (ql && cq) || (kl && ck) || q.dim() != (cq ? 3 : 4) || k.dim() != (ck ? 3 : 4) || !on_current(q)) return false;
+    const at::Device dev = q.device();
+    const at::ScalarType type = q.scalar_type();
+    const int64_t B = cq ? cq->numel() - 1 : q.size(0), D = q.size(q.dim() - 1), Hq = q.size(q.dim() - 2), Hk = k.size(k.dim() - 2);
+    const int64_t Lq = cq ? -1 : q.size(1), Lk = ck ? -1 : k.size(1);
+    if (B != (ck ? ck->numel() - 1 : k.size(0)) || k.size(k.dim() - 1) != D || !fits(B) || !fits(Hq) || !fits(Hk) || !fits(D) || B < 1)
+        return false;
+    s = maxsim_attn{};
+    if (!view_of(q, q.sizes(), type, dev, s.q) || !view_of(k, k.sizes(), type, dev, s.k) || !view_of(v, k.sizes(), type, dev, s.v) ||
+        !int32s(cq, B + 1, dev, &s.cu_q) || !int32s(ck, B + 1, dev, &s.cu_k) || !int32s(ql, B, dev, &s.q_lens) ||
+        !int32s(kl, B, dev, &s.k_lens))
+        return false;
+    // (without cu the sizes are the bounds, whatever max_q and max_k say)
+    if (cq ? !int_of(a[7], s.max_q) : !fits(Lq)) return false;
+    if (ck ? !int_of(a[8], s.max_k) : !fits(Lk)) return false;
+    if (!cq) s.max_q = (int32_t)Lq;
+    if (!ck) s.max_k = (int32_t)Lk;
+    if (!int_of(PyTuple_GET_ITEM(a[1], 0), s.left) || !int_of(PyTuple_GET_ITEM(a[1], 1), s.right) || !int_of(a[2], s.sinks)) return false;
+    s.rows_q = cq ? q.size(0) : 0;
+    s.rows_k = ck ? k.size(0) : 0;
+    s.B = (int32_t)B;
+    s.Hq = (int32_t)Hq;
+    s.Hk = (int32_t)Hk;
+    s.D = (int32_t)D;
+    s.dtype = code_of(type);
+    s.scale = a[0] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : (float)PyFloat_AS_DOUBLE(a[0]);
+    s.lse_step = 1;
+    return true;
+}
+
+// (q, k, v, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k, with_lse) -> (out, lse)
+PyObject* attn_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    bool plain = n == 13;
+    if (!plain) Py_RETURN_NONE;
+    const Tensor *q = tensor(a[0], plain), *k = tensor(a[1], plain), *v = tensor(a[2], plain);
+    const int lse_wanted = PyObject_IsTrue(a[12]);
+    if (lse_wanted < 0) return nullptr;
+    maxsim_attn s;
+    if (!plain || !q || !k || !v || !attn_of(*q, *k, *v, a + 3, s)) Py_RETURN_NONE;
+    Tensor out = empty(q->sizes(), *q, q->scalar_type()), lse, ws;
+    view_of(out, q->sizes(), q->scalar_type(), q->device(), s.out);
+    if (lse_wanted) {
+        s.lse_step = 1 + s.D / 2;
+        std::vector<int64_t> shape = q->sizes().vec();
+        shape.back() = s.lse_step;
+        lse = empty(shape, *q, at::kFloat);
+    }
+    s.zero_rest = s.cu_q || s.q_lens;
+    const size_t bytes = maxsim_attn_fwd_workspace_bytes(&s);
+    if (bytes) ws = empty({(int64_t)bytes}, *q, at::kByte);
+    if (maxsim_attn_fwd(&s, lse_wanted ? lse.data_ptr<float>() : nullptr, bytes ? ws.data_ptr() : nullptr, bytes, stream_of(*q)) !=
+        MAXSIM_OK)
+        Py_RETURN_NONE;
+    return tuple({out, lse_wanted ? lse.select(-1, 0) : Tensor()});
+    END_HANDLE_TH_ERRORS
+}
+
+// (dout, q, k, v, out, lse, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k) -> (dq, dk, dv)
+PyObject* attn_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    bool plain = n == 15;
+    if (!plain) Py_RETURN_NONE;
+    const Tensor *g = tensor(a[0], plain), *q = tensor(a[1], plain), *k = tensor(a[2], plain), *v = tensor(a[3], plain),
+                 *out = tensor(a[4], plain), *lse = tensor(a[5], plain);
+    maxsim_attn s;
+    if (!plain || !g || !q || !k || !v || !out || !lse || !attn_of(*q, *k, *v, a + 6, s)) Py_RETURN_NONE;
+    const at::Device dev = q->device();
+    const at::ScalarType type = q->scalar_type();
+    maxsim_view gv, dqv, dkv, dvv;
+    if (!view_of(*out, q->sizes(), type, dev, s.out) || !view_of(*g, q->sizes(), type, dev, gv)) Py_RETURN_NONE;
+    // lse as the forward made it (with what rounding left off out behind each value), or contiguous
+    if (lse->scalar_type() != at::kFloat || lse->device() != dev || lse->dim() != q->dim() - 1 ||
+        lse->sizes() != q->sizes().slice(0, q->dim() - 1))
+        Py_RETURN_NONE;
+    if (!lse->is_contiguous()) {
+        int64_t want = s.lse_step = 1 + s.D / 2;
+        for (int64_t d = lse->dim() - 1; d >= 0; want *= lse->size(d), --d)
+            if (lse->size(d) > 1 && lse->stride(d) != want) Py_RETURN_NONE;
+        if (4 * (lse->storage_offset() + lse->numel() * s.lse_step) > (int64_t)lse->storage().nbytes()) Py_RETURN_NONE;
+    }
+    Tensor dq = empty(q->sizes(), *q, type), dk = empty(k->sizes(), *q, type), dv = empty(k->sizes(), *q, type), ws;
+    view_of(dq, q->sizes(), type, dev, dqv);
+    view_of(dk, k->sizes(), type, dev, dkv);
+    view_of(dv, k->sizes(), type, dev, dvv);
+    s.zero_rest = s.cu_q || s.cu_k || s.q_lens || s.k_lens;
+    const size_t bytes = maxsim_attn_bwd_workspace_bytes(&s);
+    if (bytes) ws = empty({(int64_t)bytes}, *q, at::kByte);
+    if (maxsim_attn_bwd(&s, lse->data_ptr<float>(), &gv, &dqv, &dkv, &dvv, bytes ? ws.data_ptr() : nullptr, bytes,
+                        stream_of(*q)) != MAXSIM_OK)
+        Py_RETURN_NONE;
+    return tuple({dq, dk, dv});
+    END_HANDLE_TH_ERRORS
+}
+
+// scores [N, V] with index, teacher [N, K], all contiguous
+bool distill_of(const Tensor* z, const Tensor* index, const Tensor* teacher, PyObject* temperature) {
+    if (!z || !index || !teacher || !PyFloat_Check(temperature) || z->dim() != 2 || index->dim() != 2 || !on_current(*z) ||
+        !z->is_contiguous() || !is_float(code_of(z->scalar_type())))
+        return false;
+    return good(*index, at::kInt, z->device()) && index->size(0) == z->size(0) && good(*teacher, at::kFloat, z->device()) &&
+           teacher->numel() == index->numel() && fits(z->size(0)) && fits(z->size(1)) && fits(index->size(1));
+}
+
+// (scores, index, teacher, temperature) -> (loss, stat)
+PyObject* distill_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    bool plain = n == 4;
+    if (!plain) Py_RETURN_NONE;
+    const Tensor *z = tensor(a[0], plain), *index = tensor(a[1], plain), *teacher = tensor(a[2], plain);
+    if (!plain || !distill_of(z, index, teacher, a[3])) Py_RETURN_NONE;
+    const int32_t N = (int32_t)z->size(0), V = (int32_t)z->size(1);
+    Tensor loss = empty({N}, *z, at::kFloat), stat = empty({N, 2}, *z, at::kFloat), ws;
+    const size_t bytes = maxsim_distill_workspace_bytes(N, V);
+    if (bytes) ws = empty({(int64_t)bytes}, *z, at::kByte);
+    if (maxsim_distill_fwd(z->data_ptr(), V, index->data_ptr<int32_t>(), teacher->data_ptr<float>(), N, V, (int32_t)index->size(1),
+                           code_of(z->scalar_type()), (float)PyFloat_AS_DOUBLE(a[3]), loss.data_ptr<float>(),
+                           stat.data_ptr<float>(), bytes ? ws.data_ptr() : nullptr, bytes, stream_of(*z)) != MAXSIM_OK)
+        Py_RETURN_NONE;
+    return tuple({loss, stat});
+    END_HANDLE_TH_ERRORS
+}
+
+// (dloss, scores, stat, index, teacher, temperature) -> dscores
+PyObject* distill_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    bool plain = n == 6;
+    if (!plain) Py_RETURN_NONE;
+    const Tensor *w = tensor(a[0], plain), *z = tensor(a[1], plain), *stat = tensor(a[2], plain), *index = tensor(a[3], plain),
+                 *teacher = tensor(a[4], plain);
+    if (!plain || !w || !stat || !distill_of(z, index, teacher, a[5]) || !good(*w, at::kFloat, z->device()) ||
+        w->numel() != z->size(0) || !good(*stat, at::kFloat, z->device()) || stat->numel() != 2 * z->size(0))
+        Py_RETURN_NONE;
+    const int32_t N = (int32_t)z->size(0), V = (int32_t)z->size(1);
+    Tensor d = empty({N, V}, *z, z->scalar_type());
+    if (maxsim_distill_bwd(w->data_ptr<float>(), z->data_ptr(), V, stat->data_ptr<float>(), index->data_ptr<int32_t>(),
+                           teacher->data_ptr<float>(), N, V, (int32_t)index->size(1), code_of(z->scalar_type()),
+                           (float)PyFloat_AS_DOUBLE(a[5]), d.data_ptr(), V, stream_of(*z)) != MAXSIM_OK)
+        Py_RETURN_NONE;
+    return wrap(d);
+    END_HANDLE_TH_ERRORS
+}
+
 #define FAST(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {FAST(rmsnorm_fwd), FAST(rmsnorm_bwd), FAST(quant_fp8), FAST(gemm_fp8), FAST(adamw),
+PyMethodDef methods[] = {FAST(rmsnorm_fwd), FAST(rmsnorm_bwd), FAST(quant_fp8), FAST(gemm_fp8), FAST(adamw), FAST(rope),
+                         FAST(attn_fwd), FAST(attn_bwd), FAST(distill_fwd), FAST(distill_bwd),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -186,3 +186,51 @@ def test_no_sequences(bd):
         out, lse = bd.maxsim_attn_fwd(q, k, k, with_lse=True)
         dq, dk, dv = bd.maxsim_attn_bwd(q, q, k, k, out, lse)
         assert torch.all(out == 0) and torch.all(lse == -math.inf) and torch.all(dq == 0) and torch.all(dk == 0) and torch.all(dv == 0)
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_both_ways_of_making_a_call(bd, monkeypatch, packed):
+    """The extension's calls and the general ones: the same results, views of any layout among them, and the same refusals."""
+    s = state(bd, 3)
+    taken = []
+    for name in ("rope", "attn_fwd", "attn_bwd", "distill_fwd", "distill_bwd"):
+        def count(*a, f=getattr(bd._fast, name), name=name):
+            got = f(*a)
+            taken.append((name, got is not None))
+            return got
+        monkeypatch.setattr(bd._fast, name, count)
+    x, fused = s["x"], rand(2, 90, 9, 72, dtype=F16, seed=8)
+    q, k, v, g = (fused[..., i:j, :64] for i, j in ((0, 4), (4, 6), (6, 8), (2, 6)))
+    lens = dict(q_lens=s["how"]["q_lens"], k_lens=s["how"]["k_lens"])
+    if packed:
+        q, k, v, g = (t.flatten(0, 1) for t in (q, k, v, g))
+        cu = torch.tensor([0, 100, 170], dtype=torch.int32, device=DEV)
+        lens = dict(cu_q=cu, cu_k=cu, max_q=100, max_k=100)
+    at = torch.randint(0, 1000, (2, 90), dtype=torch.int32, device=DEV)
+    calls = [lambda **w: [bd.maxsim_rope(x, s["f"], positions=at, layout="interleaved", scale=1.25, inverse=True, **w)],
+             lambda **w: [bd.maxsim_rope(x[:, :, 3:5], s["f"], offsets=s["off"], **w)],
+             lambda **w: [t for t in bd.maxsim_attn_fwd(q, k, v, scale=0.3, window=(9, 3), sinks=1, **lens, **w) if t is not None],
+             lambda **w: list(bd.maxsim_attn_fwd(q, k, v, with_lse=True, **lens, **w)),
+             lambda **w: list(bd.maxsim_distill_fwd(s["z"], s["index"], s["teacher"], temperature=0.5, **w))]
+    out, lse = bd.maxsim_attn_fwd(q, k, v, with_lse=True, **lens)
+    _, stat = bd.maxsim_distill_fwd(s["z"], s["index"], s["teacher"])
+    calls += [lambda **w: list(bd.maxsim_attn_bwd(g, q, k, v, out, lse, **lens, **w)),
+              lambda **w: list(bd.maxsim_attn_bwd(g, q, k, v, out, lse.contiguous(), **lens, **w)),
+              lambda **w: [bd.maxsim_distill_bwd(s["w"], s["z"], stat, s["index"], s["teacher"], **w)]]
+    for call in calls:
+        del taken[:]
+        fast, general = call(), call(stream=torch.cuda.current_stream())
+        assert taken and taken[-1][1], taken
+        for a, b in zip(fast, general):
+            assert a.shape == b.shape and a.dtype == b.dtype and a.stride() == b.stride() and torch.equal(a, b)
+    for error, call in ((ValueError, lambda: bd.maxsim_rope(x, s["f"], layout="both")), (TypeError, lambda: bd.maxsim_rope(x, s["f"].float())),
+                        (bd.MaxSimError, lambda: bd.maxsim_rope(x, s["f"], positions=at, offsets=s["off"])),
+                        (bd.MaxSimError, lambda: bd.maxsim_attn_fwd(q, k, v, scale=-1.0, **lens)),
+                        (bd.MaxSimError, lambda: bd.maxsim_attn_fwd(q, k, v, sinks=-1, **lens)),
+                        (bd.MaxSimError, lambda: bd.maxsim_attn_fwd(q[..., 4:], k[..., 4:], v[..., 4:], **lens)),  # 8-byte aligned
+                        (ValueError, lambda: bd.maxsim_attn_fwd(q, k, v[..., :56], **lens)),
+                        (ValueError, lambda: bd.maxsim_attn_bwd(g, q, k, v, out, lse[..., :2], **lens)),
+                        (bd.MaxSimError, lambda: bd.maxsim_distill_fwd(s["z"], s["index"], s["teacher"], temperature=0.0)),
+                        (ValueError, lambda: bd.maxsim_distill_fwd(s["z"], s["index"], s["teacher"][:, :3]))):
+        with pytest.raises(error):
+            call()
