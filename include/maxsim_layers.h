@@ -116,7 +116,8 @@ int maxsim_attn_bwd(const maxsim_attn* a, const float* lse, const maxsim_view* d
  *   index    [N, K] int32, teacher [N, K] fp32: the teacher's columns and scores.  An index outside
  *            [0, V) is no entry (rows with fewer than K); a column listed twice counts twice.
  *   loss     [N] fp32 out
- *   stat     [N, 2] fp32 out, for the backward: the row's largest z, and log of the sum of exp((z_v - largest) / T)
+ *   stat     [N, 4] fp32 out, for the backward: the row's largest z, log of the sum of exp((z_v - largest) / T), and
+ *            the same of the teacher's entries (of none: 0 and +infinity)
  * A row without entries (or whose entries are all -infinity) gives 0 and no gradient.  Scores of -infinity are
  * columns that are not there (p = 0); one that the teacher's q > 0 asks for gives an infinite loss.
  * Requires N, V >= 0, 0 <= K <= 1024, N < 2^24, V < 2^30, T finite and > 0.

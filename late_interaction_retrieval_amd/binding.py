@@ -1507,7 +1507,7 @@ def maxsim_distill_fwd(scores, index, teacher, temperature=1.0, loss=None, stat=
     """A loss for each row of scores [N, V] (fp16, bf16, fp32) from a teacher's top scores: with
     q = softmax(teacher / T) over the row's entries and p = softmax(scores / T) over its columns,
     T^2 sum_k q_k (log q_k - log p[index_k]).  index [N, K] int32 (an index outside [0, V) is no entry), teacher [N, K]
-    fp32, K <= 1024.  Returns (loss [N], stat [N, 2]) fp32; the backward takes stat."""
+    fp32, K <= 1024.  Returns (loss [N], stat [N, 4]) fp32; the backward takes stat."""
     if loss is None and stat is None and workspace is None and stream is None:
         got = _fast.distill_fwd(scores, index, teacher, temperature)
         if got is not None:
@@ -1531,9 +1531,9 @@ def _distill_fwd(scores, index, teacher, temperature, loss, stat, workspace):
     if loss is None:
         loss = scores.new_empty(N, dtype=torch.float32)
     if stat is None:
-        stat = scores.new_empty((N, 2), dtype=torch.float32)
+        stat = scores.new_empty((N, 4), dtype=torch.float32)
     _flat(loss, "loss", N, torch.float32, dev)
-    _flat(stat, "stat", 2 * N, torch.float32, dev)
+    _flat(stat, "stat", 4 * N, torch.float32, dev)
     workspace, nbytes = _workspace(scores, workspace, _lib.maxsim_distill_workspace_bytes(N, V))
     st = _lib.maxsim_distill_fwd(scores.data_ptr(), ld, index.data_ptr(), teacher.data_ptr(), N, V, K, code, temperature,
                                  loss.data_ptr(), stat.data_ptr(), None if workspace is None else workspace.data_ptr(),
@@ -1558,7 +1558,7 @@ def _distill_bwd(dloss, scores, stat, index, teacher, temperature, dscores):
     dev = scores.device
     N, V, K, code, ld = _distill_sizes(scores, index, teacher)
     _flat(dloss, "dloss", N, torch.float32, dev)
-    _flat(stat, "stat", 2 * N, torch.float32, dev)
+    _flat(stat, "stat", 4 * N, torch.float32, dev)
     ldd = V
     if dscores is None:
         dscores = scores.new_empty((N, V))

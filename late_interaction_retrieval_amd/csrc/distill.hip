@@ -17,10 +17,13 @@
 namespace maxsim {
 namespace {
 
-constexpr int kMostEntries = 1024;
+constexpr size_t kLastCache = (size_t)256 << 20;  // bytes
 constexpr int kThreads = 256;
 constexpr int kShortRow = 1024;  // columns that one wave takes by itself
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 // The largest z and the sum of exp((z - largest) / T).
 struct Soft {
@@ -63,6 +66,24 @@ __device__ __forceinline__ float add_row(float v, float* part) {
     return v;
 }
 
+// Vectors that pass the caches by (STREAM) or not.
+template <typename T, bool STREAM>
+__device__ __forceinline__ typename Pack8<T>::V load_vec(const T* row, int c, int n) {
+    if (STREAM && c + kVec <= n) return __builtin_nontemporal_load(reinterpret_cast<const typename Pack8<T>::V*>(row + c));
+    return load8<T>(row, c, n);
+}
+template <typename T, bool STREAM>
+__device__ __forceinline__ void store_vec(T* row, int c, int n, const float* f) {
+    if (STREAM && c + kVec <= n) {
+        typename Pack8<T>::V v;
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) v[i] = (T)f[i];
+        __builtin_nontemporal_store(v, reinterpret_cast<typename Pack8<T>::V*>(row + c));
+    } else {
+        store8<T>(row, c, n, f);
+    }
+}
+
 // A row's threads have read and written what comes before: one wave's, or the workgroup's.
 template <int TPR>
 __device__ __forceinline__ void row_sync() {
@@ -76,18 +97,21 @@ __device__ __forceinline__ void row_sync() {
     }
 }
 
-// A row's columns [from, to) by its threads.
+// A row's columns [from, to) by its threads; the next ones are on their way while these are worked on.
 template <typename T, int TPR>
 __device__ __forceinline__ Soft soft_of(const T* z, int from, int to, int lane, float c) {
     constexpr int AHEAD = 4;
     Soft s = {-INFINITY, 0.f};
-    for (int at = from + lane * kVec; at < to; at += AHEAD * TPR * kVec) {
-        typename Pack8<T>::V v[AHEAD];
+    typename Pack8<T>::V v[AHEAD], next[AHEAD];
+    const auto load = [&](int first, typename Pack8<T>::V* to_) {
 #pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            const int col = at + a * TPR * kVec;
-            if (col < to) v[a] = load8<T>(z, col, to);
-        }
+        for (int a = 0; a < AHEAD; ++a)
+            if (first + a * TPR * kVec < to) to_[a] = load8<T>(z, first + a * TPR * kVec, to);
+    };
+    int at = from + lane * kVec;
+    load(at, v);
+    while (at < to) {
+        load(at + AHEAD * TPR * kVec, next);
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a) {
             const int col = at + a * TPR * kVec;
@@ -104,6 +128,9 @@ __device__ __forceinline__ Soft soft_of(const T* z, int from, int to, int lane, 
 #pragma unroll
             for (int i = 0; i < kVec; ++i) s.sum += __builtin_amdgcn_exp2f((f[i] - base) * c);
         }
+        at += AHEAD * TPR * kVec;
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a) v[a] = next[a];
     }
     return s;
 }
@@ -141,8 +168,8 @@ __device__ __forceinline__ void finish(const DistillArgs& p, int64_t row, Soft z
     loss = add_row<TPR>(loss, parts);
     if (lane == 0) {
         p.loss[row] = loss * (t * t);
-        p.stat[2 * row] = z.top;
-        p.stat[2 * row + 1] = log_sum;
+        const f32x4 stat = {z.top, log_sum, q.sum == 0.f ? 0.f : q.top, q.sum == 0.f ? INFINITY : __builtin_amdgcn_logf(q.sum) * kLn2};
+        *reinterpret_cast<f32x4_any*>(p.stat + 4 * row) = stat;
     }
 }
 
@@ -185,46 +212,47 @@ __global__ __launch_bounds__(64) void distill_finish_kernel(DistillArgs p, int s
     finish<typename TT::type, 64>(p, row, join64(z, c), lane, c, nullptr, nullptr);
 }
 
-// dz over columns [from, to) of a row by TPR threads, and the entries among them.
-template <typename TT, int TPR>
+// dz over columns [from, to) of a row by TPR threads, and the entries among them.  The first columns are on their way
+// while the entries are looked at.  STREAM: scores past what the last cache holds (256 MB), which would only push each other out of it
+// (8192 x 32768 bf16: 222 -> 202 us, and the next forward 155 -> 126).
+template <typename TT, int TPR, bool STREAM>
 __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(DistillArgs p, int splits, int width) {
     typedef typename TT::type T;
     constexpr int PER = kThreads / TPR, AHEAD = 4;
-    __shared__ Soft part[kThreads / 64];
     extern __shared__ __align__(16) float entries[];  // for each row: columns, q, then p of the entries in the range
     const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const int64_t row = (int64_t)(blockIdx.x / splits) * PER + sub;
     const int from = (int)(blockIdx.x % splits) * width, to = min(p.V, from + width);
-    if (row >= p.N) return;
+    if (row >= p.N) return;  // whole waves, and whole workgroups where they meet
     int* col = (int*)entries + sub * 3 * p.K;
     float *q = (float*)col + p.K, *prob = q + p.K;
     const T* z = (const T*)p.scores + row * p.ld;
     T* dz = (T*)p.dscores + row * p.ldd;
-    const float c = kLog2e / p.temperature, top = p.stat[2 * row] == -INFINITY ? 0.f : p.stat[2 * row];
-    const float log_sum = p.stat[2 * row + 1] * kLog2e;
-    const bool nothing = p.stat[2 * row] == -INFINITY;  // no column is there: p = 0
-    const int32_t* index = p.index + row * p.K;
-    const Soft t = teacher_of<TPR>(p, index, p.teacher + row * p.K, lane, c, part);
-    // no entries: no gradient
-    const float k = t.sum == 0.f ? 0.f : p.dloss[row] * p.temperature;
+    typename Pack8<T>::V v[AHEAD];
+    int at = from + lane * kVec;
+    const auto load = [&](int first) {
+#pragma unroll
+        for (int a = 0; a < AHEAD; ++a)
+            if (first + a * TPR * kVec < to) v[a] = load_vec<T, STREAM>(z, first + a * TPR * kVec, to);
+    };
+    load(at);
+    const f32x4 stat = *reinterpret_cast<const f32x4_any*>(p.stat + 4 * row);
+    const float c = kLog2e / p.temperature, top = stat[0] == -INFINITY ? 0.f : stat[0], log_sum = stat[1] * kLog2e;
+    const bool nothing = stat[0] == -INFINITY;   // no column is there: p = 0
+    const float k = stat[3] == INFINITY ? 0.f : p.dloss[row] * p.temperature;  // no entries: no gradient
     const auto p_of = [&](float s) {
         return nothing ? 0.f : __builtin_amdgcn_exp2f(__builtin_fmaf(s - top, c, -log_sum));
     };
-    for (int i = lane; i < p.K; i += TPR) {  // before anything of the row is written: it may be in place
-        const int v = index[i];
-        const bool here = v >= from && v < to;
-        col[i] = (uint32_t)v < (uint32_t)p.V ? v : -1;
-        q[i] = t.sum == 0.f ? 0.f : __builtin_amdgcn_exp2f((p.teacher[row * p.K + i] - t.top) * c) / t.sum;
-        prob[i] = here ? p_of((float)z[v]) : 0.f;
+    const bool in_place = p.scores == p.dscores;
+    for (int i = lane; i < p.K; i += TPR) {
+        const int n = p.index[row * p.K + i];
+        const bool here = n >= from && n < to;
+        col[i] = (uint32_t)n < (uint32_t)p.V ? n : -1;
+        q[i] = stat[3] == INFINITY ? 0.f : __builtin_amdgcn_exp2f(__builtin_fmaf(p.teacher[row * p.K + i] - stat[2], c, -stat[3] * kLog2e));
+        if (here) prob[i] = p_of((float)z[n]);
     }
-    row_sync<TPR>();
-    for (int at = from + lane * kVec; at < to; at += AHEAD * TPR * kVec) {
-        typename Pack8<T>::V v[AHEAD];
-#pragma unroll
-        for (int a = 0; a < AHEAD; ++a) {
-            const int cl = at + a * TPR * kVec;
-            if (cl < to) v[a] = load8<T>(z, cl, to);
-        }
+    if (in_place) row_sync<TPR>();  // nothing of the row is written before its entries' scores are read
+    while (at < to) {
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a) {
             const int cl = at + a * TPR * kVec;
@@ -232,16 +260,18 @@ __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(DistillArgs p, in
             float f[kVec];
 #pragma unroll
             for (int i = 0; i < kVec; ++i) f[i] = k == 0.f ? 0.f : p_of((float)v[a][i]) * k;
-            store8<T>(dz, cl, to, f);
+            store_vec<T, STREAM>(dz, cl, to, f);
         }
+        at += AHEAD * TPR * kVec;
+        load(at);
     }
     row_sync<TPR>();  // the row is written: its entries' columns come after
     for (int i = lane; i < p.K; i += TPR) {
-        const int v = col[i];
-        if (v < from || v >= to) continue;
+        const int n = col[i];
+        if (n < from || n >= to) continue;
         float all = 0.f;  // a column may be listed more than once: the same value from each
-        for (int j = 0; j < p.K; ++j) all += col[j] == v ? q[j] : 0.f;
-        dz[v] = (T)(k == 0.f ? 0.f : (prob[i] - all) * k);
+        for (int j = 0; j < p.K; ++j) all += col[j] == n ? q[j] : 0.f;
+        dz[n] = (T)(k == 0.f ? 0.f : (prob[i] - all) * k);
     }
 }
 
@@ -277,11 +307,14 @@ hipError_t fwd(const DistillArgs& a, hipStream_t stream) {
 template <typename TT>
 hipError_t bwd(const DistillArgs& a, hipStream_t stream) {
     const DistillPlan d = plan_of(a.N, a.V);
+    const size_t bytes = (size_t)a.N * a.V * (a.dtype == MAXSIM_F32 ? 4 : 2);
     if (a.V <= kShortRow)
-        distill_bwd_kernel<TT, 64><<<(unsigned)ceil_div(a.N, kThreads / 64), kThreads, (size_t)a.K * 12 * (kThreads / 64), stream>>>(
-            a, 1, a.V);
+        distill_bwd_kernel<TT, 64, false>
+            <<<(unsigned)ceil_div(a.N, kThreads / 64), kThreads, (size_t)a.K * 12 * (kThreads / 64), stream>>>(a, 1, a.V);
+    else if (bytes <= kLastCache)
+        distill_bwd_kernel<TT, kThreads, false><<<(unsigned)(a.N * d.splits), kThreads, (size_t)a.K * 12, stream>>>(a, d.splits, d.width);
     else
-        distill_bwd_kernel<TT, kThreads><<<(unsigned)(a.N * d.splits), kThreads, (size_t)a.K * 12, stream>>>(a, d.splits, d.width);
+        distill_bwd_kernel<TT, kThreads, true><<<(unsigned)(a.N * d.splits), kThreads, (size_t)a.K * 12, stream>>>(a, d.splits, d.width);
     return hipGetLastError();
 }
 

@@ -467,7 +467,7 @@ PyObject* distill_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor *z = tensor(a[0], plain), *index = tensor(a[1], plain), *teacher = tensor(a[2], plain);
     if (!plain || !distill_of(z, index, teacher, a[3])) Py_RETURN_NONE;
     const int32_t N = (int32_t)z->size(0), V = (int32_t)z->size(1);
-    Tensor loss = empty({N}, *z, at::kFloat), stat = empty({N, 2}, *z, at::kFloat), ws;
+    Tensor loss = empty({N}, *z, at::kFloat), stat = empty({N, 4}, *z, at::kFloat), ws;
     const size_t bytes = maxsim_distill_workspace_bytes(N, V);
     if (bytes) ws = empty({(int64_t)bytes}, *z, at::kByte);
     if (maxsim_distill_fwd(z->data_ptr(), V, index->data_ptr<int32_t>(), teacher->data_ptr<float>(), N, V, (int32_t)index->size(1),
@@ -486,7 +486,7 @@ PyObject* distill_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor *w = tensor(a[0], plain), *z = tensor(a[1], plain), *stat = tensor(a[2], plain), *index = tensor(a[3], plain),
                  *teacher = tensor(a[4], plain);
     if (!plain || !w || !stat || !distill_of(z, index, teacher, a[5]) || !good(*w, at::kFloat, z->device()) ||
-        w->numel() != z->size(0) || !good(*stat, at::kFloat, z->device()) || stat->numel() != 2 * z->size(0))
+        w->numel() != z->size(0) || !good(*stat, at::kFloat, z->device()) || stat->numel() != 4 * z->size(0))
         Py_RETURN_NONE;
     const int32_t N = (int32_t)z->size(0), V = (int32_t)z->size(1);
     Tensor d = empty({N, V}, *z, z->scalar_type());

@@ -55,7 +55,7 @@ struct DistillArgs {
     const float* dloss;  // backward
     void* dscores;
     float* loss;
-    float* stat;     // [N][2]
+    float* stat;     // [N][4]
     float* partial;  // [N][parts][2] (workspace), where a row is split
     int64_t ld, ldd;
     int N, V, K, dtype;
