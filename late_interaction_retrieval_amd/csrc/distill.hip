@@ -17,12 +17,14 @@
 namespace maxsim {
 namespace {
 
+constexpr int kMostEntries = 1024;
 constexpr size_t kLastCache = (size_t)256 << 20;  // bytes
 constexpr int kThreads = 256;
 constexpr int kShortRow = 1024;  // columns that one wave takes by itself
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 // The largest z and the sum of exp((z - largest) / T).
@@ -219,15 +221,17 @@ template <typename TT, int TPR, bool STREAM>
 __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(DistillArgs p, int splits, int width) {
     typedef typename TT::type T;
     constexpr int PER = kThreads / TPR, AHEAD = 4;
-    extern __shared__ __align__(16) float entries[];  // for each row: columns, q, then p of the entries in the range
+    extern __shared__ __align__(16) float entries[];  // for each row: the entries' columns and q, in fours
     const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
     const int64_t row = (int64_t)(blockIdx.x / splits) * PER + sub;
     const int from = (int)(blockIdx.x % splits) * width, to = min(p.V, from + width);
     if (row >= p.N) return;  // whole waves, and whole workgroups where they meet
-    int* col = (int*)entries + sub * 3 * p.K;
-    float *q = (float*)col + p.K, *prob = q + p.K;
+    const int fours = (p.K + 3) / 4 * 4;
+    int* col = (int*)entries + sub * 2 * fours;
+    float* q = (float*)col + fours;
     const T* z = (const T*)p.scores + row * p.ld;
     T* dz = (T*)p.dscores + row * p.ldd;
+    const int32_t* index = p.index + row * p.K;
     typename Pack8<T>::V v[AHEAD];
     int at = from + lane * kVec;
     const auto load = [&](int first) {
@@ -243,15 +247,26 @@ __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(DistillArgs p, in
     const auto p_of = [&](float s) {
         return nothing ? 0.f : __builtin_amdgcn_exp2f(__builtin_fmaf(s - top, c, -log_sum));
     };
+    // this thread's first entry; the score is read before anything of the row is written, which may be in its place
     const bool in_place = p.scores == p.dscores;
-    for (int i = lane; i < p.K; i += TPR) {
-        const int n = p.index[row * p.K + i];
-        const bool here = n >= from && n < to;
-        col[i] = (uint32_t)n < (uint32_t)p.V ? n : -1;
-        q[i] = stat[3] == INFINITY ? 0.f : __builtin_amdgcn_exp2f(__builtin_fmaf(p.teacher[row * p.K + i] - stat[2], c, -stat[3] * kLog2e));
-        if (here) prob[i] = p_of((float)z[n]);
+    const int mine = lane < p.K ? index[lane] : -1;
+    float score = 0.f;
+    if (mine >= from && mine < to) score = (float)z[mine];
+    for (int i = lane; i < fours; i += TPR) {
+        const int n = i < p.K ? index[i] : -1;
+        const bool there = (uint32_t)n < (uint32_t)p.V;
+        col[i] = there ? n : -1;
+        q[i] = !there || stat[3] == INFINITY ? 0.f
+                                             : __builtin_amdgcn_exp2f(__builtin_fmaf(p.teacher[row * p.K + i] - stat[2], c, -stat[3] * kLog2e));
     }
-    if (in_place) row_sync<TPR>();  // nothing of the row is written before its entries' scores are read
+    float more[kMostEntries / TPR - 1];  // with more entries than threads: the other ones' scores
+#pragma unroll
+    for (int r = 1; r < kMostEntries / TPR; ++r) {
+        more[r - 1] = 0.f;
+        const int i = lane + r * TPR, n = i < p.K ? index[i] : -1;
+        if (n >= from && n < to) more[r - 1] = (float)z[n];
+    }
+    if (in_place) row_sync<TPR>();
     while (at < to) {
 #pragma unroll
         for (int a = 0; a < AHEAD; ++a) {
@@ -266,12 +281,21 @@ __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(DistillArgs p, in
         load(at);
     }
     row_sync<TPR>();  // the row is written: its entries' columns come after
-    for (int i = lane; i < p.K; i += TPR) {
+#pragma unroll
+    for (int r = 0; r < kMostEntries / TPR; ++r) {
+        const int i = lane + r * TPR;
+        if (i >= p.K) break;
         const int n = col[i];
         if (n < from || n >= to) continue;
-        float all = 0.f;  // a column may be listed more than once: the same value from each
-        for (int j = 0; j < p.K; ++j) all += col[j] == n ? q[j] : 0.f;
-        dz[n] = (T)(k == 0.f ? 0.f : (prob[i] - all) * k);
+        f32x4 all = {0.f, 0.f, 0.f, 0.f};  // a column may be listed more than once: the same value from each
+#pragma unroll 4
+        for (int j = 0; j < fours; j += 4) {
+            const i32x4 cs = *reinterpret_cast<const i32x4*>(col + j);
+            const f32x4 qs = *reinterpret_cast<const f32x4*>(q + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) all[e] += cs[e] == n ? qs[e] : 0.f;
+        }
+        dz[n] = (T)(k == 0.f ? 0.f : (p_of(r == 0 ? score : more[r > 0 ? r - 1 : 0]) - ((all[0] + all[1]) + (all[2] + all[3]))) * k);
     }
 }
 
@@ -307,14 +331,15 @@ hipError_t fwd(const DistillArgs& a, hipStream_t stream) {
 template <typename TT>
 hipError_t bwd(const DistillArgs& a, hipStream_t stream) {
     const DistillPlan d = plan_of(a.N, a.V);
+    const size_t lds = (size_t)((a.K + 3) / 4 * 4) * 8;
     const size_t bytes = (size_t)a.N * a.V * (a.dtype == MAXSIM_F32 ? 4 : 2);
     if (a.V <= kShortRow)
         distill_bwd_kernel<TT, 64, false>
-            <<<(unsigned)ceil_div(a.N, kThreads / 64), kThreads, (size_t)a.K * 12 * (kThreads / 64), stream>>>(a, 1, a.V);
+            <<<(unsigned)ceil_div(a.N, kThreads / 64), kThreads, lds * (kThreads / 64), stream>>>(a, 1, a.V);
     else if (bytes <= kLastCache)
-        distill_bwd_kernel<TT, kThreads, false><<<(unsigned)(a.N * d.splits), kThreads, (size_t)a.K * 12, stream>>>(a, d.splits, d.width);
+        distill_bwd_kernel<TT, kThreads, false><<<(unsigned)(a.N * d.splits), kThreads, lds, stream>>>(a, d.splits, d.width);
     else
-        distill_bwd_kernel<TT, kThreads, true><<<(unsigned)(a.N * d.splits), kThreads, (size_t)a.K * 12, stream>>>(a, d.splits, d.width);
+        distill_bwd_kernel<TT, kThreads, true><<<(unsigned)(a.N * d.splits), kThreads, lds, stream>>>(a, d.splits, d.width);
     return hipGetLastError();
 }
 

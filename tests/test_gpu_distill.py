@@ -140,3 +140,25 @@ def test_autograd_of_scores(bd):
     got, = torch.autograd.grad((loss * dloss).sum(), z)
     _, stat = bd.maxsim_distill_fwd(z.detach(), index, teacher, temperature=2.0)
     assert torch.equal(got, bd.maxsim_distill_bwd(dloss, z.detach(), stat, index, teacher, temperature=2.0))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
+def test_scores_past_the_last_cache(bd, dtype):
+    """Over 256 MB, whose loads and stores go past the caches: the same values as its rows by themselves."""
+    N, V = 70, (1 << 20) * (2 if dtype == BF16 else 1) + 3
+    g = torch.Generator(device=DEV).manual_seed(3)
+    z = (3 * torch.randn(N, V, device=DEV, generator=g)).to(dtype)
+    index = torch.randint(0, V, (N, 9), device=DEV, generator=g, dtype=torch.int32)
+    index[5, 3] = index[5, 7]
+    teacher, dloss = torch.randn(N, 9, device=DEV, generator=g), torch.rand(N, device=DEV, generator=g)
+    loss, stat = bd.maxsim_distill_fwd(z, index, teacher)
+    d = bd.maxsim_distill_bwd(dloss, z, stat, index, teacher)
+    for a in range(0, N, 10):
+        r = slice(a, a + 10)
+        part = bd.maxsim_distill_bwd(dloss[r].contiguous(), z[r], stat[r].contiguous(), index[r].contiguous(), teacher[r].contiguous())
+        assert torch.equal(part, d[r])
+    want = ref.distill(z[5:6].cpu(), index[5:6].cpu(), teacher[5:6].cpu(), 1.0, dloss[5:6].cpu())
+    ref.check(loss[5:6], want["loss"], "loss")
+    ref.check(d[5:6], want["dscores"], "dscores")
+    bd.maxsim_distill_bwd(dloss, z, stat, index, teacher, dscores=z)
+    assert torch.equal(z, d)

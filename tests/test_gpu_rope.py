@@ -124,3 +124,16 @@ def test_gradient(bd, layout):
     change = ((moved - y).double() * g.double()).sum()
     size = ((moved.abs() + y.abs()).double() * g.double().abs()).sum()
     assert abs(change - (d.double() * dx.double()).sum()) <= 32 * ref.U * size
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rows_past_the_last_cache(bd, layout):
+    """Over 256 MB in and out, whose loads go past the caches: the same values as some of its rows by themselves."""
+    x = torch.randn(3, 12000, 20, 100, device=DEV, dtype=torch.float32).to(BF16)
+    f, _ = bd.rope_frequencies(66, device=DEV)
+    y = bd.maxsim_rope(x, f, layout=layout)
+    assert torch.equal(y[1, :500], bd.maxsim_rope(x[1, :500], f, layout=layout))
+    assert torch.equal(y[2, :700], bd.maxsim_rope(x[2, :700], f, layout=layout))
+    want = y.clone()
+    bd.maxsim_rope(x, f, layout=layout, out=x)
+    assert torch.equal(x, want)
