@@ -35,9 +35,9 @@ __device__ __forceinline__ float lift_of(float top) {
 __device__ __forceinline__ int far_from(const maxsim_attn& a, const Seq& s, int j0) {
     return max(0, min(s.lq, min(j0 + kRows, s.lk) + a.left - (s.lk - s.lq)));
 }
-__device__ __forceinline__ float* far_row(const AttnArgs& p, int b, int h, int tile, int slot, int row) {
-    const int64_t block = (((int64_t)b * p.a.Hk + h) * p.far_tiles + tile) * (p.far_chunks + 1) + slot;
-    return p.part_far + (block * 2 * p.far_rows + row) * p.a.D;
+__device__ __forceinline__ float* part_row(const AttnArgs& p, int b, int h, int tile, int slot, int row) {
+    const int64_t block = (((int64_t)b * p.a.Hk + h) * p.part_tiles + tile) * ((p.far_chunks + 1) * p.head_splits) + slot;
+    return p.part + (block * 2 * p.part_rows + row) * p.a.D;
 }
 
 template <typename TT, int DP>
@@ -181,13 +181,13 @@ __global__ __launch_bounds__(64 * kWaves, WAVES) void attn_dkv_kernel(AttnArgs p
     const maxsim_attn& a = p.a;
     Work w;
     const int fars = p.far_tiles * p.far_chunks;
-    if (!work_of(w, a.B, a.Hk, tiles + fars)) return;
-    const int b = w.b, h = w.h;
-    const bool far = w.part < fars;
-    const int tile = far ? w.part / p.far_chunks : w.part - fars, chunk = far ? w.part % p.far_chunks : 0;
+    if (!work_of(w, a.B, a.Hk, (tiles + fars) * p.head_splits)) return;
+    const int b = w.b, h = w.h, heads = w.part % p.head_splits, unit = w.part / p.head_splits;
+    const bool far = unit < fars;
+    const int tile = far ? unit / p.far_chunks : unit - fars, chunk = far ? unit % p.far_chunks : 0;
     const Seq s = sequence(a, b);
-    const int G = p.group, D = a.D;
-    if (a.zero_rest && !far) {
+    const int G = p.group, D = a.D, g0 = G * heads / p.head_splits, g1 = G * (heads + 1) / p.head_splits;
+    if (a.zero_rest && !far && heads == 0) {
         const int part = h * tiles + tile, parts = a.Hk * tiles, item = (b * a.Hk + h) * tiles + tile, items = a.B * a.Hk * tiles;
         zero_rest<T>(p.dk, nullptr, 1, a.cu_k, a.B, a.rows_k, b, s.k0, s.lk, s.all_k, a.Hk, D, part, parts, item, items);
         zero_rest<T>(p.dv, nullptr, 1, a.cu_k, a.B, a.rows_k, b, s.k0, s.lk, s.all_k, a.Hk, D, part, parts, item, items);
@@ -205,7 +205,7 @@ __global__ __launch_bounds__(64 * kWaves, WAVES) void attn_dkv_kernel(AttnArgs p
         i_hi = min(s.lq, i_lo + p.far_tokens);
         if (i_lo >= i_hi) return;
     }
-    const int steps = (max(i_hi - i_lo, 0) + TR - 1) / TR, total = steps * G;
+    const int steps = (max(i_hi - i_lo, 0) + TR - 1) / TR, total = steps * (g1 - g0);
 
     const int wj = j0 + wave * 32, j_hi = min(wj + 31, s.lk - 1);  // the wave's keys
     const int j = min(wj + (lane & 31), s.lk - 1);
@@ -240,7 +240,7 @@ __global__ __launch_bounds__(64 * kWaves, WAVES) void attn_dkv_kernel(AttnArgs p
     Loader<DP, TR, kWaves> lq, lg;
     lq.init(wave, lane, a.q.token, D);
     lg.init(wave, lane, p.dout.token, D);
-    int g_next = 0, i_next = i_lo;  // the head and the token that the next tile starts with
+    int g_next = g0, i_next = i_lo;  // the head and the token that the next tile starts with
     const auto load = [&](uint8_t* qt, uint8_t* gt, float* stat) {
         lq.load(qs + (int64_t)g_next * a.q.head + (int64_t)i_next * a.q.token, s.lq - i_next, a.q.token, D, qt, wave);
         lg.load(gs + (int64_t)g_next * p.dout.head + (int64_t)i_next * p.dout.token, s.lq - i_next, p.dout.token, D, gt, wave);
@@ -336,16 +336,16 @@ __global__ __launch_bounds__(64 * kWaves, WAVES) void attn_dkv_kernel(AttnArgs p
         work(q_1, g_1, stat_1);
     }
     const float kf = is_f16<T>() && lift != 0.f ? a.scale / lift : a.scale, vf = is_f16<T>() ? 1.f / 256.f : 1.f;
-    const bool part = apart && j < a.sinks;
-    if (!far) {
+    const bool part = p.head_splits > 1 || (apart && j < a.sinks);
+    if (!far && p.head_splits == 1) {
         T* dkr = first<T>(p.dk, packed, b, s.k0, h) + (int64_t)j * p.dk.token;
         T* dvr = first<T>(p.dv, packed, b, s.k0, h) + (int64_t)j * p.dv.token;
         store_row<T, DB>(dkr, mine && !part, dk, kf, lane, D);
         store_row<T, DB>(dvr, mine && !part, dv, vf, lane, D);
     }
-    if (part && mine) {
-        float* to = far_row(p, b, h, tile, far ? chunk + 1 : 0, j - j0);
-        const int64_t other = (int64_t)p.far_rows * D;
+    if (part && mine && (!far || j < a.sinks)) {
+        float* to = part_row(p, b, h, tile, (far ? chunk + 1 : 0) * p.head_splits + heads, j - j0);
+        const int64_t other = (int64_t)p.part_rows * D;
 #pragma unroll
         for (int db = 0; db < DB; ++db)
 #pragma unroll
@@ -364,21 +364,24 @@ __global__ __launch_bounds__(64 * kWaves, WAVES) void attn_dkv_kernel(AttnArgs p
     }
 }
 
-// The first tokens' rows of dK and dV: the parts of the tokens near and far, added in order.  32 threads to a row, 4 columns each.
+// The rows of dK and dV that more than one workgroup adds to: their parts, added in order.  32 threads to a row, 4 columns each.
 template <typename TT>
-__global__ __launch_bounds__(64) void attn_far_kernel(AttnArgs p) {
+__global__ __launch_bounds__(64) void attn_parts_kernel(AttnArgs p, int keys) {
     typedef typename TT::type T;
     typedef T V4 __attribute__((ext_vector_type(4)));
     const maxsim_attn& a = p.a;
-    const int keys = min(a.sinks, a.max_k), j = blockIdx.x % keys, pair = blockIdx.x / keys, h = pair % a.Hk, b = pair / a.Hk;
+    const int j = blockIdx.x % keys, pair = blockIdx.x / keys, h = pair % a.Hk, b = pair / a.Hk;
     const Seq s = sequence(a, b);
     const int d = (threadIdx.x & 31) * 4, tile = j / kRows, j0 = tile * kRows;
     if (j >= s.lk || d >= a.D) return;
     const bool of_v = threadIdx.x >= 32;
-    const int chunks = (max(s.lq - far_from(a, s, j0), 0) + p.far_tokens - 1) / p.far_tokens;
+    int slots = p.head_splits;
+    if (tile < p.far_tiles && j < a.sinks)
+        slots += (max(s.lq - far_from(a, s, j0), 0) + p.far_tokens - 1) / p.far_tokens * p.head_splits;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    for (int n = 0; n <= chunks; ++n)
-        sum += *reinterpret_cast<const f32x4*>(far_row(p, b, h, tile, n, j - j0) + (of_v ? (int64_t)p.far_rows * a.D : 0) + d);
+#pragma unroll 4
+    for (int n = 0; n < slots; ++n)
+        sum += *reinterpret_cast<const f32x4*>(part_row(p, b, h, tile, n, j - j0) + (of_v ? (int64_t)p.part_rows * a.D : 0) + d);
     const maxsim_view& out = of_v ? p.dv : p.dk;
     V4 y;
 #pragma unroll
@@ -386,21 +389,33 @@ __global__ __launch_bounds__(64) void attn_far_kernel(AttnArgs p) {
     *reinterpret_cast<V4*>(first<T>(out, a.cu_k != nullptr, b, s.k0, h) + (int64_t)j * out.token + d) = y;
 }
 
-// Where first tokens stay visible past the window, their key tile would go over all queries and the others over a
-// window's worth.  With more than two such stretches of queries the far ones get workgroups of their own.
-void plan_far(const maxsim_attn& a, AttnArgs& p) {
-    p.far_tiles = p.far_chunks = p.far_tokens = p.far_rows = 0;
-    if (a.sinks == 0 || a.left < 0 || a.max_k == 0 || a.sinks > 2 * kRows) return;
-    const int64_t right = a.right < 0 ? 0 : a.right, stretch = ((int64_t)kRows + a.left + right + 63) / 64 * 64;
-    if (a.max_q <= 2 * stretch) return;
-    p.far_tokens = (int)stretch;
-    p.far_chunks = (int)((a.max_q + stretch - 1) / stretch);
-    const int keys = a.sinks < a.max_k ? a.sinks : a.max_k;
-    p.far_tiles = (keys + kRows - 1) / kRows;
-    p.far_rows = keys < kRows ? keys : kRows;
+int key_tiles(const maxsim_attn& a) { return std::max(1, (a.max_k + kRows - 1) / kRows); }
+
+// How the work on dK and dV is shared out.  Where first tokens stay visible past the window, their key tile would go
+// over all queries and the others over a window's worth: with more than two such stretches of queries the far ones get workgroups
+// of their own (8192 tokens, a window of 2048 and 4 first tokens, 32 / 8 heads: 1542 -> 686 us).  Fewer than 256
+// workgroups: several for the query heads of a key head (9 sequences of up to 601 tokens, 6 / 2 heads: TODO us).
+void plan_parts(const maxsim_attn& a, AttnArgs& p) {
+    p.far_tiles = p.far_chunks = p.far_tokens = p.part_tiles = p.part_rows = 0;
+    p.head_splits = 1;
+    if (a.max_k == 0) return;
+    const int keys = std::min(a.sinks, a.max_k);
+    if (a.sinks > 0 && a.left >= 0 && a.sinks <= 2 * kRows) {
+        const int64_t right = a.right < 0 ? 0 : a.right, stretch = ((int64_t)kRows + a.left + right + 63) / 64 * 64;
+        // (a launch of a wave for each of their rows holds fewer than 2^32 threads)
+        if (a.max_q > 2 * stretch && (int64_t)a.B * a.Hk * keys < (int64_t)1 << 25) {
+            p.far_tokens = (int)stretch;
+            p.far_chunks = (int)((a.max_q + stretch - 1) / stretch);
+            p.far_tiles = (keys + kRows - 1) / kRows;
+        }
+    }
+    const int64_t items = (int64_t)a.B * a.Hk * (key_tiles(a) + p.far_tiles * p.far_chunks);
+    if (items < 256) p.head_splits = (int)std::min<int64_t>(a.Hq / a.Hk, 512 / items);
+    p.part_tiles = p.head_splits > 1 ? key_tiles(a) : p.far_tiles;
+    p.part_rows = p.head_splits > 1 ? kRows : std::min(keys, kRows);
 }
-int64_t far_floats(const maxsim_attn& a, const AttnArgs& p) {
-    return (int64_t)a.B * a.Hk * p.far_tiles * (p.far_chunks + 1) * 2 * p.far_rows * a.D;
+int64_t part_floats(const maxsim_attn& a, const AttnArgs& p) {
+    return (int64_t)a.B * a.Hk * p.part_tiles * (p.far_chunks + 1) * p.head_splits * 2 * p.part_rows * a.D;
 }
 
 template <typename TT, int DP>
@@ -409,17 +424,19 @@ hipError_t launch(const AttnArgs& p, hipStream_t stream) {
     const int64_t pairs = (int64_t)a.B * a.Hk;
     // (of no queries, or no keys, the rows of no sequence are still to be made 0)
     const int q_tiles = (int)std::max<int64_t>(1, ((int64_t)a.max_q * p.group + kRows - 1) / kRows);
-    const int k_tiles = std::max(1, (a.max_k + kRows - 1) / kRows), each = k_tiles + p.far_tiles * p.far_chunks;
+    const int k_tiles = key_tiles(a), each = (k_tiles + p.far_tiles * p.far_chunks) * p.head_splits;
     attn_dq_kernel<TT, DP><<<(unsigned)blocks_for(pairs, q_tiles), 64 * kWaves, 0, stream>>>(p, q_tiles);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t blocks = blocks_for(pairs, each);
-    // a width of 128: two workgroups to a CU where there are so many
-    const auto dkv = DP == 128 && blocks <= 384 ? attn_dkv_kernel<TT, DP, DP == 128 ? 1 : 2> : attn_dkv_kernel<TT, DP, 2>;
+    // a width of 128: two workgroups to a CU where there are so many (2 x 4096 tokens, 4 key heads, 256 workgroups: one to a
+    // CU 600 us, two 780; 16 x 1024 tokens, 512: 320 and 270)
+    const auto dkv = DP == 128 && blocks <= 256 ? attn_dkv_kernel<TT, DP, DP == 128 ? 1 : 2> : attn_dkv_kernel<TT, DP, 2>;
     dkv<<<(unsigned)blocks, 64 * kWaves, 0, stream>>>(p, k_tiles);
     e = hipGetLastError();
-    if (e != hipSuccess || p.far_chunks == 0) return e;
-    attn_far_kernel<TT><<<(unsigned)(pairs * std::min(a.sinks, a.max_k)), 64, 0, stream>>>(p);
+    if (e != hipSuccess || p.part_tiles == 0) return e;
+    const int keys = p.head_splits > 1 ? a.max_k : std::min(a.sinks, a.max_k);
+    attn_parts_kernel<TT><<<(unsigned)(pairs * keys), 64, 0, stream>>>(p, keys);
     return hipGetLastError();
 }
 
@@ -432,14 +449,14 @@ int64_t stat_floats(const maxsim_attn& a) {  // the parts after them start at a 
 
 size_t attn_bwd_workspace_bytes(const maxsim_attn& a) {
     AttnArgs p{};
-    plan_far(a, p);
-    return (size_t)(stat_floats(a) + far_floats(a, p)) * sizeof(float);
+    plan_parts(a, p);
+    return (size_t)(stat_floats(a) + part_floats(a, p)) * sizeof(float);
 }
 
 hipError_t launch_attn_bwd(const maxsim_attn& a, const float* lse, const maxsim_view& dout, const maxsim_view& dq,
                            const maxsim_view& dk, const maxsim_view& dv, void* workspace, hipStream_t stream) {
     AttnArgs p{};
-    plan_far(a, p);
+    plan_parts(a, p);
     p.a = a;
     if (a.left < 0 || a.left > kNoBound) p.a.left = kNoBound;
     if (a.right < 0 || a.right > kNoBound) p.a.right = kNoBound;
@@ -452,7 +469,7 @@ hipError_t launch_attn_bwd(const maxsim_attn& a, const float* lse, const maxsim_
     p.splits = 1;
     p.rows = rows_in_memory(a);
     p.row_stat = static_cast<float*>(workspace);
-    p.part_far = p.row_stat + stat_floats(a);
+    p.part = p.row_stat + stat_floats(a);
     const bool half = a.dtype == MAXSIM_F16;
     if (a.D <= 64) return half ? launch<F16, 64>(p, stream) : launch<BF16, 64>(p, stream);
     return half ? launch<F16, 128>(p, stream) : launch<BF16, 128>(p, stream);

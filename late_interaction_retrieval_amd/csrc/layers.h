@@ -34,10 +34,12 @@ struct AttnArgs {
     int64_t rows;    // of q in memory
     float* row_stat; // backward: [2][Hq][rows]: lse in powers of 2 (+infinity where it is -infinity), rowsum(dO * out);
                      // fp16: a third, the rows' largest |dO|
-    // Backward: queries past the window see the first tokens' keys alone.  They are worked on apart, `far_tokens` at a
-    // time, and their sums joined: part_far [B * Hk][key tiles with first tokens][far_chunks + 1][dk, dv][far_rows][D].
-    int far_tiles, far_chunks, far_tokens, far_rows;
-    float* part_far;
+    // Backward, dK and dV.  Queries past the window see the first tokens' keys alone: of the first far_tiles key tiles they
+    // are worked on apart, far_tokens at a time.  Where key tiles are few, the query heads of a key head are shared out too,
+    // over head_splits workgroups.  What more than one workgroup adds to goes through parts:
+    // part [B * Hk][part_tiles][(far_chunks + 1) * head_splits][dk, dv][part_rows][D].
+    int far_tiles, far_chunks, far_tokens, head_splits, part_tiles, part_rows;
+    float* part;
 };
 constexpr int kNoBound = 1 << 29;  // past every position
 
