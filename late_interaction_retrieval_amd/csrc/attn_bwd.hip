@@ -100,6 +100,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
         if (is_f16<T>()) stat[2 * p.rows * a.Hq] = top;
     }
     const float lift = is_f16<T>() ? lift_of(top) : 1.f;
+    const Place place = place_of<DP>(lane);
 
     const int p_lo = min(wr, rows - 1) / G + shift, p_hi = min(wr + 31, rows - 1) / G + shift, pos = token + shift;
     const int lo = pos - a.left, hi = min(pos + a.right, s.lk - 1);
@@ -129,9 +130,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
             const uint8_t *kb = kt + nb * 32 * Tile<DP>::ROW, *vb = vt + nb * 32 * Tile<DP>::ROW;
             f32x16 x = zero16(), dp = zero16();
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk) x = mma<T>(rows_at<T, DP>(kb, lane, kk), q[kk], x);
+            for (int kk = 0; kk < KS; ++kk) x = mma<T>(rows_at<T, DP>(kb, place, kk), q[kk], x);
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk) dp = mma<T>(rows_at<T, DP>(vb, lane, kk), g[kk], dp);
+            for (int kk = 0; kk < KS; ++kk) dp = mma<T>(rows_at<T, DP>(vb, place, kk), g[kk], dp);
 #pragma unroll
             for (int i = 0; i < 16; ++i) x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i], c, -lse));
             if (!whole) {
@@ -146,7 +147,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
             for (int t2 = 0; t2 < 2; ++t2) {
                 const V8 ds = pack8<T>(x, 8 * t2);
 #pragma unroll
-                for (int db = 0; db < DB; ++db) acc[db] = mma<T>(cols_at<T, DP>(kb, lane, t2, db), ds, acc[db]);
+                for (int db = 0; db < DB; ++db) acc[db] = mma<T>(cols_at<T, DP>(kb, place, t2, db), ds, acc[db]);
             }
         }
     };
@@ -212,6 +213,7 @@ __global__ __launch_bounds__(64 * kWaves, WAVES) void attn_dkv_kernel(AttnArgs p
     const bool mine = wj + (lane & 31) < s.lk, packed = a.cu_k != nullptr;
     V8 k[K_IN_LDS ? 1 : KS], v[KS];
     const int k_at = wave * KS * 1024 + lane * 16;
+    const Place place = place_of<DP>(lane);
     const T* kr = first<T>(a.k, packed, b, s.k0, h) + (int64_t)j * a.k.token;
     const T* vr = first<T>(a.v, packed, b, s.k0, h) + (int64_t)j * a.v.token;
 #pragma unroll
@@ -280,19 +282,21 @@ __global__ __launch_bounds__(64 * kWaves, WAVES) void attn_dkv_kernel(AttnArgs p
             if (ib > any_hi || ib + 31 < any_lo) continue;
             const bool whole = ib >= all_lo && ib + 31 <= all_hi;
             const uint8_t *qb = qt + nb * 32 * Tile<DP>::ROW, *gb = gt + nb * 32 * Tile<DP>::ROW;
-            // (the compiler is not to see that k's operands are the same in each step: it would keep them in registers)
+            // (the compiler is not to see that these places are the same in each step: it would keep all that follows from them,
+            // and k's operands, in registers that the sums need)
             int ka = k_at;
-            asm volatile("" : "+v"(ka));
+            Place at_ = place;
+            asm volatile("" : "+v"(ka), "+v"(at_.rows), "+v"(at_.cols));
             f32x16 x = zero16(), dp = zero16();
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
                 V8 kx;
                 if constexpr (K_IN_LDS) kx = *reinterpret_cast<const V8*>(k_lds + ka + kk * 1024);
                 else kx = k[kk];
-                x = mma<T>(rows_at<T, DP>(qb, lane, kk), kx, x);
+                x = mma<T>(rows_at<T, DP>(qb, at_, kk), kx, x);
             }
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk) dp = mma<T>(rows_at<T, DP>(gb, lane, kk), v[kk], dp);
+            for (int kk = 0; kk < KS; ++kk) dp = mma<T>(rows_at<T, DP>(gb, at_, kk), v[kk], dp);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const f32x4 l = *reinterpret_cast<const f32x4*>(stat + 32 * nb + 8 * q + 4 * (lane >> 5));
@@ -309,7 +313,7 @@ __global__ __launch_bounds__(64 * kWaves, WAVES) void attn_dkv_kernel(AttnArgs p
             for (int t = 0; t < 2; ++t) {
                 const V8 pt = pack8<T>(x, 8 * t);
 #pragma unroll
-                for (int db = 0; db < DB; ++db) dv[db] = mma<T>(cols_at<T, DP>(gb, lane, t, db), pt, dv[db]);
+                for (int db = 0; db < DB; ++db) dv[db] = mma<T>(cols_at<T, DP>(gb, at_, t, db), pt, dv[db]);
             }
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -321,7 +325,7 @@ __global__ __launch_bounds__(64 * kWaves, WAVES) void attn_dkv_kernel(AttnArgs p
             for (int t = 0; t < 2; ++t) {
                 const V8 ds = pack8<T>(x, 8 * t);
 #pragma unroll
-                for (int db = 0; db < DB; ++db) dk[db] = mma<T>(cols_at<T, DP>(qb, lane, t, db), ds, dk[db]);
+                for (int db = 0; db < DB; ++db) dk[db] = mma<T>(cols_at<T, DP>(qb, at_, t, db), ds, dk[db]);
             }
         }
     };

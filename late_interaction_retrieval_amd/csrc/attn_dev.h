@@ -214,25 +214,29 @@ struct Loader {
     }
 };
 
-// A operand from a tile's rows: row l % 32 of a block of 32, values 16 kk + 8 (l / 32) on.
+// Where a lane reads: its first place of either kind, from which the others differ by an exclusive or (a place's turn does
+// not reach beyond its row).
+struct Place {
+    int rows, cols;
+};
 template <int DP>
-__device__ __forceinline__ int row_place(int lane, int kk) {
-    const int r = lane & 31, c = 2 * kk + (lane >> 5);
-    return r * Tile<DP>::ROW + ((c ^ Tile<DP>::turn(r)) << 4);
+__device__ __forceinline__ Place place_of(int lane) {
+    const int r = lane & 31, k = 4 * (lane >> 5) + ((lane & 15) >> 2), c = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+    return {r * Tile<DP>::ROW + (((lane >> 5) ^ Tile<DP>::turn(r)) << 4),
+            k * Tile<DP>::ROW + ((c ^ Tile<DP>::turn(k)) << 4) + ((lane & 1) << 3)};
 }
+// A operand from a tile's rows: row l % 32 of a block of 32, values 16 kk + 8 (l / 32) on.
 template <typename T, int DP>
-__device__ __forceinline__ typename Vec8<T>::V rows_at(const uint8_t* block, int lane, int kk) {
-    return *reinterpret_cast<const typename Vec8<T>::V*>(block + row_place<DP>(lane, kk));
+__device__ __forceinline__ typename Vec8<T>::V rows_at(const uint8_t* block, const Place& at, int kk) {
+    return *reinterpret_cast<const typename Vec8<T>::V*>(block + (at.rows ^ (kk << 5)));
 }
 // A operand from a tile transposed: column 32 db + l % 32 of its rows slot(l / 32, 0 .. 7) from row 16 t of `block` on.
+// (8 rows further the turn differs by 2.)
 template <typename T, int DP>
-__device__ __forceinline__ typename Vec8<T>::V cols_at(const uint8_t* block, int lane, int t, int db) {
-    const int r = 4 * (lane >> 5) + ((lane & 15) >> 2);
-    const int c = 4 * db + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
-    const uint8_t* at = block + (16 * t + r) * Tile<DP>::ROW + ((lane & 1) << 3);
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ltr_t)(at + ((c ^ Tile<DP>::turn(r)) << 4)));
-    const s16x4 hi =
-        __builtin_amdgcn_ds_read_tr16_b64_v4i16((ltr_t)(at + 8 * Tile<DP>::ROW + ((c ^ Tile<DP>::turn(r + 8)) << 4)));
+__device__ __forceinline__ typename Vec8<T>::V cols_at(const uint8_t* block, const Place& at, int t, int db) {
+    const uint8_t* from = block + 16 * t * Tile<DP>::ROW;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ltr_t)(from + (at.cols ^ (db << 6))));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ltr_t)(from + 8 * Tile<DP>::ROW + (at.cols ^ (db << 6) ^ 32)));
     return __builtin_bit_cast(typename Vec8<T>::V, (s16x8)__builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 // B operand from memory: 8 values of a row from column c on, zeros from column D on.

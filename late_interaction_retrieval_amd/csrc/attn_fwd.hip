@@ -28,6 +28,7 @@ struct Rows {
     typename Vec8<T>::V q[KS];
     f32x16 o[DB];
     float ref, sum;
+    Place at;
     int lo, hi;  // the lane's row sees keys [lo, hi] (and those below `sinks` that are at most hi)
 
     __device__ __forceinline__ void start(const T* row, int lane, int D, int pos, int lk, const maxsim_attn& a) {
@@ -35,6 +36,7 @@ struct Rows {
         for (int kk = 0; kk < KS; ++kk) q[kk] = row8<T>(row, 16 * kk + 8 * (lane >> 5), D);
 #pragma unroll
         for (int db = 0; db < DB; ++db) o[db] = zero16();
+        at = place_of<DP>(lane);
         ref = -INFINITY;
         sum = 0.f;
         lo = pos - a.left;
@@ -52,14 +54,13 @@ struct Rows {
     // The reference stays while the maximum passes it by less than 2^8: P grows to 256 at most, which both types hold,
     // and relative to the row's sum nothing is lost.
     template <int NB>
-    __device__ __forceinline__ void step(const uint8_t* kt, const uint8_t* vt, int lane, bool all, const uint32_t* bits, float c,
-                                         float slack) {
+    __device__ __forceinline__ void step(const uint8_t* kt, const uint8_t* vt, bool all, const uint32_t* bits, float c, float slack) {
         f32x16 s[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             s[nb] = zero16();
 #pragma unroll
-            for (int kk = 0; kk < KS; ++kk) s[nb] = mma<T>(rows_at<T, DP>(kt + nb * 32 * Tile<DP>::ROW, lane, kk), q[kk], s[nb]);
+            for (int kk = 0; kk < KS; ++kk) s[nb] = mma<T>(rows_at<T, DP>(kt + nb * 32 * Tile<DP>::ROW, at, kk), q[kk], s[nb]);
         }
         if (!all) {
 #pragma unroll
@@ -99,7 +100,7 @@ struct Rows {
             for (int t = 0; t < 2; ++t) {
                 const typename Vec8<T>::V p = pack8<T>(s[nb], 8 * t);
 #pragma unroll
-                for (int db = 0; db < DB; ++db) o[db] = mma<T>(cols_at<T, DP>(vt, lane, 2 * nb + t, db), p, o[db]);
+                for (int db = 0; db < DB; ++db) o[db] = mma<T>(cols_at<T, DP>(vt, at, 2 * nb + t, db), p, o[db]);
             }
         }
     }
@@ -164,7 +165,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : 2) void attn_fwd_kernel
 #pragma unroll
             for (int nb = 0; nb < kKeys / 32; ++nb) bits[nb] = row.bits(j + 32 * nb, end, a.sinks, lane);
         }
-        row.template step<kKeys / 32>(kt, vt, lane, all, bits, c, slack);
+        row.template step<kKeys / 32>(kt, vt, all, bits, c, slack);
     };
     if (t0 < t1) load(t0, k_0, v_0);
     for (int t = t0; t < t1; t += 2) {
@@ -250,7 +251,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_few_kernel(AttnArgs p
         const int j = span.at(t, kKeysFew), end = span.end(t);
         const bool whole = j + 32 <= end && j + 31 <= min(p_lo + a.right, s.lk - 1) && (j >= p_hi - a.left || j + 32 <= a.sinks);
         const uint32_t bits = whole ? 0u : row.bits(j, end, a.sinks, lane);
-        row.template step<1>(kt + wave * BYTES, vt + wave * BYTES, lane, whole, &bits, c, slack);
+        row.template step<1>(kt + wave * BYTES, vt + wave * BYTES, whole, &bits, c, slack);
     };
     const auto landed = [&](bool ahead) {  // the tile's loads; those of the next one may stay on their way
         asm volatile("" ::: "memory");
