@@ -170,7 +170,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
 // dK^T = Q^T dS, and a lane's result rows stay in registers.  WAVES to a SIMD: two leave a wave 256 registers, which do
 // not hold k's operands beside the sums at a width of 128 (they stay in LDS), one leaves 512.
 template <typename TT, int DP, int WAVES>
-__global__ __launch_bounds__(64 * kWaves, WAVES) void attn_dkv_kernel(AttnArgs p, int tiles) {
+__global__ __launch_bounds__(64 * kWaves, DP == 64 ? 3 : WAVES) void attn_dkv_kernel(AttnArgs p, int tiles) {
     typedef typename TT::type T;
     typedef typename Vec8<T>::V V8;
     constexpr int TR = DP == 128 && WAVES == 2 ? 32 : 64;
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(64 * kWaves, WAVES) void attn_dkv_kernel(AttnArgs p
             // and k's operands, in registers that the sums need)
             int ka = k_at;
             Place at_ = place;
-            asm volatile("" : "+v"(ka), "+v"(at_.rows), "+v"(at_.cols));
+            if constexpr (WAVES == 2) asm volatile("" : "+v"(ka), "+v"(at_.rows), "+v"(at_.cols));
             f32x16 x = zero16(), dp = zero16();
 #pragma unroll
             for (int kk = 0; kk < KS; ++kk) {
@@ -397,8 +397,9 @@ int key_tiles(const maxsim_attn& a) { return std::max(1, (a.max_k + kRows - 1) /
 
 // How the work on dK and dV is shared out.  Where first tokens stay visible past the window, their key tile would go
 // over all queries and the others over a window's worth: with more than two such stretches of queries the far ones get workgroups
-// of their own (8192 tokens, a window of 2048 and 4 first tokens, 32 / 8 heads: 1542 -> 686 us).  Fewer than 256
-// workgroups: several for the query heads of a key head (9 sequences of up to 601 tokens, 6 / 2 heads: TODO us).
+// of their own (8192 tokens, a window of 2048 and 4 first tokens, 32 / 8 heads: 1542 -> 686 us).  Up to 256
+// workgroups: several for the query heads of a key head (9 sequences of up to 601 tokens, 6 / 2 heads: 46 -> 37 us; 2 x 4096
+// tokens, 16 / 4 heads: 687 -> 561).
 void plan_parts(const maxsim_attn& a, AttnArgs& p) {
     p.far_tiles = p.far_chunks = p.far_tokens = p.part_tiles = p.part_rows = 0;
     p.head_splits = 1;
@@ -414,7 +415,7 @@ void plan_parts(const maxsim_attn& a, AttnArgs& p) {
         }
     }
     const int64_t items = (int64_t)a.B * a.Hk * (key_tiles(a) + p.far_tiles * p.far_chunks);
-    if (items < 256) p.head_splits = (int)std::min<int64_t>(a.Hq / a.Hk, 512 / items);
+    if (items <= 256) p.head_splits = (int)std::min<int64_t>(a.Hq / a.Hk, 512 / items);
     p.part_tiles = p.head_splits > 1 ? key_tiles(a) : p.far_tiles;
     p.part_rows = p.head_splits > 1 ? kRows : std::min(keys, kRows);
 }
@@ -433,8 +434,8 @@ hipError_t launch(const AttnArgs& p, hipStream_t stream) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t blocks = blocks_for(pairs, each);
-    // a width of 128: two workgroups to a CU where there are so many (2 x 4096 tokens, 4 key heads, 256 workgroups: one to a
-    // CU 600 us, two 780; 16 x 1024 tokens, 512: 320 and 270)
+    // a width of 128: two workgroups to a CU where there are so many (4096 tokens, 8 heads, 256 workgroups: one to a CU
+    // 185 us, two 221; 16 x 1024 tokens, 512: 320 and 247)
     const auto dkv = DP == 128 && blocks <= 256 ? attn_dkv_kernel<TT, DP, DP == 128 ? 1 : 2> : attn_dkv_kernel<TT, DP, 2>;
     dkv<<<(unsigned)blocks, 64 * kWaves, 0, stream>>>(p, k_tiles);
     e = hipGetLastError();
