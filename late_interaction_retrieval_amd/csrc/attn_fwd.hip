@@ -331,45 +331,73 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_few_kernel(AttnArgs p
     }
 }
 
-// Rows whose keys were split: their parts, joined in order.  32 threads to a row (of one head), 4 columns each.
-template <typename TT>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p, int groups) {
+// Rows whose keys were split: their parts, joined in order.  GROUPS groups of 32 threads to a row (of one head), each thread 4
+// columns of every GROUPS-th part, all of them on their way at once; the parts' references and sums are a lane's each.
+// (One thread after the other over the parts took 30 us for 64; 8 groups for two parts of 8192 rows 35 us.)
+constexpr int kMostSplits = 64;
+template <typename TT, int GROUPS>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p, int row_groups) {
     typedef typename TT::type T;
+    constexpr int ROWS = 8 / GROUPS, EACH = GROUPS == 1 ? 8 : kMostSplits / GROUPS;
+    __shared__ float factor[ROWS][kMostSplits];
+    __shared__ __align__(16) f32x4 share[GROUPS == 1 ? 1 : GROUPS][32];
     const maxsim_attn& a = p.a;
-    const int b = blockIdx.x / groups, g = blockIdx.x % groups;
+    const int b = blockIdx.x / row_groups, g = blockIdx.x % row_groups;
     const Seq s = sequence(a, b);
     if (a.zero_rest)
-        zero_rest<T>(a.out, p.lse, a.lse_step, a.cu_q, a.B, a.rows_q, b, s.q0, s.lq, s.all_q, a.Hq, a.D, g, groups, (int)blockIdx.x,
-                     (int)gridDim.x);
-    const int64_t r = (int64_t)g * 8 + (threadIdx.x >> 5);
-    if (r >= (int64_t)s.lq * a.Hq) return;
-    const int d = (threadIdx.x & 31) * 4, token = (int)(r / a.Hq), head = (int)(r % a.Hq);
+        zero_rest<T>(a.out, p.lse, a.lse_step, a.cu_q, a.B, a.rows_q, b, s.q0, s.lq, s.all_q, a.Hq, a.D, g, row_groups,
+                     (int)blockIdx.x, (int)gridDim.x);
+    const int lane = threadIdx.x & 31, group = GROUPS == 1 ? 0 : threadIdx.x >> 5, sub = GROUPS == 1 ? threadIdx.x >> 5 : 0;
+    const int r = min(g * ROWS + sub, s.lq * a.Hq - 1), d = lane * 4;
+    if (g * ROWS >= s.lq * a.Hq) return;
+    const bool mine = g * ROWS + sub < s.lq * a.Hq && d < a.D;
+    const int token = r / a.Hq, head = r % a.Hq;
     const int64_t at = (first_row(a, s, b) + token) * a.Hq + head, step = p.rows * a.Hq;
-    float most = -INFINITY;
-    for (int i = 0; i < p.splits; ++i)
-        if (!is_zero(p.part_ml[2 * (at + i * step) + 1])) most = fmaxf(most, p.part_ml[2 * (at + i * step)]);
-    float total = 0.f;
-    f32x4 o = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int i = 0; i < p.splits; ++i) {
-        const float l = p.part_ml[2 * (at + i * step) + 1];
-        const float f = is_zero(l) ? 0.f : __builtin_amdgcn_exp2f(p.part_ml[2 * (at + i * step)] - most);
-        total += l * f;
-        if (d < a.D) {
-            const f32x4 v = *reinterpret_cast<const f32x4*>(p.part_o + (at + i * step) * a.D + d);
+    f32x4 part[EACH];
+    const float* o = p.part_o + at * a.D + d;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) o[q] += v[q] * f;
-        }
+    for (int n = 0; n < EACH; ++n) {
+        const int i = group + GROUPS * n;
+        part[n] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (i < p.splits && mine) part[n] = *reinterpret_cast<const f32x4*>(o + i * step * a.D);
     }
-    const float inv = is_zero(total) ? 0.f : 1.f / total;
-    if (d < a.D) {
-        o *= inv;
+    // every wave makes its rows' factors for itself: of one row with 64 parts, or of two with 32
+    constexpr int WIDE = GROUPS == 1 ? 32 : 64;
+    const int i = threadIdx.x & (WIDE - 1);
+    float top = -INFINITY, l = 0.f;
+    if (i < p.splits) {
+        l = p.part_ml[2 * (at + i * step) + 1];
+        top = is_zero(l) ? -INFINITY : p.part_ml[2 * (at + i * step)];
+    }
+    float most = top;
+#pragma unroll
+    for (int x = 1; x < WIDE; x <<= 1) most = fmaxf(most, __shfl_xor(most, x));
+    const float f = is_zero(l) ? 0.f : __builtin_amdgcn_exp2f(top - most);
+    float total = l * f;
+#pragma unroll
+    for (int x = 1; x < WIDE; x <<= 1) total += __shfl_xor(total, x);
+    if (GROUPS == 1 || threadIdx.x < 64) factor[sub][i] = f;
+    __syncthreads();
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int n = 0; n < EACH; ++n) {
+        const int k = group + GROUPS * n;
+        if (k < p.splits && factor[sub][k] != 0.f) sum += part[n] * factor[sub][k];  // (a part of no keys holds nothing)
+    }
+    if constexpr (GROUPS > 1) {
+        share[group][lane] = sum;
+        __syncthreads();
+        if (group > 0) return;
+#pragma unroll
+        for (int k = 1; k < GROUPS; ++k) sum += share[k][lane];
+    }
+    if (mine) {
+        sum *= is_zero(total) ? 0.f : 1.f / total;
         T* rest = rest_of<T>(p, at);
         store4<T>(first<T>(a.out, a.cu_q != nullptr, b, s.q0, 0) + (int64_t)token * a.out.token + (int64_t)head * a.out.head + d,
-                  rest ? rest + d : nullptr, o);
+                  rest ? rest + d : nullptr, sum);
+        if (p.lse && lane == 0) p.lse[at * a.lse_step] = is_zero(total) ? -INFINITY : (most + __builtin_amdgcn_logf(total)) * kLn2;
     }
-    if (p.lse && (threadIdx.x & 31) == 0)
-        p.lse[at * a.lse_step] = is_zero(total) ? -INFINITY : (most + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
 struct Plan {
@@ -379,7 +407,12 @@ struct Plan {
 };
 int64_t rows_in_memory(const maxsim_attn& a) { return a.cu_q ? a.rows_q : (int64_t)a.B * a.max_q; }
 
-// Keys are split where the rows alone do not fill the chip.
+// Keys are split where the rows alone do not fill the chip and the second launch, which joins the parts, costs less
+// than what it spares.  Measured (us, one key head's worth of rows to a workgroup):
+//     a next token, 16 / 2 heads of 128:  500 keys 10.4 whole, 11.6 in parts; 852 13.1, 11.7; 8192 65.9, 13.6; 32768 250, 19
+//     512 tokens, 16 / 4 heads of 64:     768 keys 15.5 whole, 20.2 in parts; 1536 26.0, 23.8; 8192 117, 46
+// As many workgroups as there are CUs (4 x next token, 32 / 8 heads, 8192 keys: 28.7, twice as many 33.1); long keys of
+// up to 64 columns take more (512 tokens as above, 32768 keys: 130 and 103).
 Plan plan_of(const maxsim_attn& a) {
     Plan p;
     const int64_t group = a.Hq / a.Hk, rows = (int64_t)a.max_q * group;
@@ -390,14 +423,13 @@ Plan plan_of(const maxsim_attn& a) {
     int64_t keys = a.max_k;
     if (a.left >= 0 && a.right >= 0)
         keys = std::min<int64_t>(keys, (int64_t)a.left + a.right + std::min<int64_t>(rows, kRows) / group + 2 + a.sinks);
-    const int64_t wanted = p.few ? 512 : 512, least = 256;  // workgroups; keys of a split
-    int64_t splits = base > 0 ? wanted / base : 1;
-    splits = std::min(splits, keys / least);
-    p.splits = rows > 0 ? (int)std::max<int64_t>(1, std::min<int64_t>(splits, 64)) : 1;
+    const int64_t from = p.few ? 640 : 1024, least = p.few && keys < 4096 ? 128 : 256;  // keys to be split; of a part
+    const int64_t wanted = a.D <= 64 && keys >= 8192 && !p.few ? 512 : 256;
+    p.splits = 1;
+    if (base > 0 && keys >= from) p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({wanted / base, keys / least, kMostSplits}));
     p.blocks = blocks_for((int64_t)a.Hk * a.B, (int64_t)p.tiles * p.splits);
     return p;
 }
-int64_t join_groups(const maxsim_attn& a) { return ((int64_t)a.max_q * a.Hq + 7) / 8; }
 
 template <typename TT, int DP>
 void launch(const AttnArgs& p, const Plan& plan, hipStream_t stream) {
@@ -438,9 +470,12 @@ hipError_t launch_attn_fwd(const maxsim_attn& a, float* lse, void* workspace, hi
     else half ? launch<F16, 128>(p, plan, stream) : launch<BF16, 128>(p, plan, stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || plan.splits == 1) return e;
-    const int groups = (int)join_groups(a);
-    if (half) attn_join_kernel<F16><<<groups * a.B, 256, 0, stream>>>(p, groups);
-    else attn_join_kernel<BF16><<<groups * a.B, 256, 0, stream>>>(p, groups);
+    // the rows are few, or the parts are
+    const bool many = plan.splits > 8;
+    const int groups = many ? a.max_q * a.Hq : (a.max_q * a.Hq + 7) / 8;
+    const auto join = half ? (many ? attn_join_kernel<F16, 8> : attn_join_kernel<F16, 1>)
+                           : (many ? attn_join_kernel<BF16, 8> : attn_join_kernel<BF16, 1>);
+    join<<<(unsigned)groups * a.B, 256, 0, stream>>>(p, groups);
     return hipGetLastError();
 }
 
