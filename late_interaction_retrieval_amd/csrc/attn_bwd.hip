@@ -65,6 +65,18 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
     const bool mine = wr + (lane & 31) < rows;
     const bool packed = a.cu_q != nullptr;
 
+    const T* ks = first<T>(a.k, a.cu_k != nullptr, b, s.k0, h);
+    const T* vs = first<T>(a.v, a.cu_k != nullptr, b, s.k0, h);
+    Loader<DP, kTile, kWaves> lk, lv;
+    lk.init(wave, lane, a.k.token, D);
+    lv.init(wave, lane, a.v.token, D);
+    const auto load = [&](int t, uint8_t* kt, uint8_t* vt) {
+        const int j = span.at(t, kTile);
+        lk.load(ks + (int64_t)j * a.k.token, s.lk - j, a.k.token, D, kt, wave);
+        lv.load(vs + (int64_t)j * a.v.token, s.lk - j, a.v.token, D, vt, wave);
+    };
+    if (span.tiles > 0) load(0, k_0, v_0);  // on its way while the rows are read
+
     // the row's q and dO as operands, delta, and lse in powers of 2: a row that sees nothing has P = 0
     V8 q[KS], g[KS];
     const T* qr = first<T>(a.q, packed, b, s.q0, 0) + (int64_t)token * a.q.token + (int64_t)head * a.q.head;
@@ -109,16 +121,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
 #pragma unroll
     for (int db = 0; db < DB; ++db) acc[db] = zero16();
 
-    const T* ks = first<T>(a.k, a.cu_k != nullptr, b, s.k0, h);
-    const T* vs = first<T>(a.v, a.cu_k != nullptr, b, s.k0, h);
-    Loader<DP, kTile, kWaves> lk, lv;
-    lk.init(wave, lane, a.k.token, D);
-    lv.init(wave, lane, a.v.token, D);
-    const auto load = [&](int t, uint8_t* kt, uint8_t* vt) {
-        const int j = span.at(t, kTile);
-        lk.load(ks + (int64_t)j * a.k.token, s.lk - j, a.k.token, D, kt, wave);
-        lv.load(vs + (int64_t)j * a.v.token, s.lk - j, a.v.token, D, vt, wave);
-    };
     const auto work = [&](int t, const uint8_t* kt, const uint8_t* vt) {
         const int j0 = span.at(t, kTile), end = span.end(t);
         if (wr >= rows) return;
@@ -151,7 +153,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
             }
         }
     };
-    if (span.tiles > 0) load(0, k_0, v_0);
     for (int t = 0; t < span.tiles; t += 2) {
         tile_ready();
         if (t + 1 < span.tiles) load(t + 1, k_1, v_1);
@@ -208,6 +209,28 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 3 : WAVES) void attn_dkv_ke
     }
     const int steps = (max(i_hi - i_lo, 0) + TR - 1) / TR, total = steps * (g1 - g0);
 
+    const T* qs = first<T>(a.q, a.cu_q != nullptr, b, s.q0, h * G);
+    const T* gs = first<T>(p.dout, a.cu_q != nullptr, b, s.q0, h * G);
+    const int64_t row0 = first_row(a, s, b);
+    Loader<DP, TR, kWaves> lq, lg;
+    lq.init(wave, lane, a.q.token, D);
+    lg.init(wave, lane, p.dout.token, D);
+    int g_next = g0, i_next = i_lo;  // the head and the token that the next tile starts with
+    const auto load = [&](uint8_t* qt, uint8_t* gt, float* stat) {
+        lq.load(qs + (int64_t)g_next * a.q.head + (int64_t)i_next * a.q.token, s.lq - i_next, a.q.token, D, qt, wave);
+        lg.load(gs + (int64_t)g_next * p.dout.head + (int64_t)i_next * p.dout.token, s.lq - i_next, p.dout.token, D, gt, wave);
+        if (wave < STATS) {  // the rows' values of one kind; zeros past the last row, whose q and dO are zeros too
+            const uint64_t at = (uint64_t)(p.row_stat + ((int64_t)wave * a.Hq + h * G + g_next) * p.rows + row0 + i_next);
+            const uint32_t low = __builtin_amdgcn_readfirstlane((uint32_t)at), high = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
+            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+                (void*)(((uint64_t)high << 32) | low), (short)0, min(s.lq - i_next, TR) * 4, 0x00020000);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lptr_t)(stat + wave * 64), 4, lane * 4, 0, 0, 0);
+        }
+        i_next += TR;
+        if (i_next >= i_hi) i_next = i_lo, ++g_next;
+    };
+    if (total > 0) load(q_0, g_0, stat_0);  // on its way while the keys' rows are read
+
     const int wj = j0 + wave * 32, j_hi = min(wj + 31, s.lk - 1);  // the wave's keys
     const int j = min(wj + (lane & 31), s.lk - 1);
     const bool mine = wj + (lane & 31) < s.lk, packed = a.cu_k != nullptr;
@@ -236,26 +259,6 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 3 : WAVES) void attn_dkv_ke
     for (int db = 0; db < DB; ++db) dk[db] = dv[db] = zero16();
     float lift = 0.f;  // of what dk holds (fp16): the smallest of the rows' so far; 0: nothing yet
 
-    const T* qs = first<T>(a.q, a.cu_q != nullptr, b, s.q0, h * G);
-    const T* gs = first<T>(p.dout, a.cu_q != nullptr, b, s.q0, h * G);
-    const int64_t row0 = first_row(a, s, b);
-    Loader<DP, TR, kWaves> lq, lg;
-    lq.init(wave, lane, a.q.token, D);
-    lg.init(wave, lane, p.dout.token, D);
-    int g_next = g0, i_next = i_lo;  // the head and the token that the next tile starts with
-    const auto load = [&](uint8_t* qt, uint8_t* gt, float* stat) {
-        lq.load(qs + (int64_t)g_next * a.q.head + (int64_t)i_next * a.q.token, s.lq - i_next, a.q.token, D, qt, wave);
-        lg.load(gs + (int64_t)g_next * p.dout.head + (int64_t)i_next * p.dout.token, s.lq - i_next, p.dout.token, D, gt, wave);
-        if (wave < STATS) {  // the rows' values of one kind; zeros past the last row, whose q and dO are zeros too
-            const uint64_t at = (uint64_t)(p.row_stat + ((int64_t)wave * a.Hq + h * G + g_next) * p.rows + row0 + i_next);
-            const uint32_t low = __builtin_amdgcn_readfirstlane((uint32_t)at), high = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
-            const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(((uint64_t)high << 32) | low), (short)0, min(s.lq - i_next, TR) * 4, 0x00020000);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lptr_t)(stat + wave * 64), 4, lane * 4, 0, 0, 0);
-        }
-        i_next += TR;
-        if (i_next >= i_hi) i_next = i_lo, ++g_next;
-    };
     int i_now = i_lo;  // the token that the tile at hand starts with
     const auto work = [&](const uint8_t* qt, const uint8_t* gt, const float* stat) {
         const int at = i_now;
@@ -329,7 +332,6 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 3 : WAVES) void attn_dkv_ke
             }
         }
     };
-    if (total > 0) load(q_0, g_0, stat_0);
     for (int t = 0; t < total; t += 2) {
         tile_ready();
         if (t + 1 < total) load(q_1, g_1, stat_1);

@@ -132,6 +132,18 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : 2) void attn_fwd_kernel
     const Span span = span_of(a, s.lk, r0 / G + shift, last / G + shift, kKeys);
     const int t0 = (int)((int64_t)span.tiles * split / p.splits), t1 = (int)((int64_t)span.tiles * (split + 1) / p.splits);
 
+    const T* ks = first<T>(a.k, a.cu_k != nullptr, w.b, s.k0, w.h);
+    const T* vs = first<T>(a.v, a.cu_k != nullptr, w.b, s.k0, w.h);
+    Loader<DP, kKeys, kWaves> lk, lv;
+    lk.init(wave, lane, a.k.token, D);
+    lv.init(wave, lane, a.v.token, D);
+    const auto load = [&](int t, uint8_t* kt, uint8_t* vt) {
+        const int j = span.at(t, kKeys);
+        lk.load(ks + (int64_t)j * a.k.token, s.lk - j, a.k.token, D, kt, wave);
+        lv.load(vs + (int64_t)j * a.v.token, s.lk - j, a.v.token, D, vt, wave);
+    };
+    if (t0 < t1) load(t0, k_0, v_0);  // on its way while the queries are read
+
     const int wr = r0 + wave * kRowsWave;
     const int r = min(wr + (lane & 31), rows - 1), token = r / G, head = w.h * G + r % G;
     const T* qs = first<T>(a.q, a.cu_q != nullptr, w.b, s.q0, 0);
@@ -145,16 +157,6 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : 2) void attn_fwd_kernel
         return j + kKeys <= end && j + kKeys - 1 <= min(p_lo + a.right, s.lk - 1) && (j >= p_hi - a.left || j + kKeys <= a.sinks);
     };
 
-    const T* ks = first<T>(a.k, a.cu_k != nullptr, w.b, s.k0, w.h);
-    const T* vs = first<T>(a.v, a.cu_k != nullptr, w.b, s.k0, w.h);
-    Loader<DP, kKeys, kWaves> lk, lv;
-    lk.init(wave, lane, a.k.token, D);
-    lv.init(wave, lane, a.v.token, D);
-    const auto load = [&](int t, uint8_t* kt, uint8_t* vt) {
-        const int j = span.at(t, kKeys);
-        lk.load(ks + (int64_t)j * a.k.token, s.lk - j, a.k.token, D, kt, wave);
-        lv.load(vs + (int64_t)j * a.v.token, s.lk - j, a.v.token, D, vt, wave);
-    };
     const auto work = [&](int t, const uint8_t* kt, const uint8_t* vt) {
         const int j = span.at(t, kKeys), end = span.end(t);
         if (wr >= rows) return;
@@ -167,7 +169,6 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : 2) void attn_fwd_kernel
         }
         row.template step<kKeys / 32>(kt, vt, all, bits, c, slack);
     };
-    if (t0 < t1) load(t0, k_0, v_0);
     for (int t = t0; t < t1; t += 2) {
         tile_ready();
         if (t + 1 < t1) load(t + 1, k_1, v_1);
