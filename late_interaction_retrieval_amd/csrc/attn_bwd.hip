@@ -70,12 +70,14 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
     Loader<DP, kTile, kWaves> lk, lv;
     lk.init(wave, lane, a.k.token, D);
     lv.init(wave, lane, a.v.token, D);
-    const auto load = [&](int t, uint8_t* kt, uint8_t* vt) {
-        const int j = span.at(t, kTile);
-        lk.load(ks + (int64_t)j * a.k.token, s.lk - j, a.k.token, D, kt, wave);
-        lv.load(vs + (int64_t)j * a.v.token, s.lk - j, a.v.token, D, vt, wave);
+    Walk<T> next;
+    next.start(span, 0, kTile, ks, vs, a.k.token, a.v.token);
+    const auto load = [&](uint8_t* kt, uint8_t* vt) {
+        lk.load(next.k, s.lk - next.j, a.k.token, D, kt, wave);
+        lv.load(next.v, s.lk - next.j, a.v.token, D, vt, wave);
+        next.next(span, kTile, ks, vs, a.k.token, a.v.token);
     };
-    if (span.tiles > 0) load(0, k_0, v_0);  // on its way while the rows are read
+    if (span.tiles > 0) load(k_0, v_0);  // on its way while the rows are read
 
     // the row's q and dO as operands, delta, and lse in powers of 2: a row that sees nothing has P = 0
     V8 q[KS], g[KS];
@@ -155,11 +157,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
     };
     for (int t = 0; t < span.tiles; t += 2) {
         tile_ready();
-        if (t + 1 < span.tiles) load(t + 1, k_1, v_1);
+        if (t + 1 < span.tiles) load(k_1, v_1);
         work(t, k_0, v_0);
         if (t + 1 >= span.tiles) break;
         tile_ready();
-        if (t + 2 < span.tiles) load(t + 2, k_0, v_0);
+        if (t + 2 < span.tiles) load(k_0, v_0);
         work(t + 1, k_1, v_1);
     }
     T* out = first<T>(p.dq, packed, b, s.q0, 0) + (int64_t)token * p.dq.token + (int64_t)head * p.dq.head;
@@ -215,19 +217,33 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 3 : WAVES) void attn_dkv_ke
     Loader<DP, TR, kWaves> lq, lg;
     lq.init(wave, lane, a.q.token, D);
     lg.init(wave, lane, p.dout.token, D);
-    int g_next = g0, i_next = i_lo;  // the head and the token that the next tile starts with
+    // the token that the next tile starts with, and where q, dO and the rows' values lie there
+    int i_next = i_lo;
+    const T* q_next = qs + (int64_t)g0 * a.q.head + (int64_t)i_lo * a.q.token;
+    const T* g_next = gs + (int64_t)g0 * p.dout.head + (int64_t)i_lo * p.dout.token;
+    const float* stat_next = p.row_stat + ((int64_t)wave * a.Hq + h * G + g0) * p.rows + row0 + i_lo;
+    const int64_t q_back = a.q.head - (int64_t)steps * TR * a.q.token, g_back = p.dout.head - (int64_t)steps * TR * p.dout.token;
+    const int64_t stat_back = p.rows - (int64_t)steps * TR;
     const auto load = [&](uint8_t* qt, uint8_t* gt, float* stat) {
-        lq.load(qs + (int64_t)g_next * a.q.head + (int64_t)i_next * a.q.token, s.lq - i_next, a.q.token, D, qt, wave);
-        lg.load(gs + (int64_t)g_next * p.dout.head + (int64_t)i_next * p.dout.token, s.lq - i_next, p.dout.token, D, gt, wave);
+        lq.load(q_next, s.lq - i_next, a.q.token, D, qt, wave);
+        lg.load(g_next, s.lq - i_next, p.dout.token, D, gt, wave);
         if (wave < STATS) {  // the rows' values of one kind; zeros past the last row, whose q and dO are zeros too
-            const uint64_t at = (uint64_t)(p.row_stat + ((int64_t)wave * a.Hq + h * G + g_next) * p.rows + row0 + i_next);
+            const uint64_t at = (uint64_t)stat_next;
             const uint32_t low = __builtin_amdgcn_readfirstlane((uint32_t)at), high = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
             const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
                 (void*)(((uint64_t)high << 32) | low), (short)0, min(s.lq - i_next, TR) * 4, 0x00020000);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lptr_t)(stat + wave * 64), 4, lane * 4, 0, 0, 0);
         }
         i_next += TR;
-        if (i_next >= i_hi) i_next = i_lo, ++g_next;
+        q_next += TR * a.q.token;
+        g_next += TR * p.dout.token;
+        stat_next += TR;
+        if (i_next >= i_hi) {  // on to the next head
+            i_next = i_lo;
+            q_next += q_back;
+            g_next += g_back;
+            stat_next += stat_back;
+        }
     };
     if (total > 0) load(q_0, g_0, stat_0);  // on its way while the keys' rows are read
 

@@ -125,6 +125,32 @@ __device__ __forceinline__ Span span_of(const maxsim_attn& a, int lk, int p_lo, 
     return s;
 }
 
+// The tiles of a span one after the other, from tile t0 on: the key that the next one starts with, and where k and v lie
+// there.  (A product of 64 bits for each tile cost the scalar unit as much as the tile's softmax the vector unit.)
+template <typename T>
+struct Walk {
+    const T *k, *v;
+    int j, t;
+    __device__ __forceinline__ void start(const Span& s, int t0, int step, const T* k0, const T* v0, int64_t kt, int64_t vt) {
+        t = t0;
+        j = s.at(t0, step);
+        k = k0 + (int64_t)j * kt;
+        v = v0 + (int64_t)j * vt;
+    }
+    __device__ __forceinline__ void next(const Span& s, int step, const T* k0, const T* v0, int64_t kt, int64_t vt) {
+        ++t;
+        if (t == s.first) {  // on to the window
+            j = s.lo;
+            k = k0 + (int64_t)j * kt;
+            v = v0 + (int64_t)j * vt;
+        } else {
+            j += step;
+            k += step * kt;
+            v += step * vt;
+        }
+    }
+};
+
 // What a block works on: sequence b, key head h, and one of the `each` parts of their work.  Blocks go round-robin over
 // the 8 XCDs; the parts of one (b, h) read the same keys and go to one XCD, whose L2 holds them.  Many (b, h), of
 // lengths that differ, are dealt out in turn; few of them in runs, which leave no XCD without work (16 sequences of

@@ -137,12 +137,14 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : 2) void attn_fwd_kernel
     Loader<DP, kKeys, kWaves> lk, lv;
     lk.init(wave, lane, a.k.token, D);
     lv.init(wave, lane, a.v.token, D);
-    const auto load = [&](int t, uint8_t* kt, uint8_t* vt) {
-        const int j = span.at(t, kKeys);
-        lk.load(ks + (int64_t)j * a.k.token, s.lk - j, a.k.token, D, kt, wave);
-        lv.load(vs + (int64_t)j * a.v.token, s.lk - j, a.v.token, D, vt, wave);
+    Walk<T> next;
+    next.start(span, t0, kKeys, ks, vs, a.k.token, a.v.token);
+    const auto load = [&](uint8_t* kt, uint8_t* vt) {
+        lk.load(next.k, s.lk - next.j, a.k.token, D, kt, wave);
+        lv.load(next.v, s.lk - next.j, a.v.token, D, vt, wave);
+        next.next(span, kKeys, ks, vs, a.k.token, a.v.token);
     };
-    if (t0 < t1) load(t0, k_0, v_0);  // on its way while the queries are read
+    if (t0 < t1) load(k_0, v_0);  // on its way while the queries are read
 
     const int wr = r0 + wave * kRowsWave;
     const int r = min(wr + (lane & 31), rows - 1), token = r / G, head = w.h * G + r % G;
@@ -171,11 +173,11 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : 2) void attn_fwd_kernel
     };
     for (int t = t0; t < t1; t += 2) {
         tile_ready();
-        if (t + 1 < t1) load(t + 1, k_1, v_1);
+        if (t + 1 < t1) load(k_1, v_1);
         work(t, k_0, v_0);
         if (t + 1 >= t1) break;
         tile_ready();
-        if (t + 2 < t1) load(t + 2, k_0, v_0);
+        if (t + 2 < t1) load(k_0, v_0);
         work(t + 1, k_1, v_1);
     }
 
