@@ -48,7 +48,7 @@ enum { MAXSIM_ROPE_HALF = 0 /* (i, i + rotary/2) */, MAXSIM_ROPE_INTERLEAVED = 1
  *   offsets    [B] int32, or NULL.  (Not both.)
  * The angle is formed in fp64 and brought into one turn before it is rounded, so that far positions
  * lose nothing; sine and cosine are fp32.  Rows need the alignment of one element (16 bytes are fastest).
- * Requires B, L >= 0, H >= 1, 1 <= D <= 1024, rotary even, 2 <= rotary <= D, B * L < 2^26 and scale finite.
+ * Requires B, L >= 0, H >= 1, 1 <= D <= 1024, rotary even, 2 <= rotary <= D, B * L < 2^25 and scale finite.
  */
 int maxsim_rope(const maxsim_view* x, const maxsim_view* y, int32_t B, int32_t L, int32_t H, int32_t D, int32_t rotary,
                 int32_t layout, int32_t dtype, const double* inv_freq, const int32_t* positions, const int32_t* offsets,
@@ -93,7 +93,7 @@ typedef struct {
     int32_t lse_step;
 } maxsim_attn;
 
-/* Bytes of device workspace (may be 0; 0 on bad sizes).  Only sizes, types and the window are looked at. */
+/* Bytes of device workspace (may be 0; 0 on bad sizes).  Sizes, type, the window and which lengths are given are looked at, no data. */
 size_t maxsim_attn_fwd_workspace_bytes(const maxsim_attn* a);
 size_t maxsim_attn_bwd_workspace_bytes(const maxsim_attn* a);
 

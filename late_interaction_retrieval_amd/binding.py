@@ -1424,8 +1424,10 @@ def _attn_fwd(q, k, v, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, 
         a.lse_step = 1 + q.shape[-1] // 2
         lse = make(q.shape[:-1] + (a.lse_step,), dtype=torch.float32, device=q.device)[..., 0]
     a.zero_rest = not given and (cu_q is not None or q_lens is not None)
-    if a.B == 0 and a.zero_rest:
+    if a.B == 0 and a.zero_rest:  # rows of no sequence, all of them
         out.zero_()
+        if lse is not None:
+            lse.zero_()
     workspace, nbytes = _workspace(q, workspace, _lib.maxsim_attn_fwd_workspace_bytes(ctypes.byref(a)))
     st = _lib.maxsim_attn_fwd(ctypes.byref(a), None if lse is None else lse.data_ptr(),
                               None if workspace is None else workspace.data_ptr(), nbytes, _raw_stream(q.device))

@@ -494,6 +494,7 @@ hipError_t launch_attn_bwd(const maxsim_attn& a, const float* lse, const maxsim_
     p.row_stat = static_cast<float*>(workspace);
     p.part = p.row_stat + stat_floats(a);
     const bool half = a.dtype == MAXSIM_F16;
+    (void)hipGetLastError();  // an error that an earlier call left unread is not this one's
     if (a.D <= 64) return half ? launch<F16, 64>(p, stream) : launch<BF16, 64>(p, stream);
     return half ? launch<F16, 128>(p, stream) : launch<BF16, 128>(p, stream);
 }

@@ -126,7 +126,7 @@ __device__ __forceinline__ Span span_of(const maxsim_attn& a, int lk, int p_lo, 
 }
 
 // The tiles of a span one after the other, from tile t0 on: the key that the next one starts with, and where k and v lie
-// there.  (A product of 64 bits for each tile cost the scalar unit as much as the tile's softmax the vector unit.)
+// there.
 template <typename T>
 struct Walk {
     const T *k, *v;

@@ -471,6 +471,7 @@ hipError_t launch_attn_fwd(const maxsim_attn& a, float* lse, void* workspace, hi
     p.part_o = static_cast<float*>(workspace);
     p.part_ml = p.part_o + (size_t)plan.splits * p.rows * a.Hq * a.D;
     const bool half = a.dtype == MAXSIM_F16;
+    (void)hipGetLastError();  // an error that an earlier call left unread is not this one's
     if (a.D <= 64) half ? launch<F16, 64>(p, plan, stream) : launch<BF16, 64>(p, plan, stream);
     else half ? launch<F16, 128>(p, plan, stream) : launch<BF16, 128>(p, plan, stream);
     const hipError_t e = hipGetLastError();

@@ -65,7 +65,7 @@ int maxsim_rope(const maxsim_view* x, const maxsim_view* y, int32_t B, int32_t L
         return MAXSIM_ERR_SHAPE;
     if (D > 1024 || !is_float(dtype) || (layout != MAXSIM_ROPE_HALF && layout != MAXSIM_ROPE_INTERLEAVED))
         return MAXSIM_ERR_UNSUPPORTED;
-    if ((int64_t)B * L >= (int64_t)1 << 26 || (positions && offsets)) return MAXSIM_ERR_SHAPE;
+    if ((int64_t)B * L >= (int64_t)1 << 25 || (positions && offsets)) return MAXSIM_ERR_SHAPE;
     if (!x || !y) return MAXSIM_ERR_NULL;
     if (!steps_ok(*x) || !steps_ok(*y) || !apart(*y, D, H, L, B)) return MAXSIM_ERR_SHAPE;
     if (B == 0 || L == 0) return MAXSIM_OK;

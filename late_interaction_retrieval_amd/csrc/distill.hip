@@ -320,6 +320,7 @@ DistillPlan backward_plan(int N, int V) { return plan_of(N, V, kShortRow); }
 template <typename TT>
 hipError_t fwd(const DistillArgs& a, hipStream_t stream) {
     const DistillPlan d = forward_plan(a.N, a.V);
+    (void)hipGetLastError();  // an error that an earlier call left unread is not this one's
     if (d.splits > 1) {
         distill_part_kernel<TT><<<(unsigned)(a.N * d.splits), kThreads, 0, stream>>>(a, d.splits, d.width);
         const hipError_t e = hipGetLastError();
@@ -335,6 +336,7 @@ hipError_t fwd(const DistillArgs& a, hipStream_t stream) {
 template <typename TT>
 hipError_t bwd(const DistillArgs& a, hipStream_t stream) {
     const DistillPlan d = backward_plan(a.N, a.V);
+    (void)hipGetLastError();
     const size_t lds = (size_t)((a.K + 3) / 4 * 4) * 8;
     const size_t bytes = (size_t)a.N * a.V * (a.dtype == MAXSIM_F32 ? 4 : 2);
     if (a.V <= kShortRow)

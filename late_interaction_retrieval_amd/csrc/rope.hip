@@ -41,13 +41,12 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs p, RopePlan pla
     typedef typename TT::type T;
     __shared__ __align__(16) float cosine[kTable], sine[kTable];
     const int half = p.rotary / 2;
-    const int64_t all = (int64_t)p.B * p.L, t0 = (int64_t)(blockIdx.x / plan.splits) * plan.tokens;
+    const int t0 = (int)(blockIdx.x / plan.splits) * plan.tokens;  // B * L < 2^25
     const int h0 = (int)(blockIdx.x % plan.splits) * plan.heads;
-    const int tokens = (int)min((int64_t)plan.tokens, all - t0), heads = min(plan.heads, p.H - h0);
+    const int tokens = min(plan.tokens, p.B * p.L - t0), heads = min(plan.heads, p.H - h0);
     for (int e = threadIdx.x; e < tokens * plan.pitch; e += kThreads) {
         const int k = e / plan.pitch, i = e - k * plan.pitch;
-        const int64_t t = t0 + k;
-        const int b = (int)(t / p.L), l = (int)(t - (int64_t)b * p.L);
+        const int t = t0 + k, b = t / p.L, l = t - b * p.L;
         const double at = p.positions ? (double)p.positions[t] : (double)l + (p.offsets ? (double)p.offsets[b] : 0.0);
         const double turns = i < half ? at * (p.inv_freq[i] * 0.15915494309189533577) : 0.0;
         float s, c;
@@ -64,8 +63,7 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(RopeArgs p, RopePlan pla
     int k = 0, h = (int)threadIdx.x / plan.units;
     while (h >= heads) h -= heads, ++k;
     for (; k < tokens;) {
-        const int64_t t = t0 + k;
-        const int b = (int)(t / p.L), l = (int)(t - (int64_t)b * p.L);
+        const int t = t0 + k, b = t / p.L, l = t - b * p.L;
         const T* x = (const T*)p.x.data + b * p.x.batch + l * p.x.token + (int64_t)(h0 + h) * p.x.head;
         T* y = (T*)p.y.data + b * p.y.batch + l * p.y.token + (int64_t)(h0 + h) * p.y.head;
         const float *cs = cosine + k * plan.pitch, *sn = sine + k * plan.pitch;
@@ -121,6 +119,7 @@ hipError_t launch_rope(const RopeArgs& a, hipStream_t stream) {
     const auto kernel = a.dtype == MAXSIM_F32    ? (stream_past ? rope_kernel<F32, true> : rope_kernel<F32, false>)
                         : a.dtype == MAXSIM_BF16 ? (stream_past ? rope_kernel<BF16, true> : rope_kernel<BF16, false>)
                                                  : (stream_past ? rope_kernel<F16, true> : rope_kernel<F16, false>);
+    (void)hipGetLastError();  // an error that an earlier call left unread is not this one's
     kernel<<<blocks, kThreads, 0, stream>>>(a, plan);
     return hipGetLastError();
 }

@@ -310,3 +310,72 @@ def test_autograd(bd):
     assert torch.equal(got, full.sum(0, keepdim=True))
     with torch.no_grad():
         assert torch.equal(bd.attention(d["q"], d["k"], d["v"], **how), run(bd, c)[0])
+
+
+def test_packed_queries_against_a_padded_cache(bd):
+    """The queries' layout and the keys' are independent: packed new tokens against a cache with room left, and the other way."""
+    c = case(BF16, [3, 0, 9, 1], [40, 77, 9, 130], 4, 2, 64, (50, 0), 2, train=True, Lk=150)
+    d, how = device_args(c)
+    want = run(bd, c)
+    nq, nk, lq = torch.tensor(c["nq"]), torch.tensor(c["nk"]), c["Lq"]
+    q_rows = torch.cat([torch.arange(n) + b * lq for b, n in enumerate(c["nq"])]).to(DEV)
+    k_rows = torch.cat([torch.arange(n) + b * 150 for b, n in enumerate(c["nk"])]).to(DEV)
+    pick = lambda t, rows: t.flatten(0, 1)[rows].contiguous()  # noqa: E731
+    how = dict(window=(50, 0), sinks=2)
+    for packed_q in (True, False):
+        q, g = (pick(d[n], q_rows) if packed_q else d[n] for n in "qg")
+        k, v = (d[n] if packed_q else pick(d[n], k_rows) for n in "kv")
+        lens = dict(cu_q=cu_of(c["nq"]).to(DEV), max_q=9, k_lens=nk.to(torch.int32).to(DEV)) if packed_q else \
+            dict(q_lens=nq.to(torch.int32).to(DEV), cu_k=cu_of(c["nk"]).to(DEV), max_k=130)
+        out, lse = bd.maxsim_attn_fwd(q, k, v, with_lse=True, **how, **lens)
+        got = [out, lse] + list(bd.maxsim_attn_bwd(g, q, k, v, out, lse, **how, **lens))
+        for a, b, m in zip(got, want, "qqqkk"):
+            if (m == "q") == packed_q:
+                b = pick(b, q_rows if m == "q" else k_rows)
+            assert torch.equal(a, b), m
+
+
+@pytest.mark.parametrize("G,B,L", [(4, 1, 700), (3, 9, 300), (1, 2, 900), (8, 1, 40)])
+def test_few_key_tiles_share_out_their_query_heads(bd, G, B, L):
+    """dK and dV in parts: of query heads, and of far queries of the first tokens; with one query head in none."""
+    n = [L] + [max(1, L // (i + 2)) for i in range(B - 1)]
+    run(bd, case(BF16, n, n, 2 * G, 2, 128, (60, 0), 3, packed=True, train=True))
+    run(bd, case(F16, n, n, G, 1, 64, (-1, -1), 0, train=True))
+
+
+def test_first_tokens_past_a_key_tile(bd):
+    """More first tokens than a tile of keys, and as many as the split allows, over sequences much longer than the window."""
+    for sinks in (130, 256, 257):
+        run(bd, case(BF16, [900, 131], [900, 131], 2, 1, 64, (20, 0), sinks, packed=True, train=True))
+    run(bd, case(BF16, [500], [900], 2, 2, 64, (20, 5), 9, train=True))
+    run(bd, case(F16, [900], [500], 2, 2, 64, (20, 5), 9, train=True))
+
+
+def test_more_query_sequences_than_fit_a_round_of_xcds(bd):
+    """Numbers of (sequence, key head) pairs that are dealt out over the XCDs in turn, in runs, and with a rest."""
+    for B, Hk in ((9, 1), (8, 1), (65, 1), (13, 5), (3, 1)):
+        n = [1 + (7 * i) % 60 for i in range(B)]
+        run(bd, case(BF16, n, n, Hk, Hk, 16, (9, 9), 1, packed=True, train=True))
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_seeded_random_calls(bd, seed):
+    """Sizes, layouts, windows and head counts by a seed, forward and backward within their bounds."""
+    import random
+    r = random.Random(seed)
+    Hk = r.choice([1, 1, 2, 3])
+    packed = r.random() < 0.5
+    nk = [r.choice([0, 1, r.randint(1, 60), r.randint(1, 330)]) for _ in range(r.choice([1, 2, 5]))]
+    if max(nk) == 0:
+        nk[0] = 17
+    kind = r.choice(["same", "same", "fewer", "any"])
+    nq = [n if kind == "same" else r.randint(0, n) if kind == "fewer" else r.randint(0, 200) for n in nk]
+    if max(nq) == 0:
+        nq[0] = 1
+    window = (r.choice([-1, 0, r.randint(1, 30), r.randint(1, 300)]), r.choice([-1, 0, 0, r.randint(1, 100)]))
+    c = case(r.choice([F16, BF16]), nq, nk, Hk * r.choice([1, 2, 5]), Hk, 8 * r.randint(1, 16), window,
+             r.choice([0, 1, 4, 40, 300]), packed=packed, train=True, more=r.choice([0, 3]), size=r.choice([0.3, 1.0, 3.0]))
+    if not packed:
+        c = case(c["t"]["q"].dtype, nq, nk, c["t"]["q"].shape[1], Hk, c["D"], window, c["sinks"], train=True,
+                 Lq=max(nq) + r.choice([0, 2]), Lk=max(nk) + r.choice([0, 70]))
+    run(bd, c, where="seed %d" % seed)

@@ -57,7 +57,7 @@ def rope(xv=None, yv=None, **kw):
 @pytest.mark.parametrize("want,kw", [
     (SHAPE, dict(B=-1)), (SHAPE, dict(L=-1)), (SHAPE, dict(H=0)), (SHAPE, dict(D=0)), (SHAPE, dict(rotary=0)),
     (SHAPE, dict(rotary=63)), (SHAPE, dict(rotary=66)), (SHAPE, dict(scale=float("nan"))), (SHAPE, dict(scale=float("inf"))),
-    (SHAPE, dict(B=1 << 13, L=1 << 13)), (SHAPE, dict(pos=A, off=A)), (UNSUPPORTED, dict(dt=I8)), (UNSUPPORTED, dict(layout=2)),
+    (SHAPE, dict(B=1 << 13, L=1 << 12)), (SHAPE, dict(pos=A, off=A)), (UNSUPPORTED, dict(dt=I8)), (UNSUPPORTED, dict(layout=2)),
     (UNSUPPORTED, dict(D=1026, yv=view(token=4096, head=2048))), (SHAPE, dict(yv=view(head=63))), (SHAPE, dict(yv=view(token=63))),
     (SHAPE, dict(yv=view(batch=63))), (SHAPE, dict(xv=view(token=-1))), (SHAPE, dict(yv=view(batch=1 << 41))),
     (SHAPE, dict(yv=view(head=128))),  # x's memory with other steps
