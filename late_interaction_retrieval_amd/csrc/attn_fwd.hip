@@ -7,6 +7,21 @@
 // queries as columns: S^T = K Q^T leaves a query's scores in one lane pair, so its maximum
 // and sum need one exchange between lanes and the factors of a new maximum are the lane's own; P^T goes
 // from the registers it was made in to out^T = V^T P^T as it stands.
+//
+// What bounds it: with many keys the matrix pipes and the exponentials together (a 64 x 32 tile at a width of 128 is
+// 1024 cycles of matrix instructions and about 900 of the vector unit, half of them exponentials at a quarter of its rate);
+// two waves to a SIMD overlap them to 52 % of the matrix pipes' cycles.  LDS has no bank conflicts.  A next
+// token is bound by the cache's bytes.  Measured, the kernels alone:
+//     8192 tokens, causal, 2048 back and the first 4, 32 / 8 heads of 128, bf16     260 us, 0.93 PFLOP/s of the pairs that see
+//                                                                            each other (library product of 8192^3: 1.2 - 1.4)
+//     2 x 4096 tokens, 16 / 4 heads of 128, all pairs                        275 us, 1.00 PFLOP/s
+//     2 x 4096 tokens, 32 heads of 64, all pairs                             313 us, 0.88 PFLOP/s
+//     64 packed documents of 32 to 1024 tokens, 128 to each side and the first, 16 heads of 64    84 - 89 us: the vector unit (79 %
+//                                              of a resident wave's share), 3616 workgroups in 3.5 rounds, 4576 that find nothing
+//     16 next tokens, caches of 8192 to 32768 keys, 8 key heads of 128       266 us + 6.6 the join, 1.45 GB at 5.4 TB/s
+// Tried and slower: the next tile's scores made beside this one's softmax (through the branches between them the compiler
+// moves the accumulators to memory: 8 times the time); leaving out hidden blocks of 32 keys, or their exponentials, by
+// branches (89 -> 98 and 117 us); first tokens in blocks of 32 before the window's tiles (no difference).
 #include <algorithm>
 
 #include "attn_dev.h"
@@ -49,8 +64,7 @@ struct Rows {
         return slots_seen(lo - j, min(hi, end - 1) - j, sinks - j);
     }
 
-    // NB blocks of 32 keys.  all: every row sees all of them; else bits[nb] are the lane's.  (Leaving out a block that no
-    // row sees, by a branch, was slower: 88 -> 98 us over ragged documents, 284 -> 300 over whole rows of 4096 keys.)
+    // NB blocks of 32 keys.  all: every row sees all of them; else bits[nb] are the lane's.
     // The reference stays while the maximum passes it by less than 2^8: P grows to 256 at most, which both types hold,
     // and relative to the row's sum nothing is lost.
     template <int NB>

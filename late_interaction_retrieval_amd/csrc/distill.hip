@@ -9,6 +9,9 @@
 // dloss T p over the whole row and then the entries' columns again.  Few long rows are split over
 // workgroups.  Differences z - max are formed before they are multiplied by 1 / T, and the backward gets
 // the maximum and the sum's logarithm apart, so that large scores at a low temperature lose nothing.
+//
+// Measured, the kernels alone: 8192 x 32768 bf16 forward 125 - 128 us (537 MB at 4.2 TB/s), backward 209 - 213 (1.07 GB at
+// 5.1); 32 x 200003 fp32 forward 7.4 + 5.0 (the parts' join), backward 12.3; 64 x 64 4.8 and 5.4, a launch each.
 #include <algorithm>
 
 #include "encoder_dev.h"
@@ -216,7 +219,7 @@ __global__ __launch_bounds__(64) void distill_finish_kernel(DistillArgs p, int s
 
 // dz over columns [from, to) of a row by TPR threads, and the entries among them.  The first columns are on their way
 // while the entries are looked at.  STREAM: scores past what the last cache holds (256 MB), which would only push each other out of it
-// (8192 x 32768 bf16: 222 -> 202 us, and the next forward 155 -> 126).
+// (8192 x 32768 bf16: 225 -> 213 us, and the next forward 158 -> 123).
 template <typename TT, int TPR, bool STREAM>
 __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(DistillArgs p, int splits, int width) {
     typedef typename TT::type T;

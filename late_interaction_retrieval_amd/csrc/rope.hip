@@ -8,6 +8,9 @@
 //
 // The angle is a product in fp64 in turns, whose whole part is dropped before it becomes fp32: at position 2^20 a
 // product in fp32 would be off by up to 0.06 radians.
+//
+// Measured, the kernel alone: 32768 tokens, 20 heads of 128, bf16 63.5 us, 336 MB at 5.3 TB/s (a copy of 1 GiB: 5.1);
+// 5003 tokens, 7 heads of 80, 48 turned, fp32 6.3 - 7.2, 22 MB in cache; 8 next tokens 3.4, a launch.
 #include <algorithm>
 
 #include "encoder_dev.h"
