@@ -260,6 +260,10 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_few_kernel(AttnArgs p
     lv.init(0, lane, a.v.token, D);
     constexpr int LOADS = 2 * Loader<DP, kKeysFew, 1>::N;  // on their way for the next tile
     const auto load = [&](int t, uint8_t* kt, uint8_t* vt) {
+        // the reads of what these loads overwrite are done, not only on their way
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        asm volatile("" ::: "memory");
         const int j = span.at(t, kKeysFew);
         lk.load(ks + (int64_t)j * a.k.token, s.lk - j, a.k.token, D, kt + wave * BYTES, 0);
         lv.load(vs + (int64_t)j * a.v.token, s.lk - j, a.v.token, D, vt + wave * BYTES, 0);
