@@ -74,8 +74,10 @@ int maxsim_rope(const maxsim_view* x, const maxsim_view* y, int32_t B, int32_t L
  * Rows of no sequence (past a sequence's length, past the last one) are not read; in outputs they are
  * left as they were, or made 0 where zero_rest is not 0 (of packed rows: those past the last sequence).
  * Scores, statistics and sums are fp32; P (and in the backward dS) is rounded to dtype for its product, as
- * the matrix cores take it; each output is rounded once.  Values of one sequence have to be finite: a NaN or an
- * infinity reaches all rows that see it and may reach rows near them that do not.
+ * the matrix cores take it; each output is rounded once.  Keys that no query of their sequence sees are not read and
+ * may hold anything (entries dropped from a cache; their gradients are 0).  A NaN or an infinity elsewhere in a
+ * sequence reaches all rows that see it and may reach rows near them that do not.  fp16 gradients pass dO (v_j - out),
+ * with dO's row scaled to at most 2, through fp16: sure to hold while |v| <= 128, and beyond that where that product does.
  * Requires data 16-byte aligned and steps multiples of 8, token steps of at least D and at most 2^20; D a multiple of 8 from 8 to 128;
  * Hq a multiple of Hk; 0 <= max_q * (Hq / Hk), max_k < 2^29; scale finite and > 0; sinks >= 0; and tiles of
  * 128 rows, of queries (max_q * (Hq / Hk)) or keys, of which B * Hk times one more than there are stay below 2^21.

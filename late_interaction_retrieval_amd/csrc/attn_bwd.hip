@@ -82,8 +82,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
     Walk<T> next;
     next.start(span, 0, kTile, ks, vs, a.k.token, a.v.token);
     const auto load = [&](uint8_t* kt, uint8_t* vt) {
-        lk.load(next.k, s.lk - next.j, a.k.token, D, kt, wave);
-        lv.load(next.v, s.lk - next.j, a.v.token, D, vt, wave);
+        const int left = span.end(next.t) - next.j;
+        lk.load(next.k, left, a.k.token, D, kt, wave);
+        lv.load(next.v, left, a.v.token, D, vt, wave);
         next.next(span, kTile, ks, vs, a.k.token, a.v.token);
     };
     if (span.tiles > 0) load(k_0, v_0);  // on its way while the rows are read
@@ -234,13 +235,13 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 3 : WAVES) void attn_dkv_ke
     const int64_t q_back = a.q.head - (int64_t)steps * TR * a.q.token, g_back = p.dout.head - (int64_t)steps * TR * p.dout.token;
     const int64_t stat_back = p.rows - (int64_t)steps * TR;
     const auto load = [&](uint8_t* qt, uint8_t* gt, float* stat) {
-        lq.load(q_next, s.lq - i_next, a.q.token, D, qt, wave);
-        lg.load(g_next, s.lq - i_next, p.dout.token, D, gt, wave);
+        lq.load(q_next, i_hi - i_next, a.q.token, D, qt, wave);
+        lg.load(g_next, i_hi - i_next, p.dout.token, D, gt, wave);
         if (wave < STATS) {  // the rows' values of one kind; zeros past the last row, whose q and dO are zeros too
             const uint64_t at = (uint64_t)stat_next;
             const uint32_t low = __builtin_amdgcn_readfirstlane((uint32_t)at), high = __builtin_amdgcn_readfirstlane((uint32_t)(at >> 32));
             const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-                (void*)(((uint64_t)high << 32) | low), (short)0, min(s.lq - i_next, TR) * 4, 0x00020000);
+                (void*)(((uint64_t)high << 32) | low), (short)0, min(i_hi - i_next, TR) * 4, 0x00020000);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lptr_t)(stat + wave * 64), 4, lane * 4, 0, 0, 0);
         }
         i_next += TR;
@@ -262,18 +263,19 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 3 : WAVES) void attn_dkv_ke
     V8 k[K_IN_LDS ? 1 : KS], v[KS];
     const int k_at = wave * KS * 1024 + lane * 16;
     const Place place = place_of<DP>(lane);
-    const T* kr = first<T>(a.k, packed, b, s.k0, h) + (int64_t)j * a.k.token;
-    const T* vr = first<T>(a.v, packed, b, s.k0, h) + (int64_t)j * a.v.token;
-#pragma unroll
-    for (int kk = 0; kk < KS; ++kk) {
-        const V8 x = row8<T>(kr, 16 * kk + 8 * (lane >> 5), D);
-        if constexpr (K_IN_LDS) *reinterpret_cast<V8*>(k_lds + k_at + kk * 1024) = x;
-        else k[kk] = x;
-        v[kk] = row8<T>(vr, 16 * kk + 8 * (lane >> 5), D);
-    }
-    // the lane's key is seen by tokens [lo, hi] of these
+    // the lane's key is seen by tokens [lo, hi] of these; one that none of them sees is zeros, whatever it holds
     const int hi_first = i_hi - 1, hi_plain = far ? -1 : min(i_hi - 1, j + a.left - shift);
     const int lo = max(i_lo, j - a.right - shift), hi = j < a.sinks ? hi_first : hi_plain;
+    const T* kr = first<T>(a.k, packed, b, s.k0, h) + (int64_t)j * a.k.token;
+    const T* vr = first<T>(a.v, packed, b, s.k0, h) + (int64_t)j * a.v.token;
+    const int columns = lo <= hi ? D : 0;
+#pragma unroll
+    for (int kk = 0; kk < KS; ++kk) {
+        const V8 x = row8<T>(kr, 16 * kk + 8 * (lane >> 5), columns);
+        if constexpr (K_IN_LDS) *reinterpret_cast<V8*>(k_lds + k_at + kk * 1024) = x;
+        else k[kk] = x;
+        v[kk] = row8<T>(vr, 16 * kk + 8 * (lane >> 5), columns);
+    }
     // all of the wave's keys by tokens [all_lo, all_hi], any of them by [any_lo, any_hi]
     const int all_lo = max(i_lo, j_hi - a.right - shift), any_lo = max(i_lo, wj - a.right - shift);
     const int all_hi = j_hi < a.sinks ? hi_first : far ? -1 : min(i_hi - 1, wj + a.left - shift);

@@ -107,7 +107,8 @@ __device__ __forceinline__ int64_t first_row(const maxsim_attn& a, const Seq& s,
 }
 
 // The keys that a workgroup's rows see, cut into tiles: `first` tiles over the keys [0, sinks) that lie
-// before the window, then [lo, hi).
+// before the window, then [lo, hi).  What none of the rows sees is in no tile and is not read: entries that were
+// dropped from a cache may hold anything, and 0 times a NaN is not 0.
 struct Span {
     int lo, hi, sink_end, first, tiles;
     __device__ __forceinline__ int at(int t, int step) const { return t < first ? t * step : lo + (t - first) * step; }
@@ -117,8 +118,7 @@ __device__ __forceinline__ Span span_of(const maxsim_attn& a, int lk, int p_lo, 
     Span s;
     s.lo = max(0, p_lo - a.left);
     s.hi = max(min(lk, p_hi + a.right + 1), 0);
-    // first tokens that reach into the window, or nearly: no tiles of their own
-    if (a.sinks > 0 && s.lo <= max(a.sinks, step)) s.lo = 0;
+    if (s.lo <= a.sinks) s.lo = 0;  // first tokens that reach into the window: no tiles of their own
     s.sink_end = min(min(a.sinks, s.lo), lk);
     s.first = (s.sink_end + step - 1) / step;
     s.tiles = s.first + (max(s.hi - s.lo, 0) + step - 1) / step;

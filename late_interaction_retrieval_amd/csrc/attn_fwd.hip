@@ -154,8 +154,9 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : 2) void attn_fwd_kernel
     Walk<T> next;
     next.start(span, t0, kKeys, ks, vs, a.k.token, a.v.token);
     const auto load = [&](uint8_t* kt, uint8_t* vt) {
-        lk.load(next.k, s.lk - next.j, a.k.token, D, kt, wave);
-        lv.load(next.v, s.lk - next.j, a.v.token, D, vt, wave);
+        const int left = span.end(next.t) - next.j;
+        lk.load(next.k, left, a.k.token, D, kt, wave);
+        lv.load(next.v, left, a.v.token, D, vt, wave);
         next.next(span, kKeys, ks, vs, a.k.token, a.v.token);
     };
     if (t0 < t1) load(k_0, v_0);  // on its way while the queries are read
@@ -264,9 +265,9 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_few_kernel(AttnArgs p
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
         asm volatile("" ::: "memory");
-        const int j = span.at(t, kKeysFew);
-        lk.load(ks + (int64_t)j * a.k.token, s.lk - j, a.k.token, D, kt + wave * BYTES, 0);
-        lv.load(vs + (int64_t)j * a.v.token, s.lk - j, a.v.token, D, vt + wave * BYTES, 0);
+        const int j = span.at(t, kKeysFew), left = span.end(t) - j;
+        lk.load(ks + (int64_t)j * a.k.token, left, a.k.token, D, kt + wave * BYTES, 0);
+        lv.load(vs + (int64_t)j * a.v.token, left, a.v.token, D, vt + wave * BYTES, 0);
     };
     const auto work = [&](int t, const uint8_t* kt, const uint8_t* vt) {
         const int j = span.at(t, kKeysFew), end = span.end(t);

@@ -379,3 +379,26 @@ def test_seeded_random_calls(bd, seed):
         c = case(c["t"]["q"].dtype, nq, nk, c["t"]["q"].shape[1], Hk, c["D"], window, c["sinks"], train=True,
                  Lq=max(nq) + r.choice([0, 2]), Lk=max(nk) + r.choice([0, 70]))
     run(bd, c, where="seed %d" % seed)
+
+
+@pytest.mark.parametrize("G", [1, 4])
+@pytest.mark.parametrize("D,dtype", [(64, F16), (128, BF16)], ids=str)
+@pytest.mark.parametrize("nq,nk,window,sinks", [([1, 1], [700, 40], (30, 0), 4), ([1, 1], [5000, 90], (40, 0), 3), ([5, 150], [300, 400], (20, 3), 2),
+                                                ([40, 200], [400, 230], (9, 0), 0), ([3, 140], [90, 900], (5, 5), 130),
+                                                ([30, 150], [300, 200], (60, 0), 1)], ids=str)
+def test_keys_that_no_query_sees_may_hold_anything(bd, nq, nk, window, sinks, G, D, dtype):
+    """A cache's dropped entries, between the first tokens and the window: NaN there changes no bit, and their
+    gradients are 0."""
+    c = case(dtype, nq, nk, 2 * G, 2, D, window, sinks, packed=True, train=True)
+    want = run(bd, c)
+    hidden = torch.zeros(sum(nk), dtype=torch.bool)
+    for q0, n, k0, m in c["lens"]:
+        hidden[k0:k0 + m] = ~ref.seen(n, m, window, sinks).any(0)
+    assert hidden.any()
+    c["t"]["k"][hidden] = float("nan")
+    c["t"]["v"][hidden] = float("inf")
+    d, how = device_args(c)
+    out, lse = bd.maxsim_attn_fwd(d["q"], d["k"], d["v"], with_lse=True, **how)
+    got = [out, lse] + list(bd.maxsim_attn_bwd(d["g"], d["q"], d["k"], d["v"], out, lse, **how))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.all(got[3][hidden.to(DEV)] == 0) and torch.all(got[4][hidden.to(DEV)] == 0)
