@@ -71,8 +71,8 @@ int maxsim_rope(const maxsim_view* x, const maxsim_view* y, int32_t B, int32_t L
  *   lse       fp32 out, or NULL: log of the sum of exp(S_ij), of row and head n = (b * max_q + i) * Hq + h (packed:
  *             row * Hq + h) at lse[n * lse_step].  lse_step 1, or at least 1 + D/2: then the D values of dtype behind
  *             each hold what rounding left off out, which keeps rowsum(dO * out) of the backward exact
- * Rows of no sequence (past a sequence's length, past the last one) are not read; in outputs they are
- * left as they were, or made 0 where zero_rest is not 0 (of packed rows: those past the last sequence).
+ * Rows of no sequence (past a sequence's length, before the first one, past the last one) are not read; in
+ * outputs they are left as they were, or made 0 where zero_rest is not 0.  B = 0 enqueues nothing.
  * Scores, statistics and sums are fp32; P (and in the backward dS) is rounded to dtype for its product, as
  * the matrix cores take it; each output is rounded once.  Keys that no query of their sequence sees are not read and
  * may hold anything (entries dropped from a cache; their gradients are 0).  A NaN or an infinity elsewhere in a

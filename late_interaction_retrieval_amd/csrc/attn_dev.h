@@ -359,7 +359,7 @@ __device__ __forceinline__ void zero_rows(T* row0, int64_t token, int64_t head, 
     }
 }
 // The rows that belong to no sequence: [len, all) of sequence b, shared out over `parts` workgroups, and of
-// packed rows those past the last sequence, over all `items`.
+// packed rows those before the first sequence and past the last, over all `items`.
 template <typename T>
 __device__ __forceinline__ void zero_rest(const maxsim_view& v, float* lse, int lse_step, const int32_t* cu, int B, int64_t rows, int b,
                                           int64_t row0, int len, int64_t all, int heads, int D, int part, int parts,
@@ -367,8 +367,9 @@ __device__ __forceinline__ void zero_rest(const maxsim_view& v, float* lse, int 
     const int64_t at = cu ? row0 : (int64_t)b * all;  // of lse
     zero_rows<T>(first<T>(v, cu != nullptr, b, row0, 0), v.token, v.head, lse ? lse + at * heads * lse_step : nullptr, lse_step,
                  (int64_t)len + part, all, parts, heads, D);
-    if (cu)
-        zero_rows<T>((T*)v.data, v.token, v.head, lse, lse_step, clamp64(((cint_ptr)cu)[B], 0, rows) + item, rows, items, heads, D);
+    if (!cu) return;
+    zero_rows<T>((T*)v.data, v.token, v.head, lse, lse_step, item, clamp64(((cint_ptr)cu)[0], 0, rows), items, heads, D);
+    zero_rows<T>((T*)v.data, v.token, v.head, lse, lse_step, clamp64(((cint_ptr)cu)[B], 0, rows) + item, rows, items, heads, D);
 }
 
 }  // namespace

@@ -402,3 +402,19 @@ def test_keys_that_no_query_sees_may_hold_anything(bd, nq, nk, window, sinks, G,
     got = [out, lse] + list(bd.maxsim_attn_bwd(d["g"], d["q"], d["k"], d["v"], out, lse, **how))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert torch.all(got[3][hidden.to(DEV)] == 0) and torch.all(got[4][hidden.to(DEV)] == 0)
+
+
+def test_some_of_the_packed_sequences(bd):
+    """A part of the starts with all of the rows: the other sequences' rows are of no sequence, before and behind."""
+    n = [40, 7, 133, 20, 5]
+    c = case(BF16, n, n, 4, 2, 64, (30, 0), 1, packed=True, train=True)
+    want = run(bd, c)
+    d, how = device_args(c)
+    how.update(cu_q=how["cu_q"][1:4].contiguous(), cu_k=how["cu_k"][1:4].contiguous())
+    out, lse = bd.maxsim_attn_fwd(d["q"], d["k"], d["v"], with_lse=True, **how)
+    got = [out, lse] + list(bd.maxsim_attn_bwd(d["g"], d["q"], d["k"], d["v"], out, lse, **how))
+    one = bd.maxsim_attn_fwd(d["q"], d["k"], d["v"], **{**how, "max_q": 7, "max_k": 133,
+                             "cu_q": how["cu_q"][:2].contiguous(), "cu_k": how["cu_k"][:2].contiguous()})[0]
+    for a, b in zip(got, want):
+        assert torch.equal(a[40:180], b[40:180]) and torch.all(a[:40] == 0) and torch.all(a[180:] == 0)
+    assert torch.equal(one[40:47], want[0][40:47]) and torch.all(one[:40] == 0) and torch.all(one[47:] == 0)
