@@ -79,7 +79,7 @@ int maxsim_rope(const maxsim_view* x, const maxsim_view* y, int32_t B, int32_t L
  * sequence reaches all rows that see it and may reach rows near them that do not.  fp16 gradients pass dO (v_j - out),
  * with dO's row scaled to at most 2, through fp16: sure to hold while |v| <= 128, and beyond that where that product does.
  * Requires data 16-byte aligned and steps multiples of 8, token steps of at least D and at most 2^20; D a multiple of 8 from 8 to 128;
- * Hq a multiple of Hk; 0 <= max_q * (Hq / Hk), max_k < 2^29; scale finite and > 0; sinks >= 0; and tiles of
+ * Hq a multiple of Hk; 0 <= max_q * (Hq / Hk), max_k < 2^29; 2^-60 <= scale <= 2^60; sinks >= 0; and tiles of
  * 128 rows, of queries (max_q * (Hq / Hk)) or keys, of which B * Hk times one more than there are stay below 2^21.
  */
 typedef struct {
@@ -122,7 +122,7 @@ int maxsim_attn_bwd(const maxsim_attn* a, const float* lse, const maxsim_view* d
  *            the same of the teacher's entries (of none: 0 and +infinity)
  * A row without entries (or whose entries are all -infinity) gives 0 and no gradient.  Scores of -infinity are
  * columns that are not there (p = 0); one that the teacher's q > 0 asks for gives an infinite loss.
- * Requires N, V >= 0, 0 <= K <= 1024, N < 2^24, V < 2^30, T finite and > 0.
+ * Requires N, V >= 0, 0 <= K <= 1024, N < 2^24, V < 2^30, 2^-60 <= T <= 2^60.
  * The workspace (rows split over workgroups): 16-byte aligned, NULL is fine when 0 bytes are needed.
  */
 size_t maxsim_distill_workspace_bytes(int32_t N, int32_t V);

@@ -438,8 +438,9 @@ void plan_parts(const maxsim_attn& a, AttnArgs& p) {
         const int64_t right = a.right < 0 ? 0 : a.right, stretch = ((int64_t)kRows + a.left + right + 63) / 64 * 64;
         // (a launch of a wave for each of their rows holds fewer than 2^32 threads)
         if (a.max_q > 2 * stretch && (int64_t)a.B * a.Hk * keys < (int64_t)1 << 25) {
-            p.far_tokens = (int)stretch;
-            p.far_chunks = (int)((a.max_q + stretch - 1) / stretch);
+            // (64 chunks at most, which bounds the parts' memory: narrow windows over long sequences)
+            p.far_tokens = (int)std::max<int64_t>(stretch, ((int64_t)a.max_q + 63) / 64);
+            p.far_chunks = (a.max_q + p.far_tokens - 1) / p.far_tokens;
             p.far_tiles = (keys + kRows - 1) / kRows;
         }
     }

@@ -15,6 +15,9 @@ bool is_float(int32_t dt) { return dt == MAXSIM_F16 || dt == MAXSIM_BF16 || dt =
 uintptr_t elem(int32_t dt) { return dt == MAXSIM_F32 ? 4 : 2; }
 int hip_status(hipError_t e) { return e == hipSuccess ? MAXSIM_OK : MAXSIM_ERR_HIP; }
 
+// A factor of scores that leaves their exponents, and its own square, inside fp32.
+bool factor_ok(float f) { return f >= 0x1p-60f && f <= 0x1p60f; }
+
 // Steps whose multiples stay far inside 64 bits.
 bool steps_ok(const maxsim_view& v) {
     const int64_t most = (int64_t)1 << 40;
@@ -30,8 +33,7 @@ int64_t rows_k(const maxsim_attn& a) { return a.cu_k ? a.rows_k : (int64_t)a.B *
 
 // Sizes and the window (what the workspaces go by too).
 int attn_sizes(const maxsim_attn& a) {
-    if (a.B < 0 || a.max_q < 0 || a.max_k < 0 || a.Hq < 1 || a.Hk < 1 || a.Hq % a.Hk != 0 || a.sinks < 0 ||
-        !std::isfinite(a.scale) || !(a.scale > 0.f))
+    if (a.B < 0 || a.max_q < 0 || a.max_k < 0 || a.Hq < 1 || a.Hk < 1 || a.Hq % a.Hk != 0 || a.sinks < 0 || !factor_ok(a.scale))
         return MAXSIM_ERR_SHAPE;
     if (a.D < 8 || a.D > 128 || a.D % 8 != 0 || (a.dtype != MAXSIM_F16 && a.dtype != MAXSIM_BF16)) return MAXSIM_ERR_UNSUPPORTED;
     if (a.lse_step < 1 || (a.lse_step > 1 && a.lse_step < 1 + a.D / 2)) return MAXSIM_ERR_SHAPE;
@@ -140,7 +142,7 @@ int maxsim_attn_bwd(const maxsim_attn* a, const float* lse, const maxsim_view* d
 }
 
 static int distill_sizes(int32_t N, int32_t V, int32_t K, int32_t dtype, float temperature, int64_t ld) {
-    if (N < 0 || V < 0 || K < 0 || !std::isfinite(temperature) || !(temperature > 0.f)) return MAXSIM_ERR_SHAPE;
+    if (N < 0 || V < 0 || K < 0 || !factor_ok(temperature)) return MAXSIM_ERR_SHAPE;
     if (K > 1024 || !is_float(dtype)) return MAXSIM_ERR_UNSUPPORTED;
     if (N >= 1 << 24 || V >= 1 << 30 || ld < V || ld > (int64_t)1 << 31) return MAXSIM_ERR_SHAPE;
     return MAXSIM_OK;

@@ -418,3 +418,9 @@ def test_some_of_the_packed_sequences(bd):
     for a, b in zip(got, want):
         assert torch.equal(a[40:180], b[40:180]) and torch.all(a[:40] == 0) and torch.all(a[180:] == 0)
     assert torch.equal(one[40:47], want[0][40:47]) and torch.all(one[:40] == 0) and torch.all(one[47:] == 0)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+def test_first_tokens_of_a_long_sequence_with_a_narrow_window(bd, dtype):
+    """Far queries in as many parts as there may be, which are longer than the window then."""
+    run(bd, case(dtype, [9001], [9001], 1, 1, 16, (2, 0), 140, train=True))

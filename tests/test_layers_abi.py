@@ -163,3 +163,19 @@ def test_distill_refusals_of_one_direction():
     big = dict(N=4, V=1 << 20, ld=1 << 20)
     assert need > 0 and distill(True, **big) == NULL and distill(True, ws=A, nbytes=need - 1, **big) == WORKSPACE
     assert L.maxsim_distill_workspace_bytes(-1, 5) == 0 and L.maxsim_distill_workspace_bytes(4, 1 << 30) == 0
+
+
+@pytest.mark.parametrize("factor,want", [(1e-30, SHAPE), (1e30, SHAPE), (2.0 ** -60, OK), (2.0 ** 60, OK)])
+def test_factors_of_scores_stay_inside_fp32(factor, want):
+    """A scale or a temperature whose products with scores, or whose square, could pass fp32."""
+    a = attn(B=0, scale=factor)
+    assert L.maxsim_attn_fwd(ctypes.byref(a), None, None, 0, None) == want and bwd(a) == want
+    assert distill(True, N=0, T=factor) == want and distill(False, N=0, T=factor) == want
+
+
+def test_the_backwards_workspace_grows_no_faster_than_the_sequence():
+    """First tokens' gradients of a narrow window are added up from at most 64 parts: 2 x 64 parts of 128 rows in fp32."""
+    small, large = (L.maxsim_attn_bwd_workspace_bytes(ctypes.byref(attn(B=1, max_q=n, max_k=n, left=0, right=0, sinks=256, D=128)))
+                    for n in (1 << 14, 1 << 20))
+    stats = 2 * 2 * 4  # bytes of a row's, two heads
+    assert large - stats * (1 << 20) <= 2 * 2 * 65 * 2 * 128 * 128 * 4 and small > 0
