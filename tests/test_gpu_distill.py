@@ -167,11 +167,7 @@ def test_scores_past_the_last_cache(bd, dtype):
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
 @pytest.mark.parametrize("V,K", [(4095, 70), (4096, 33), (4097, 300)])
 def test_rows_about_as_long_as_a_wave_takes_by_itself(bd, dtype, V, K):
-    z, index, teacher = rand(9, V, seed=20).to(dtype), torch.randint(-2, V + 2, (9, K), dtype=torch.int32,
-                                                                     generator=torch.Generator().manual_seed(21)), rand(9, K, seed=22)
-    dloss = rand(9, seed=23)
-    want = ref.distill(z, index, teacher, 0.7, dloss)
-    loss, stat = bd.maxsim_distill_fwd(z.to(DEV), index.to(DEV), teacher.to(DEV), 0.7)
-    ref.check(loss, want["loss"], "loss")
-    d = bd.maxsim_distill_bwd(dloss.to(DEV), z.to(DEV), stat, index.to(DEV), teacher.to(DEV), 0.7)
-    ref.check(d, want["dscores"], "dscores")
+    z, index, teacher, dloss = make(9, V, K, dtype, seed=20)
+    index[3, ::3] = -2
+    index[4, 1:] = V + 2
+    check(bd, z, index, teacher, dloss, T=0.7)
