@@ -143,33 +143,40 @@ __device__ __forceinline__ Soft soft_of(const T* z, int from, int to, int lane, 
     return s;
 }
 
-// The teacher's softmax over a row's entries: the largest score and the sum, 0 where there are none.
-template <int TPR>
-__device__ __forceinline__ Soft teacher_of(const DistillArgs& p, const int32_t* index, const float* teacher, int lane, float c,
-                                           Soft* part) {
-    Soft s = {-INFINITY, 0.f};
-    for (int k = lane; k < p.K; k += TPR)
-        if ((uint32_t)index[k] < (uint32_t)p.V) s = join(s, {teacher[k], teacher[k] == -INFINITY ? 0.f : 1.f}, c);
-    return join_row<TPR>(s, c, part);
+// One of a row's entries: its column (-1: none), the teacher's score and the row's.
+struct Entry {
+    int col;
+    float teacher, score;
+};
+template <typename T>
+__device__ __forceinline__ Entry entry_of(const DistillArgs& p, int64_t row, int k) {
+    if (k >= p.K) return {-1, 0.f, 0.f};
+    const int v = p.index[row * p.K + k];
+    if ((uint32_t)v >= (uint32_t)p.V) return {-1, 0.f, 0.f};
+    return {v, p.teacher[row * p.K + k], (float)((const T*)p.scores)[row * p.ld + v]};
 }
 
-// A row's loss from its largest score and the logarithm of its sum.
+// A row's loss from its largest score and the logarithm of its sum.  mine: this thread's first entry, which was read before
+// the row was (10393 x 2887 fp32: 39 -> 36 us).
 template <typename T, int TPR>
-__device__ __forceinline__ void finish(const DistillArgs& p, int64_t row, Soft z, int lane, float c, Soft* part, float* parts) {
-    const int32_t* index = p.index + row * p.K;
-    const float* teacher = p.teacher + row * p.K;
-    const T* scores = (const T*)p.scores + row * p.ld;
+__device__ __forceinline__ void finish(const DistillArgs& p, int64_t row, Soft z, Entry mine, int lane, float c, Soft* part,
+                                       float* parts) {
     const float log_sum = __builtin_amdgcn_logf(z.sum) * kLn2, t = p.temperature;
-    const Soft q = teacher_of<TPR>(p, index, teacher, lane, c, part);
+    // the teacher's softmax: the largest score and the sum, 0 where there are no entries
+    Soft q = {-INFINITY, 0.f};
+    for (int k = lane; k < p.K; k += TPR) {
+        const Entry e = k < TPR ? mine : entry_of<T>(p, row, k);
+        if (e.col >= 0) q = join(q, {e.teacher, e.teacher == -INFINITY ? 0.f : 1.f}, c);
+    }
+    q = join_row<TPR>(q, c, part);
     float loss = 0.f;
     if (q.sum != 0.f) {
         const float log_q = __builtin_amdgcn_logf(q.sum) * kLn2, inv = 1.f / t;
         for (int k = lane; k < p.K; k += TPR) {
-            const int v = index[k];
-            if ((uint32_t)v >= (uint32_t)p.V) continue;
-            const float lq = (teacher[k] - q.top) * inv - log_q, w = __builtin_amdgcn_exp2f(lq * kLog2e);
-            const float s = (float)scores[v];
-            const float lp = s == -INFINITY ? -INFINITY : (s - z.top) * inv - log_sum;
+            const Entry e = k < TPR ? mine : entry_of<T>(p, row, k);
+            if (e.col < 0) continue;
+            const float lq = (e.teacher - q.top) * inv - log_q, w = __builtin_amdgcn_exp2f(lq * kLog2e);
+            const float lp = e.score == -INFINITY ? -INFINITY : (e.score - z.top) * inv - log_sum;
             if (w != 0.f) loss += w * (lq - lp);
         }
     }
@@ -190,8 +197,9 @@ __global__ __launch_bounds__(kThreads) void distill_fwd_kernel(DistillArgs p) {
     const float c = kLog2e / p.temperature;
     const int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
     if (row >= p.N) return;  // whole waves, and whole workgroups where they meet
+    const Entry mine = entry_of<T>(p, row, lane);
     const Soft z = join_row<TPR>(soft_of<T, TPR>((const T*)p.scores + row * p.ld, 0, p.V, lane, c), c, part);
-    finish<T, TPR>(p, row, z, lane, c, part, parts);
+    finish<T, TPR>(p, row, z, mine, lane, c, part, parts);
 }
 
 // Split rows: a part of a row to a workgroup, and the rest of the work when all are there.
@@ -214,10 +222,11 @@ __global__ __launch_bounds__(64) void distill_finish_kernel(DistillArgs p, int s
     const int64_t row = blockIdx.x;
     const int lane = threadIdx.x;
     const float c = kLog2e / p.temperature;
+    const Entry mine = entry_of<typename TT::type>(p, row, lane);
     Soft z = {-INFINITY, 0.f};
     for (int i = lane; i < splits; i += 64)
         z = join(z, {p.partial[2 * (row * splits + i)], p.partial[2 * (row * splits + i) + 1]}, c);
-    finish<typename TT::type, 64>(p, row, join64(z, c), lane, c, nullptr, nullptr);
+    finish<typename TT::type, 64>(p, row, join64(z, c), mine, lane, c, nullptr, nullptr);
 }
 
 // dz over columns [from, to) of a row by TPR threads, and the entries among them.  The first columns are on their way
