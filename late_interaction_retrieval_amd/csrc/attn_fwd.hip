@@ -434,7 +434,9 @@ int64_t rows_in_memory(const maxsim_attn& a) { return a.cu_q ? a.rows_q : (int64
 //     a next token, 16 / 2 heads of 128:  500 keys 10.4 whole, 11.6 in parts; 852 13.1, 11.7; 8192 65.9, 13.6; 32768 250, 19
 //     512 tokens, 16 / 4 heads of 64:     768 keys 15.5 whole, 20.2 in parts; 1536 26.0, 23.8; 8192 117, 46
 // As many workgroups as there are CUs (4 x next token, 32 / 8 heads, 8192 keys: 28.7, twice as many 33.1).  Twice as
-// many for long keys of up to 64 columns (512 tokens as above, 32768 keys: 130 and 103), and for a next token over long caches of
+// many for long keys where that makes no more than 8 parts, which one kind of join takes (16 / 4 heads of 128, 512 tokens,
+// 32768 keys: 203 and 167, 8192: 66 and 63; 2 x 493 tokens, 12 / 6 heads, 12770 keys: 150 and 111; but 8 x 64 tokens, 8 / 2 heads, 8192
+// keys, 16 parts: 41 and 62; 1024 tokens, 2048 keys: 53 and 59), and for a next token over long caches of
 // lengths that differ (16 x 8192 to 32768 keys, 32 / 8 heads of 128: 292 and 274; of one length 367 and 370).
 Plan plan_of(const maxsim_attn& a) {
     Plan p;
@@ -448,7 +450,7 @@ Plan plan_of(const maxsim_attn& a) {
         keys = std::min<int64_t>(keys, (int64_t)a.left + a.right + std::min<int64_t>(rows, kRows) / group + 2 + a.sinks);
     const int64_t from = p.few ? 640 : 1024, least = p.few && keys < 4096 ? 128 : 256;  // keys to be split; of a part
     const bool ragged = a.k_lens || a.cu_k;
-    const int64_t wanted = keys >= 8192 && (p.few ? ragged : a.D <= 64) ? 512 : 256;
+    const int64_t wanted = keys >= 8192 && (p.few ? ragged : 512 <= 8 * base) ? 512 : 256;
     p.splits = 1;
     if (base > 0 && keys >= from) p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({wanted / base, keys / least, kMostSplits}));
     p.blocks = blocks_for((int64_t)a.Hk * a.B, (int64_t)p.tiles * p.splits);
