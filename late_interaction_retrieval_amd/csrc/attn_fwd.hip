@@ -355,21 +355,23 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_few_kernel(AttnArgs p
 
 // Rows whose keys were split: their parts, joined in order.  GROUPS groups of 32 threads to a row (of one head), each thread 4
 // columns of every GROUPS-th part, all of them on their way at once; the parts' references and sums are a lane's each.
-// (One thread after the other over the parts took 30 us for 64; 8 groups for two parts of 8192 rows 35 us.)
+// (One thread after the other over the parts took 30 us for 64; 8 groups 35 us for two parts of 8192 rows and 28 for 16 of 4096, where
+// two groups take 8.4 for 16 of 2048.)
 constexpr int kMostSplits = 64;
 template <typename TT, int GROUPS>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p, int row_groups) {
     typedef typename TT::type T;
-    constexpr int ROWS = 8 / GROUPS, EACH = GROUPS == 1 ? 8 : kMostSplits / GROUPS;
+    constexpr int ROWS = 8 / GROUPS, EACH = 8;
+    static_assert(EACH * 8 == kMostSplits, "8 groups take all parts");
     __shared__ float factor[ROWS][kMostSplits];
-    __shared__ __align__(16) f32x4 share[GROUPS == 1 ? 1 : GROUPS][32];
+    __shared__ __align__(16) f32x4 share[ROWS][GROUPS][32];
     const maxsim_attn& a = p.a;
     const int b = blockIdx.x / row_groups, g = blockIdx.x % row_groups;
     const Seq s = sequence(a, b);
     if (a.zero_rest)
         zero_rest<T>(a.out, p.lse, a.lse_step, a.cu_q, a.B, a.rows_q, b, s.q0, s.lq, s.all_q, a.Hq, a.D, g, row_groups,
                      (int)blockIdx.x, (int)gridDim.x);
-    const int lane = threadIdx.x & 31, group = GROUPS == 1 ? 0 : threadIdx.x >> 5, sub = GROUPS == 1 ? threadIdx.x >> 5 : 0;
+    const int lane = threadIdx.x & 31, group = (threadIdx.x >> 5) % GROUPS, sub = (threadIdx.x >> 5) / GROUPS;
     const int r = min(g * ROWS + sub, s.lq * a.Hq - 1), d = lane * 4;
     if (g * ROWS >= s.lq * a.Hq) return;
     const bool mine = g * ROWS + sub < s.lq * a.Hq && d < a.D;
@@ -383,7 +385,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p, int row_grou
         part[n] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (i < p.splits && mine) part[n] = *reinterpret_cast<const f32x4*>(o + i * step * a.D);
     }
-    // every wave makes its rows' factors for itself: of one row with 64 parts, or of two with 32
+    // every wave makes its rows' factors for itself: of one row with up to 64 parts, or of two with up to 8
     constexpr int WIDE = GROUPS == 1 ? 32 : 64;
     const int i = threadIdx.x & (WIDE - 1);
     float top = -INFINITY, l = 0.f;
@@ -398,7 +400,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p, int row_grou
     float total = l * f;
 #pragma unroll
     for (int x = 1; x < WIDE; x <<= 1) total += __shfl_xor(total, x);
-    if (GROUPS == 1 || threadIdx.x < 64) factor[sub][i] = f;
+    if (GROUPS <= 2 || threadIdx.x < 64) factor[sub][i] = f;
     __syncthreads();
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -407,11 +409,11 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p, int row_grou
         if (k < p.splits && factor[sub][k] != 0.f) sum += part[n] * factor[sub][k];  // (a part of no keys holds nothing)
     }
     if constexpr (GROUPS > 1) {
-        share[group][lane] = sum;
+        share[sub][group][lane] = sum;
         __syncthreads();
         if (group > 0) return;
 #pragma unroll
-        for (int k = 1; k < GROUPS; ++k) sum += share[k][lane];
+        for (int k = 1; k < GROUPS; ++k) sum += share[sub][k][lane];
     }
     if (mine) {
         sum *= is_zero(total) ? 0.f : 1.f / total;
@@ -498,10 +500,11 @@ hipError_t launch_attn_fwd(const maxsim_attn& a, float* lse, void* workspace, hi
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || plan.splits == 1) return e;
     // the rows are few, or the parts are
-    const bool many = plan.splits > 8;
-    const int groups = many ? a.max_q * a.Hq : (a.max_q * a.Hq + 7) / 8;
-    const auto join = half ? (many ? attn_join_kernel<F16, 8> : attn_join_kernel<F16, 1>)
-                           : (many ? attn_join_kernel<BF16, 8> : attn_join_kernel<BF16, 1>);
+    const int each = plan.splits <= 8 ? 8 : plan.splits <= 16 ? 4 : 1;  // rows of a workgroup
+    const int groups = (a.max_q * a.Hq + each - 1) / each;
+    const auto join = each == 8   ? (half ? attn_join_kernel<F16, 1> : attn_join_kernel<BF16, 1>)
+                      : each == 4 ? (half ? attn_join_kernel<F16, 2> : attn_join_kernel<BF16, 2>)
+                                  : (half ? attn_join_kernel<F16, 8> : attn_join_kernel<BF16, 8>);
     join<<<(unsigned)groups * a.B, 256, 0, stream>>>(p, groups);
     return hipGetLastError();
 }

@@ -424,3 +424,14 @@ def test_some_of_the_packed_sequences(bd):
 def test_first_tokens_of_a_long_sequence_with_a_narrow_window(bd, dtype):
     """Far queries in as many parts as there may be, which are longer than the window then."""
     run(bd, case(dtype, [9001], [9001], 1, 1, 16, (2, 0), 140, train=True))
+
+
+@pytest.mark.parametrize("D,dtype,Lk,parts", [(64, F16, 4100, 16), (128, BF16, 4100, 16), (96, BF16, 2400, 9), (64, BF16, 2100, 8)], ids=str)
+def test_keys_in_eight_to_sixteen_parts(bd, D, dtype, Lk, parts):
+    """The join's other forms: four rows to a workgroup, and eight."""
+    nq, nk = [64, 33, 0, 1], [Lk, 700, 300, 2000]
+    c = case(dtype, nq, nk, 8, 2, D, (-1, 0), 0)
+    d, how = device_args(c)
+    a = bd._attn(d["q"], d["k"], d["v"], None, None, how["window"], 0, how["q_lens"], how["k_lens"], None, None, None, None)
+    assert bd.lib().maxsim_attn_fwd_workspace_bytes(bd.ctypes.byref(a)) == parts * 4 * 64 * 8 * (D + 2) * 4
+    run(bd, c)
