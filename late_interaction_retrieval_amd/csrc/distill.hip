@@ -10,8 +10,8 @@
 // workgroups.  Differences z - max are formed before they are multiplied by 1 / T, and the backward gets
 // the maximum and the sum's logarithm apart, so that large scores at a low temperature lose nothing.
 //
-// Measured, the kernels alone: 8192 x 32768 bf16 forward 125 - 128 us (537 MB at 4.2 TB/s), backward 209 - 213 (1.07 GB at
-// 5.1); 32 x 200003 fp32 forward 7.4 + 5.0 (the parts' join), backward 12.3; 64 x 64 4.8 and 5.4, a launch each.
+// Measured, the kernels alone: 8192 x 32768 bf16 forward 122 - 131 us (537 MB at 4.1 - 4.4 TB/s), backward 207 - 215 (1.07 GB at
+// 5.0 - 5.2); 10393 x 2887 fp32 36 and 48; 32 x 200003 fp32 forward 7.4 + 4.6 (the parts' join), backward 12.3; 64 x 64 4.8 and 5.4, a launch each.
 #include <algorithm>
 
 #include "encoder_dev.h"
