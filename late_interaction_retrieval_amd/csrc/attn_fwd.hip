@@ -454,7 +454,8 @@ Plan plan_of(const maxsim_attn& a) {
     const bool ragged = a.k_lens || a.cu_k;
     const int64_t wanted = keys >= 8192 && (p.few ? ragged : 512 <= 8 * base) ? 512 : 256;
     p.splits = 1;
-    if (base > 0 && keys >= from) p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({wanted / base, keys / least, kMostSplits}));
+    // (of no rows, those of no sequence are still to be made 0, by the one kernel: the join has nothing to join)
+    if (base > 0 && rows > 0 && keys >= from) p.splits = (int)std::max<int64_t>(1, std::min<int64_t>({wanted / base, keys / least, kMostSplits}));
     p.blocks = blocks_for((int64_t)a.Hk * a.B, (int64_t)p.tiles * p.splits);
     return p;
 }
