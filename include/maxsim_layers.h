@@ -75,8 +75,9 @@ int maxsim_rope(const maxsim_view* x, const maxsim_view* y, int32_t B, int32_t L
  * outputs they are left as they were, or made 0 where zero_rest is not 0.  B = 0 enqueues nothing.
  * Scores, statistics and sums are fp32; P (and in the backward dS) is rounded to dtype for its product, as
  * the matrix cores take it; each output is rounded once.  Keys that no query of their sequence sees are not read and
- * may hold anything (entries dropped from a cache; their gradients are 0).  A NaN or an infinity elsewhere in a
- * sequence reaches all rows that see it and may reach rows near them that do not.  fp16 gradients pass dO (v_j - out),
+ * may hold anything (entries dropped from a cache; their gradients are 0).  A NaN elsewhere in a
+ * sequence reaches all rows that see it and may reach rows near them that do not; so does an infinity, but for a score of
+ * -infinity, whose weight is 0 (a query with no other score counts as one that sees no key).  fp16 gradients pass dO (v_j - out),
  * with dO's row scaled to at most 2, through fp16: sure to hold while |v| <= 128, and beyond that where that product does.
  * Requires data 16-byte aligned and steps multiples of 8, token steps of at least D and at most 2^20; D a multiple of 8 from 8 to 128;
  * Hq a multiple of Hk; 0 <= max_q * (Hq / Hk), max_k < 2^29; 2^-60 <= scale <= 2^60; sinks >= 0; and tiles of

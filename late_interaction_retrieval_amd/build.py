@@ -30,12 +30,11 @@ HIPCC_FLAGS = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-Wno-unused-command-line-argument",
 ]
-# inputs are finite: max needs no NaN canonicalisation (infinities are kept).  Attention's files, which take these
-# flags too, test sums of exponentials by their bits, so that a NaN there still reaches the output.
+# inputs are finite: max needs no NaN canonicalisation (infinities are kept)
 FINITE_FLAGS = ["-fno-honor-nans"]
 # these pass NaN and infinity through as their formulas give them, or refuse them
 SOURCE_FLAGS = {s: [] for s in ("rmsnorm.hip", "quant.hip", "gemm_fp8.hip", "adamw.hip", "capi_encoder.cpp",
-                                   "rope.hip", "distill.hip", "capi_layers.cpp")}
+                                   "rope.hip", "attn_fwd.hip", "attn_bwd.hip", "distill.hip", "capi_layers.cpp")}
 
 
 def hipcc():

@@ -55,16 +55,19 @@ __device__ __forceinline__ f32x16 zero16() {
 // The row of D in register i, without the lane's 4 * (l / 32).
 __device__ __forceinline__ constexpr int slot(int i) { return 8 * (i >> 2) + (i & 3); }
 
+// The larger one; NaN if either is (fmaxf would drop it, and costs an instruction more for each value whose NaN may be of
+// the signalling kind).
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 __device__ __forceinline__ float swap_max(float v) {
     const auto r = __builtin_amdgcn_permlane32_swap(fbits(v), fbits(v), false, false);
-    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+    return larger(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 __device__ __forceinline__ float swap_sum(float v) {
     const auto r = __builtin_amdgcn_permlane32_swap(fbits(v), fbits(v), false, false);
     return __uint_as_float(r[0]) + __uint_as_float(r[1]);
 }
 
-// Whether a sum of exponentials is 0: no key was seen.  By its bits, since a NaN is none.
+// Whether a sum of exponentials is 0: no key was seen.
 __device__ __forceinline__ bool is_zero(float v) { return (fbits(v) << 1) == 0; }
 
 // One sequence: its rows' places, lengths, and how far queries' positions are shifted.

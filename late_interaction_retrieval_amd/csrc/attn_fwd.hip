@@ -86,10 +86,10 @@ struct Rows {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) m = fmaxf(m, s[nb][i]);
+            for (int i = 0; i < 16; ++i) m = larger(m, s[nb][i]);
         m = swap_max(m);
-        if (__any(m > ref + slack)) {  // -infinity + slack is -infinity
-            const float now = fmaxf(ref, m);
+        if (__any(!(m <= ref + slack))) {  // -infinity + slack is -infinity; a NaN becomes the reference, and with it the row
+            const float now = larger(ref, m);
             const float f = ref == now ? 1.f : __builtin_amdgcn_exp2f((ref - now) * c);
             ref = now;
             sum *= f;
@@ -303,7 +303,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_few_kernel(AttnArgs p
     __syncthreads();  // all tiles are read: their memory takes the parts
     float most = -INFINITY, total = 0.f;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) most = fmaxf(most, joined[i][lane & 31][0]);
+    for (int i = 0; i < kWaves; ++i) most = larger(most, joined[i][lane & 31][0]);
     const float f = top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(top - most);
 #pragma unroll
     for (int i = 0; i < kWaves; ++i)
@@ -395,9 +395,9 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p, int row_grou
     }
     float most = top;
 #pragma unroll
-    for (int x = 1; x < WIDE; x <<= 1) most = fmaxf(most, __shfl_xor(most, x));
-    const float f = is_zero(l) ? 0.f : __builtin_amdgcn_exp2f(top - most);
-    float total = l * f;
+    for (int x = 1; x < WIDE; x <<= 1) most = larger(most, __shfl_xor(most, x));
+    const float f = is_zero(l) ? -1.f : __builtin_amdgcn_exp2f(top - most);  // -1: a part in which the row sees nothing
+    float total = is_zero(l) ? 0.f : l * f;
 #pragma unroll
     for (int x = 1; x < WIDE; x <<= 1) total += __shfl_xor(total, x);
     if (GROUPS <= 2 || threadIdx.x < 64) factor[sub][i] = f;
@@ -406,7 +406,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs p, int row_grou
 #pragma unroll
     for (int n = 0; n < EACH; ++n) {
         const int k = group + GROUPS * n;
-        if (k < p.splits && factor[sub][k] != 0.f) sum += part[n] * factor[sub][k];  // (a part of no keys holds nothing)
+        // (a factor that fell to 0 counts, as its product with a value that is not finite does; NaN too)
+        if (k < p.splits && !(factor[sub][k] < 0.f)) sum += part[n] * factor[sub][k];
     }
     if constexpr (GROUPS > 1) {
         share[sub][group][lane] = sum;

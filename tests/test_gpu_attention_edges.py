@@ -38,3 +38,75 @@ def test_no_queries_over_long_keys(bd, Lk, packed, general):
     dq, dk, dv = bd.maxsim_attn_bwd(torch.ones_like(q), q, k, v, out, lse, **how)
     for t, like in ((dq, q), (dk, k), (dv, v)):
         assert t.shape == like.shape and torch.all(t == 0)
+
+
+# (queries, keys) of two sequences, query heads to a key head: few rows whole and in parts, many rows whole and in parts
+FORMS = [([3, 2], [60, 9], 2), ([1, 1], [3000, 700], 4), ([90, 40], [90, 300], 2), ([150, 9], [4100, 3000], 2)]
+
+
+@pytest.mark.parametrize("D,dtype", [(64, F16), (128, BF16)], ids=str)
+@pytest.mark.parametrize("nq,nk,G", FORMS, ids=str)
+@pytest.mark.parametrize("where", ["q", "k", "v", "k inf", "g"])
+def test_a_nan_reaches_the_rows_that_see_it(bd, where, nq, nk, G, D, dtype):
+    """One NaN in the last query's row, in a key, in a value, in dO, or an infinite key: out, lse and gradients of the rows
+    that see it are NaN, and the other sequence's stay as they were, bit for bit."""
+    B, Lq, Lk, H = 2, max(nq), max(nk), 2 * G
+    t = {"q": rand(B, Lq, H, D, dtype=dtype, seed=1), "k": rand(B, Lk, 2, D, dtype=dtype, seed=2),
+         "v": rand(B, Lk, 2, D, dtype=dtype, seed=3), "g": rand(B, Lq, H, D, dtype=dtype, seed=4)}
+    ints = lambda n: torch.tensor(n, dtype=torch.int32, device=DEV)  # noqa: E731
+    how = dict(window=(-1, 0), q_lens=ints(nq), k_lens=ints(nk))
+
+    def call():
+        out, lse = bd.maxsim_attn_fwd(t["q"], t["k"], t["v"], with_lse=True, **how)
+        return [out, lse, *bd.maxsim_attn_bwd(t["g"], t["q"], t["k"], t["v"], out, lse, **how)]
+
+    clean = call()
+    name = where[0]
+    at = nq[0] - 1 if name in "qg" else nk[0] - nq[0]  # the key where the first query stands: all see it
+    t[name][0, at, 1 if name in "kv" else G, 5] = INF if where == "k inf" else NAN  # heads G .. 2 G - 1 share key head 1
+    out, lse, dq, dk, dv = got = call()
+    for a, b in zip(got, clean):
+        assert torch.equal(a[1], b[1])
+        assert torch.equal(a[0, :, :G] if a.shape[2] == H else a[0, :, :1], b[0, :, :G] if b.shape[2] == H else b[0, :, :1])
+    rows, heads = (slice(at, at + 1), slice(G, G + 1)) if name in "qg" else (slice(0, nq[0]), slice(G, H))
+    none = lambda x: bool(torch.isnan(x).all())  # noqa: E731
+    if name == "g":
+        assert torch.equal(out, clean[0]) and torch.equal(lse, clean[1])
+        assert none(dq[0, at, G]) and none(dk[0, :nk[0], 1]) and none(dv[0, :nk[0], 1, 5])
+        return
+    if where == "k inf":  # scores of +infinity: NaN; of -infinity: a weight of 0
+        up = torch.zeros(B, Lq, H, dtype=torch.bool, device=DEV)
+        up[0, :nq[0], G:] = t["q"][0, :nq[0], G:, 5] > 0
+        assert none(out[up]) and none(lse[up]) and none(dq[up])
+        # of -infinity: the other keys' weights; a query that sees no other key (the first, at the infinite one) as one that sees none
+        down = ~up[0, :nq[0], G:]
+        alone = down & (torch.arange(nq[0], device=DEV) + at == 0)[:, None]
+        l, o = lse[0, :nq[0], G:], out[0, :nq[0], G:]
+        assert torch.all(l[alone] == -INF) and torch.all(o[alone] == 0)
+        assert torch.isfinite(l[down & ~alone]).all() and torch.isfinite(o[down]).all()
+        return
+    if name == "v":
+        assert none(out[0, rows, heads, 5]) and torch.isfinite(out[0, rows, heads, :5]).all() and torch.equal(lse, clean[1])
+        assert none(dq[0, rows, heads]) and none(dk[0, at, 1]) and torch.equal(dv, clean[4])
+    else:
+        assert none(out[0, rows, heads]) and none(lse[0, rows, heads]) and none(dq[0, rows, heads])
+        assert none(dk[0, at, 1]) and none(dv[0, at, 1])
+
+
+@pytest.mark.parametrize("nq,Lk", [(1, 3000), (150, 4100)])
+def test_a_nan_behind_a_weight_of_zero(bd, nq, Lk):
+    """A value that is not finite times a weight that fell to 0 is NaN, in the parts' join too."""
+    q, k, v = rand(1, nq, 2, 64), rand(1, Lk, 1, 64, seed=2), rand(1, Lk, 1, 64, seed=3)
+    q[:], k[:], k[0, :400] = 1.0, 1.0, -100.0  # scores 8, and -800 through more than the first part
+    v[0, 7, 0, 9] = NAN
+    out, lse = bd.maxsim_attn_fwd(q, k, v, with_lse=True)
+    assert torch.isnan(out[..., 9]).all() and torch.isfinite(out[..., :9]).all() and torch.isfinite(lse).all()
+
+
+def test_a_query_that_is_not_a_number_over_a_long_cache(bd):
+    """Every score of the row is NaN, in every part."""
+    q, k, v = rand(2, 1, 4, 64), rand(2, 9000, 1, 64, seed=2), rand(2, 9000, 1, 64, seed=3)
+    q[0, 0, 2] = NAN
+    out, lse = bd.maxsim_attn_fwd(q, k, v, with_lse=True)
+    assert torch.isnan(out[0, 0, 2]).all() and torch.isnan(lse[0, 0, 2])
+    assert torch.isfinite(out[1]).all() and torch.isfinite(out[0, 0, [0, 1, 3]]).all()
