@@ -32,13 +32,34 @@ constexpr bool is_f16() {
     return std::is_same<T, _Float16>::value;
 }
 // fp16 holds P and dS for their products only if they are brought into its range by powers of 2, which are
-// exact: P (at most 1, 1 / keys where attention is flat) times 2^8; dS by the size of its row's dO.
+// exact: P (at most 1, 1 / keys where attention is flat) times 2^8; dS by the size of its row's dO in dQ, and in dK by the
+// largest dS that the key has met so far.
 constexpr float kLiftP = 8.f;  // log2
 // The power of 2 that brings a row of dO with the largest magnitude `top` into [1, 2); 1 for a row of zeros.
 __device__ __forceinline__ float lift_of(float top) {
     const int e = (int)((fbits(top) >> 23) & 255u);
     return e == 0 || e == 255 ? 1.f : __uint_as_float((uint32_t)(254 - e) << 23);
 }
+// The factor of dS (fp16) of one row of the result, which the sum at hand holds too: it brought the largest magnitude at the time
+// it was set to [2^7, 2^8), and stays until one passes 2^15.  So a value is held to fp16's half step or to 2^-32 of the
+// largest one of the same sum, whichever is more, whatever the rows' dO, v and P are.
+struct Lift {
+    uint32_t bits;  // of the factor, a power of 2
+    __device__ __forceinline__ void start() { bits = 221u << 23; }  // 2^94: nothing met yet
+    __device__ __forceinline__ float factor() const { return __uint_as_float(bits); }
+    __device__ __forceinline__ float inverse() const { return __uint_as_float((254u << 23) - bits); }
+    // Takes in a block's largest magnitude; true where some lane's sums are to be multiplied by 2^shift first.
+    __device__ __forceinline__ bool take(float m, int& shift) {
+        const bool past = m > __uint_as_float((269u << 23) - bits);  // 2^15 / factor
+        shift = 0;
+        if (!__any(past)) return false;
+        const int e = min(max((int)(fbits(m) >> 23), 40), 246);
+        const uint32_t now = past ? (uint32_t)(261 - e) << 23 : bits;
+        shift = (int)(now - bits) >> 23;
+        bits = now;
+        return true;
+    }
+};
 
 // The first token past the window of all of a key tile's keys.
 __device__ __forceinline__ int far_from(const maxsim_attn& a, const Seq& s, int j0) {
@@ -121,7 +142,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
         float* stat = p.row_stat + (int64_t)head * p.rows + at;
         stat[0] = is_f16<T>() ? lse - kLiftP : lse;
         stat[p.rows * a.Hq] = delta;
-        if (is_f16<T>()) stat[2 * p.rows * a.Hq] = top;
     }
     const float lift = is_f16<T>() ? lift_of(top) : 1.f;
     const Place place = place_of<DP>(lane);
@@ -188,7 +208,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 3 : WAVES) void attn_dkv_ke
     typedef typename Vec8<T>::V V8;
     constexpr int TR = DP == 128 && WAVES == 2 ? 32 : 64;
     constexpr bool K_IN_LDS = DP == 128 && WAVES == 2;
-    constexpr int KS = DP / 16, DB = DP / 32, BYTES = TR * Tile<DP>::ROW, STATS = is_f16<T>() ? 3 : 2;
+    constexpr int KS = DP / 16, DB = DP / 32, BYTES = TR * Tile<DP>::ROW, STATS = 2;
     __shared__ __align__(16) uint8_t q_0[BYTES], g_0[BYTES], q_1[BYTES], g_1[BYTES];
     __shared__ __align__(16) float stat_0[STATS * 64], stat_1[STATS * 64];
     __shared__ __align__(16) uint8_t k_lds[K_IN_LDS ? kWaves * KS * 1024 : 16];  // 64 lanes x 16 bytes for each step
@@ -284,28 +304,14 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 3 : WAVES) void attn_dkv_ke
     f32x16 dk[DB], dv[DB];
 #pragma unroll
     for (int db = 0; db < DB; ++db) dk[db] = dv[db] = zero16();
-    float lift = 0.f;  // of what dk holds (fp16): the smallest of the rows' so far; 0: nothing yet
+    Lift lift;  // of what dk holds (fp16)
+    lift.start();
 
     int i_now = i_lo;  // the token that the tile at hand starts with
     const auto work = [&](const uint8_t* qt, const uint8_t* gt, const float* stat) {
         const int at = i_now;
         i_now = i_now + TR >= i_hi ? i_lo : i_now + TR;
         if (wj >= s.lk) return;
-        float f = 1.f;
-        if constexpr (is_f16<T>()) {
-            // rows in the scale of the largest dO seen so far, what is there already brought to it
-            const uint32_t top = max64(fbits(stat[128 + lane]));
-            const float now = lift_of(__uint_as_float(top));
-            if (top != 0 && (lift == 0.f || now < lift)) {
-                const float down = lift == 0.f ? 1.f : now / lift;
-#pragma unroll
-                for (int db = 0; db < DB; ++db)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) dk[db][i] *= down;
-                lift = now;
-            }
-            f = (lift == 0.f ? 1.f : lift) * (1.f / 256.f);  // P is lifted by 2^8
-        }
 #pragma unroll
         for (int nb = 0; nb < TR / 32; ++nb) {
             const int ib = at + 32 * nb;
@@ -349,7 +355,21 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 3 : WAVES) void attn_dkv_ke
             for (int q = 0; q < 4; ++q) {
                 const f32x4 d = *reinterpret_cast<const f32x4*>(stat + 64 + 32 * nb + 8 * q + 4 * (lane >> 5));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[4 * q + i] *= is_f16<T>() ? (dp[4 * q + i] - d[i]) * f : dp[4 * q + i] - d[i];
+                for (int i = 0; i < 4; ++i) x[4 * q + i] *= dp[4 * q + i] - d[i];
+            }
+            if constexpr (is_f16<T>()) {
+                float m = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) m = larger(m, __builtin_fabsf(x[i]));
+                int shift;
+                if (lift.take(swap_max(m), shift)) {
+#pragma unroll
+                    for (int db = 0; db < DB; ++db)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) dk[db][i] = __builtin_ldexpf(dk[db][i], shift);
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) x[i] *= lift.factor();
             }
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -368,7 +388,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 3 : WAVES) void attn_dkv_ke
         if (t + 2 < total) load(q_0, g_0, stat_0);
         work(q_1, g_1, stat_1);
     }
-    const float kf = is_f16<T>() && lift != 0.f ? a.scale / lift : a.scale, vf = is_f16<T>() ? 1.f / 256.f : 1.f;
+    const float vf = is_f16<T>() ? 1.f / 256.f : 1.f, kf = is_f16<T>() ? a.scale * (lift.inverse() * vf) : a.scale;  // P is lifted by 2^8
     const bool part = p.head_splits > 1 || (apart && j < a.sinks);
     if (!far && p.head_splits == 1) {
         T* dkr = first<T>(p.dk, packed, b, s.k0, h) + (int64_t)j * p.dk.token;
@@ -477,7 +497,7 @@ hipError_t launch(const AttnArgs& p, hipStream_t stream) {
 
 int64_t rows_in_memory(const maxsim_attn& a) { return a.cu_q ? a.rows_q : (int64_t)a.B * a.max_q; }
 int64_t stat_floats(const maxsim_attn& a) {  // the parts after them start at a multiple of 16 bytes
-    return ((a.dtype == MAXSIM_F16 ? 3 : 2) * rows_in_memory(a) * a.Hq + 3) / 4 * 4;
+    return (2 * rows_in_memory(a) * a.Hq + 3) / 4 * 4;
 }
 
 }  // namespace

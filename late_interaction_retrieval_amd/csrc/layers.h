@@ -32,8 +32,7 @@ struct AttnArgs {
     float* part_o;   // [splits][rows][Hq][D]
     float* part_ml;  // [splits][rows][Hq][2]
     int64_t rows;    // of q in memory
-    float* row_stat; // backward: [2][Hq][rows]: lse in powers of 2 (+infinity where it is -infinity), rowsum(dO * out);
-                     // fp16: a third, the rows' largest |dO|
+    float* row_stat; // backward: [2][Hq][rows]: lse in powers of 2 (+infinity where it is -infinity), rowsum(dO * out)
     // Backward, dK and dV.  Queries past the window see the first tokens' keys alone: of the first far_tiles key tiles they
     // are worked on apart, far_tokens at a time.  Where key tiles are few, the query heads of a key head are shared out too,
     // over head_splits workgroups.  What more than one workgroup adds to goes through parts:

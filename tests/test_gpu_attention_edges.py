@@ -2,6 +2,8 @@
 import pytest
 import torch
 
+import layers_ref as ref
+
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 F16, BF16 = torch.float16, torch.bfloat16
@@ -110,3 +112,51 @@ def test_a_query_that_is_not_a_number_over_a_long_cache(bd):
     out, lse = bd.maxsim_attn_fwd(q, k, v, with_lse=True)
     assert torch.isnan(out[0, 0, 2]).all() and torch.isnan(lse[0, 0, 2])
     assert torch.isfinite(out[1]).all() and torch.isfinite(out[0, 0, [0, 1, 3]]).all()
+
+
+def fp16_gradients(bd, t, window, scale, where, lens=None):
+    """dQ, dK and dV of fp16 rows on the host, one sequence [L, H, D], within the 64-bit form's bounds, where what falls below fp16's
+    values does so on the scale of a key's (or a row's) own largest dS: 2^-32 of it (2^-31, for the rounding of that largest)."""
+    q, k, v, g = (t[n] for n in "qkvg")
+    L, Hq, D = q.shape
+    Hk, Lk = k.shape[1], k.shape[0]
+    G = Hq // Hk
+    want = ref.attention(q, k, v, [(0, L, 0, Lk)], scale, window, 0, g)
+    vis = ref.seen(L, Lk, window, 0)
+    dq, dk = want["dq"][1], want["dk"][1]
+    for h in range(Hk):
+        most, less = torch.zeros(Lk, dtype=torch.float64), torch.zeros(Lk, D, dtype=torch.float64)
+        seen_q = torch.zeros(Lk, D, dtype=torch.float64)
+        for j in range(h * G, (h + 1) * G):
+            qd, kd, vd, gd = q[:, j].double(), k[:, h].double(), v[:, h].double(), g[:, j].double()
+            p = torch.softmax((scale * qd @ kd.t()).masked_fill(~vis, -INF), 1)
+            dp = gd @ vd.t()
+            ds = p * (dp - (p * dp).sum(1, keepdim=True))
+            top = gd.abs().amax(1, keepdim=True)
+            low = vis.double() * 2.0 ** -25
+            # the reference's terms of fp16's smallest values, in the scale of the rows' dO, give way to these
+            dq[:, j] += scale * (2.0 ** -31 * ds.abs().amax(1, keepdim=True) * vis.double() - low * top) @ kd.abs()
+            less += scale * (low * top.max()).t() @ qd.abs()
+            most = torch.maximum(most, ds.abs().amax(0))
+            seen_q += vis.double().t() @ qd.abs()
+        dk[:, h] += scale * 2.0 ** -31 * most[:, None] * seen_q - less
+    d = {n: x[None].to(DEV) for n, x in t.items()}
+    out, lse = bd.maxsim_attn_fwd(d["q"], d["k"], d["v"], scale=scale, window=window, with_lse=True)
+    ref.check(out, want["out"], where + " out")
+    got = bd.maxsim_attn_bwd(d["g"], d["q"], d["k"], d["v"], out, lse, scale=scale, window=window)
+    for n, x in zip(("dq", "dk", "dv"), got):
+        ref.check(x, want[n], where + " " + n)
+    return got
+
+
+@pytest.mark.parametrize("window", [(-1, 0), (-1, -1), (90, 0)], ids=str)
+@pytest.mark.parametrize("G", [1, 3])
+@pytest.mark.parametrize("r", [1, 12, 18])
+def test_one_large_row_of_dout_in_fp16(bd, r, G, window):
+    """An early row's dO is 2^r times the others': it takes nothing from the keys that it does not see, nor from those that
+    it hardly looks at."""
+    t = {n: torch.randn(1500, 2 * G if n in "qg" else 2, 64, generator=torch.Generator().manual_seed(i)).to(F16)
+         for i, n in enumerate("qkvg")}
+    t["g"] *= 2.0 ** -6
+    t["g"][1, 0] *= 2.0 ** r
+    fp16_gradients(bd, t, window, 0.125, str(r))
