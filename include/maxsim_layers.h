@@ -77,8 +77,8 @@ int maxsim_rope(const maxsim_view* x, const maxsim_view* y, int32_t B, int32_t L
  * the matrix cores take it; each output is rounded once.  Keys that no query of their sequence sees are not read and
  * may hold anything (entries dropped from a cache; their gradients are 0).  A NaN elsewhere in a
  * sequence reaches all rows that see it and may reach rows near them that do not; so does an infinity, but for a score of
- * -infinity, whose weight is 0 (a query with no other score counts as one that sees no key).  fp16 gradients pass dO (v_j - out),
- * with dO's row scaled to at most 2, through fp16: sure to hold while |v| <= 128, and beyond that where that product does.
+ * -infinity, whose weight is 0 (a query with no other score counts as one that sees no key).  In fp16, P and dS are
+ * rounded in the scale of the row's (dK, dV: the key's) largest ones, so that dO and v may be of any size that fp16 holds.
  * Requires data 16-byte aligned and steps multiples of 8, token steps of at least D and at most 2^20; D a multiple of 8 from 8 to 128;
  * Hq a multiple of Hk; 0 <= max_q * (Hq / Hk), max_k < 2^29; 2^-60 <= scale <= 2^60; sinks >= 0; and tiles of
  * 128 rows, of queries (max_q * (Hq / Hk)) or keys, of which B * Hk times one more than there are stay below 2^21.

@@ -32,14 +32,8 @@ constexpr bool is_f16() {
     return std::is_same<T, _Float16>::value;
 }
 // fp16 holds P and dS for their products only if they are brought into its range by powers of 2, which are
-// exact: P (at most 1, 1 / keys where attention is flat) times 2^8; dS by the size of its row's dO in dQ, and in dK by the
-// largest dS that the key has met so far.
+// exact: P (at most 1, 1 / keys where attention is flat) times 2^8; dS by the largest that the row of the result has met so far.
 constexpr float kLiftP = 8.f;  // log2
-// The power of 2 that brings a row of dO with the largest magnitude `top` into [1, 2); 1 for a row of zeros.
-__device__ __forceinline__ float lift_of(float top) {
-    const int e = (int)((fbits(top) >> 23) & 255u);
-    return e == 0 || e == 255 ? 1.f : __uint_as_float((uint32_t)(254 - e) << 23);
-}
 // The factor of dS (fp16) of one row of the result, which the sum at hand holds too: it brought the largest magnitude at the time
 // it was set to [2^7, 2^8), and stays until one passes 2^15.  So a value is held to fp16's half step or to 2^-32 of the
 // largest one of the same sum, whichever is more, whatever the rows' dO, v and P are.
@@ -60,6 +54,23 @@ struct Lift {
         return true;
     }
 };
+
+// A block of dS, 16 values in either lane of a pair, by that factor, with the sums brought to it where it changes.
+template <int DB>
+__device__ __forceinline__ void lifted(f32x16& x, f32x16* sums, Lift& lift) {
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = larger(m, __builtin_fabsf(x[i]));
+    int shift;
+    if (lift.take(swap_max(m), shift)) {
+#pragma unroll
+        for (int db = 0; db < DB; ++db)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sums[db][i] = __builtin_ldexpf(sums[db][i], shift);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] *= lift.factor();
+}
 
 // The first token past the window of all of a key tile's keys.
 __device__ __forceinline__ int far_from(const maxsim_attn& a, const Seq& s, int j0) {
@@ -117,7 +128,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
     const T* orow = first<T>(a.out, packed, b, s.q0, 0) + (int64_t)token * a.out.token + (int64_t)head * a.out.head;
     const int64_t at = first_row(a, s, b) + token;
     const T* rest = rest_of<T>(p, at * a.Hq + head);
-    float delta = 0.f, top = 0.f;
+    float delta = 0.f;
 #pragma unroll
     for (int kk = 0; kk < KS; ++kk) {
         const int c = 16 * kk + 8 * (lane >> 5);
@@ -129,13 +140,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
         for (int i = 0; i < 8; ++i) off[i] = (T)0.f;
         if (rest && c < D) off = *reinterpret_cast<const typename Pack8<T>::V*>(rest + c);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            delta = __builtin_fmaf((float)g[kk][i], (float)o[i] + (float)off[i], delta);
-            if (is_f16<T>()) top = fmaxf(top, __builtin_fabsf((float)g[kk][i]));
-        }
+        for (int i = 0; i < 8; ++i) delta = __builtin_fmaf((float)g[kk][i], (float)o[i] + (float)off[i], delta);
     }
     delta = swap_sum(delta);
-    top = is_f16<T>() ? swap_max(top) : 0.f;
     float lse = p.lse[(at * a.Hq + head) * a.lse_step] * kLog2e;
     if (lse == -INFINITY) lse = INFINITY;
     if (mine && lane < 32) {
@@ -143,7 +150,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
         stat[0] = is_f16<T>() ? lse - kLiftP : lse;
         stat[p.rows * a.Hq] = delta;
     }
-    const float lift = is_f16<T>() ? lift_of(top) : 1.f;
+    Lift lift;  // of what acc holds (fp16)
+    lift.start();
     const Place place = place_of<DP>(lane);
 
     const int p_lo = min(wr, rows - 1) / G + shift, p_hi = min(wr + 31, rows - 1) / G + shift, pos = token + shift;
@@ -176,7 +184,8 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
                 for (int i = 0; i < 16; ++i) x[i] = keep(bits, i, x[i], 0u);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] *= is_f16<T>() ? (dp[i] - delta) * lift : dp[i] - delta;
+            for (int i = 0; i < 16; ++i) x[i] *= dp[i] - delta;
+            if constexpr (is_f16<T>()) lifted<DB>(x, acc, lift);
 #pragma unroll
             for (int t2 = 0; t2 < 2; ++t2) {
                 const V8 ds = pack8<T>(x, 8 * t2);
@@ -195,7 +204,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
         work(t + 1, k_1, v_1);
     }
     T* out = first<T>(p.dq, packed, b, s.q0, 0) + (int64_t)token * p.dq.token + (int64_t)head * p.dq.head;
-    store_row<T, DB>(out, mine, acc, a.scale / lift, lane, D);
+    store_row<T, DB>(out, mine, acc, is_f16<T>() ? a.scale * lift.inverse() : a.scale, lane, D);
 }
 
 // A workgroup's 128 keys of one key head, 32 of a wave; the query heads that share it one after the other, TR tokens
@@ -357,20 +366,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 3 : WAVES) void attn_dkv_ke
 #pragma unroll
                 for (int i = 0; i < 4; ++i) x[4 * q + i] *= dp[4 * q + i] - d[i];
             }
-            if constexpr (is_f16<T>()) {
-                float m = 0.f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) m = larger(m, __builtin_fabsf(x[i]));
-                int shift;
-                if (lift.take(swap_max(m), shift)) {
-#pragma unroll
-                    for (int db = 0; db < DB; ++db)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) dk[db][i] = __builtin_ldexpf(dk[db][i], shift);
-                }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) x[i] *= lift.factor();
-            }
+            if constexpr (is_f16<T>()) lifted<DB>(x, dk, lift);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const V8 ds = pack8<T>(x, 8 * t);

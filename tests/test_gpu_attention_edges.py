@@ -160,3 +160,23 @@ def test_one_large_row_of_dout_in_fp16(bd, r, G, window):
     t["g"] *= 2.0 ** -6
     t["g"][1, 0] *= 2.0 ** r
     fp16_gradients(bd, t, window, 0.125, str(r))
+
+
+@pytest.mark.parametrize("window", [(-1, 0), (3, 0)], ids=str)
+@pytest.mark.parametrize("vsize,gsize", [(200.0, 1.0), (8000.0, 2.0 ** -6), (8000.0, 2.0 ** -20), (2.0 ** -12, 2000.0)], ids=str)
+def test_values_and_gradients_of_any_size_in_fp16(bd, vsize, gsize, window):
+    """dO v^T of up to millions times what fp16 holds beside a row's dO, and far below its smallest values."""
+    t = {n: torch.randn(300, 2, 64, generator=torch.Generator().manual_seed(i)) for i, n in enumerate("qkvg")}
+    t["v"] *= vsize
+    t["g"] *= gsize
+    got = fp16_gradients(bd, {n: x.to(F16) for n, x in t.items()}, window, 0.125, "%g %g" % (vsize, gsize))
+    assert all(torch.isfinite(x).all() for x in got)
+
+
+def test_large_values_that_agree_with_dout_in_fp16(bd):
+    """dO of one sign and v of either, a key's all the same: dO (v - out) is 128 columns times 30000 times dO."""
+    t = {n: torch.randn(200, 1, 128, generator=torch.Generator().manual_seed(i)) for i, n in enumerate("qkvg")}
+    t["v"] = torch.where(t["v"][..., :1] > 0, 30000.0, -30000.0).expand(200, 1, 128)
+    t["g"] = torch.full((200, 1, 128), 2.0 ** -10)
+    got = fp16_gradients(bd, {n: x.to(F16).contiguous() for n, x in t.items()}, (4, 2), 128 ** -0.5, "agree")
+    assert all(torch.isfinite(x).all() for x in got)
