@@ -70,7 +70,8 @@ int maxsim_rope(const maxsim_view* x, const maxsim_view* y, int32_t B, int32_t L
  *   max_q, max_k  bounds of the lengths (longer ones are cut)
  *   lse       fp32 out, or NULL: log of the sum of exp(S_ij), of row and head n = (b * max_q + i) * Hq + h (packed:
  *             row * Hq + h) at lse[n * lse_step].  lse_step 1, or at least 1 + D/2: then the D values of dtype behind
- *             each hold what rounding left off out, which keeps rowsum(dO * out) of the backward exact
+ *             each hold what rounding left off out, which keeps rowsum(dO * out) of the backward exact (the backward
+ *             takes of them what is half a step of out at most, so that other memory there costs no more than rounding does)
  * Rows of no sequence (past a sequence's length, before the first one, past the last one) are not read; in
  * outputs they are left as they were, or made 0 where zero_rest is not 0.  B = 0 enqueues nothing.
  * Scores, statistics and sums are fp32; P (and in the backward dS) is rounded to dtype for its product, as

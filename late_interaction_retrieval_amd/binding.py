@@ -1367,7 +1367,8 @@ def _attn(q, k, v, out, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q,
 
 
 def _lse_step(lse, q):
-    """The step of lse, a number for each row of q: 1, or that of maxsim_attn_fwd's, behind whose numbers more is kept."""
+    """The step of lse, a number for each row of q: 1, or that of maxsim_attn_fwd's, behind whose numbers more is kept.  (Of what
+    lies behind a caller's own the kernel takes only what rounding could have left off out.)"""
     if lse.device != q.device or lse.dtype != torch.float32 or lse.shape != q.shape[:-1]:
         raise ValueError("lse must be %s float32 on %s" % (tuple(q.shape[:-1]), q.device))
     if lse.is_contiguous() or lse.numel() == 0:
@@ -1398,9 +1399,9 @@ def maxsim_attn_fwd(q, k, v, scale=None, window=(-1, -1), sinks=0, q_lens=None, 
     k_lens [B] int32 where sequences are shorter; or packed [T, H, D] with cu_q, cu_k [B + 1] int32 and bounds max_q,
     max_k of the lengths.  Query i stands at p = i + Lk - Lq of its sequence and sees key j where j <= p + window[1] and
     (j >= p - window[0] or j < sinks); -1 is no bound, so window (-1, 0) is causal.  scale: of q k, 1 / sqrt(D) if None.
-    Returns (out as q, lse [..., Hq] fp32 or None).  The lse made here is a view whose memory also keeps, for the backward,
-    what rounding left off out; a contiguous one does for it too, with a less exact rowsum(dO * out).  Rows of no sequence are zeros in outputs made here, and left as
-    they were in those that are given.
+    Returns (out as q, lse [..., Hq] fp32 or None).  The lse made here is a view of [..., Hq, 1 + D / 2], whose memory also
+    keeps, for the backward, what rounding left off out (as many bytes as out); a contiguous one does for it too, with a less exact
+    rowsum(dO * out).  Rows of no sequence are zeros in outputs made here, and left as they were in those that are given.
     """
     if out is None and lse is None and workspace is None and stream is None:
         got = _fast.attn_fwd(q, k, v, scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q, max_k, with_lse)

@@ -31,6 +31,9 @@ template <typename T>
 constexpr bool is_f16() {
     return std::is_same<T, _Float16>::value;
 }
+// Half a step of a value of 1.
+template <typename T>
+constexpr float kHalfStep = is_f16<T>() ? 0x1p-11f : 0x1p-8f;
 // fp16 holds P and dS for their products only if they are brought into its range by powers of 2, which are
 // exact: P (at most 1, 1 / keys where attention is flat) times 2^8; dS by the largest that the row of the result has met so far.
 constexpr float kLiftP = 8.f;  // log2
@@ -139,6 +142,11 @@ __global__ __launch_bounds__(64 * kWaves, 2) void attn_dq_kernel(AttnArgs p, int
 #pragma unroll
         for (int i = 0; i < 8; ++i) off[i] = (T)0.f;
         if (rest && c < D) off = *reinterpret_cast<const typename Pack8<T>::V*>(rest + c);
+        // what rounding left off out is half a step of it at most (of fp16's subnormal values nothing, which is 0 as T): more
+        // than that, or a NaN, is something else that lies behind the caller's lse, and left out
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(__builtin_fabsf((float)off[i]) <= __builtin_fabsf((float)o[i]) * kHalfStep<T>)) off[i] = (T)0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) delta = __builtin_fmaf((float)g[kk][i], (float)o[i] + (float)off[i], delta);
     }

@@ -1,4 +1,7 @@
 """Attention at the edges of what its calls allow, forward and backward, on the device.  Run on an MI355X: pytest -m gpu."""
+import functools
+import types
+
 import pytest
 import torch
 
@@ -180,3 +183,31 @@ def test_large_values_that_agree_with_dout_in_fp16(bd):
     t["g"] = torch.full((200, 1, 128), 2.0 ** -10)
     got = fp16_gradients(bd, {n: x.to(F16).contiguous() for n, x in t.items()}, (4, 2), 128 ** -0.5, "agree")
     assert all(torch.isfinite(x).all() for x in got)
+
+
+@pytest.mark.parametrize("general", [False, True])
+@pytest.mark.parametrize("dtype,D", [(BF16, 64), (F16, 40)], ids=str)
+@pytest.mark.parametrize("behind", ["large", "nan", "zeros", "anything"])
+def test_an_lse_in_the_callers_own_memory(bd, behind, dtype, D, general):
+    """A view of the forward's steps with something else behind its numbers: as a contiguous lse, or, where that happens to be
+    as small as what rounding leaves, off by as much again."""
+    if general:
+        bd = types.SimpleNamespace(**{n: functools.partial(getattr(bd, n), stream=torch.cuda.current_stream())
+                                      for n in ("maxsim_attn_fwd", "maxsim_attn_bwd")})
+    t = {n: torch.randn(2 * 90, 4 if n in "qg" else 2, D, generator=torch.Generator().manual_seed(i)).to(dtype)
+         for i, n in enumerate("qkvg")}
+    d = {n: x.to(DEV).reshape(2, 90, -1, D) for n, x in t.items()}
+    out, lse = bd.maxsim_attn_fwd(d["q"], d["k"], d["v"], window=(20, 0), with_lse=True)
+    lens = [(0, 90, 0, 90), (90, 90, 90, 90)]
+    exact, want = (ref.attention(t["q"], t["k"], t["v"], lens, D ** -0.5, (20, 0), 0, t["g"], exact_rest=e) for e in (True, False))
+    plain = bd.maxsim_attn_bwd(d["g"], d["q"], d["k"], d["v"], out, lse.contiguous(), window=(20, 0))
+    own = torch.randn(2, 90, 4, 1 + D // 2, generator=torch.Generator().manual_seed(9)).to(DEV)
+    if behind != "anything":
+        own.view(dtype).fill_({"large": 3.0, "nan": NAN, "zeros": 0.0}[behind])
+    own[..., 0] = lse
+    got = bd.maxsim_attn_bwd(d["g"], d["q"], d["k"], d["v"], out, own[..., 0], window=(20, 0))
+    for n, a, b in zip(("dq", "dk", "dv"), got, plain):
+        if behind != "anything":
+            assert torch.equal(a, b), n
+        ref.check(b, want[n], n)
+        ref.check(a, (want[n][0], want[n][1] + 1.02 * (want[n][1] - exact[n][1])), n)
