@@ -1476,7 +1476,7 @@ def _loadable(t):
     steps = t.stride()
     ok = steps[-1] == 1 and t.data_ptr() % 16 == 0 and all(s % 8 == 0 for s in steps[:-1]) and \
         (t.shape[-3] <= 1 or t.shape[-1] <= steps[-3] <= 1 << 20)
-    return t if ok else t.contiguous()
+    return t if ok else t.clone(memory_format=torch.contiguous_format)  # (contiguous() is t itself where only its start is off)
 
 
 class AttentionFunction(torch.autograd.Function):

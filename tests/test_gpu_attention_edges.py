@@ -211,3 +211,20 @@ def test_an_lse_in_the_callers_own_memory(bd, behind, dtype, D, general):
             assert torch.equal(a, b), n
         ref.check(b, want[n], n)
         ref.check(a, (want[n][0], want[n][1] + 1.02 * (want[n][1] - exact[n][1])), n)
+
+
+@pytest.mark.parametrize("at", [1, 4])
+def test_autograd_of_rows_that_start_anywhere(bd, at):
+    """Contiguous q, k, v and a contiguous dO whose memory starts 2 or 8 bytes off 16: the same bits as aligned ones."""
+    def off(t):
+        flat = torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)
+        return flat[at:at + t.numel()].copy_(t.flatten()).view(t.shape)
+
+    q, k, v, g = (rand(2, 40, 4, 64, dtype=F16, seed=i) for i in range(4))
+    want = torch.autograd.grad(bd.attention(*(x := [t.requires_grad_() for t in (q, k, v)]), window=(9, 0)), x, g)
+    x = [off(t.detach()).requires_grad_() for t in (q, k, v)]
+    assert x[0].is_contiguous() and x[0].data_ptr() % 16
+    o = bd.attention(*x, window=(9, 0))
+    assert torch.equal(o, bd.attention(q, k, v, window=(9, 0)))
+    for a, b in zip(torch.autograd.grad(o, x, off(g)), want):
+        assert torch.equal(a, b)

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 from late_interaction_retrieval_amd import binding as bd
 
@@ -29,3 +30,20 @@ def test_no_queries_are_not_split_over_keys(max_k, packed):
     assert bd.lib().maxsim_attn_fwd_workspace_bytes(ctypes.byref(a)) == 0
     if max_k >= 4096:  # one query is split
         assert bd.lib().maxsim_attn_fwd_workspace_bytes(ctypes.byref(attn(max_q=1, max_k=max_k))) > 0
+
+
+def test_rows_that_no_tile_can_be_loaded_from_are_copied():
+    """attention() takes views of any layout: a contiguous one that starts off 16 bytes too."""
+    flat = torch.zeros(2 * 3 * 4 * 64 + 8, dtype=torch.bfloat16)
+    for at in (1, 4):
+        t = flat[at:at + 2 * 3 * 4 * 64].view(2, 3, 4, 64)
+        assert t.is_contiguous() and t.data_ptr() % 16 != 0
+        u = bd._loadable(t)
+        assert u.data_ptr() % 16 == 0 and u.is_contiguous() and torch.equal(u, t)
+    whole = flat[:2 * 3 * 4 * 64].view(2, 3, 4, 64)
+    assert bd._loadable(whole) is whole
+    some = whole[:, :1, :, :36]  # rows of 72 bytes, 128 apart
+    assert bd._loadable(some) is some
+    for t in (whole.transpose(-1, -2), whole[:, :, :, 4:], whole[:, :, :, ::2]):
+        u = bd._loadable(t)
+        assert u.data_ptr() % 16 == 0 and u.is_contiguous() and torch.equal(u, t)
