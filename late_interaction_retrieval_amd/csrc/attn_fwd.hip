@@ -36,10 +36,13 @@ constexpr int kKeys = 64;                      // of a tile
 constexpr int kKeysFew = 32;                   // of a wave's own tile, with few rows
 
 // A wave's state for its 32 rows: out^T and, for the lane's row, the reference of the exponents in
-// units of the scores and the sum of this lane's keys.
+// units of the scores and the sum of this lane's keys.  out^T and the sum hold P times 2^LIFT, a power of 2 that costs nothing: in fp16 a
+// weight then keeps a step of 2^-31 of the largest one's instead of 2^-24, which 65536 keys of 2^-25.5 behind a first
+// token would fall below together, 1 / 700 of the row.
 template <typename T, int DP>
 struct Rows {
     static constexpr int KS = DP / 16, DB = DP / 32;
+    static constexpr float LIFT = std::is_same<T, _Float16>::value ? 7.f : 0.f;  // log2
     typename Vec8<T>::V q[KS];
     f32x16 o[DB];
     float ref, sum;
@@ -58,6 +61,9 @@ struct Rows {
         hi = min(pos + a.right, lk - 1);
     }
 
+    // The exponent, in powers of 2, that the sum is in units of; `none` of a row that has seen nothing.
+    __device__ __forceinline__ float top(float c, float none) const { return ref == -INFINITY ? none : ref * c - LIFT; }
+
     // Which of a block's keys from j0 on, before `end`, the lane's row sees.
     __device__ __forceinline__ uint32_t bits(int j0, int end, int sinks, int lane) const {
         const int j = j0 + 4 * (lane >> 5);
@@ -65,8 +71,11 @@ struct Rows {
     }
 
     // NB blocks of 32 keys.  all: every row sees all of them; else bits[nb] are the lane's.
-    // The reference stays while the maximum passes it by less than 2^8: P grows to 256 at most, which both types hold,
-    // and relative to the row's sum nothing is lost.
+    // The reference stays while the maximum passes it by less than 2^8: P grows to 256 at most (2^15 with LIFT), which both
+    // types hold, and relative to the row's sum nothing is lost.  P is rounded to T for its product: the matrix instruction
+    // takes both operands in one type, and v comes in T.  (That
+    // takes out's error from the 0.0017 of its norm that its own rounding makes in bf16 to 0.0022 - 0.0023, in fp16 from 0.00020 to 0.00024;
+    // P in two halves would take the product twice.)
     template <int NB>
     __device__ __forceinline__ void step(const uint8_t* kt, const uint8_t* vt, bool all, const uint32_t* bits, float c, float slack) {
         f32x16 s[NB];
@@ -98,7 +107,7 @@ struct Rows {
 #pragma unroll
                 for (int i = 0; i < 16; ++i) o[db][i] *= f;
         }
-        const float base = ref == -INFINITY ? 0.f : -ref * c;  // a row that has seen nothing yet
+        const float base = ref == -INFINITY ? 0.f : LIFT - ref * c;  // a row that has seen nothing yet
         float part[4] = {0.f, 0.f, 0.f, 0.f};  // chains that do not wait for each other
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -196,7 +205,7 @@ __global__ __launch_bounds__(64 * kWaves, DP == 64 ? 4 : 2) void attn_fwd_kernel
         work(t + 1, k_1, v_1);
     }
 
-    const float sum = swap_sum(row.sum), top = row.ref == -INFINITY ? 0.f : row.ref * c;
+    const float sum = swap_sum(row.sum), top = row.top(c, 0.f);
     const bool mine = wr + (lane & 31) < rows;
     const int64_t at = (first_row(a, s, w.b) + token) * a.Hq + head;
     if (p.splits == 1) {
@@ -295,7 +304,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_few_kernel(AttnArgs p
     }
 
     // the waves' parts: references and sums first, then out^T, scaled to the largest reference, added in order
-    const float sum = swap_sum(row.sum), top = row.ref == -INFINITY ? -INFINITY : row.ref * c;
+    const float sum = swap_sum(row.sum), top = row.top(c, -INFINITY);
     if (lane < 32) {
         joined[wave][lane][0] = top;
         joined[wave][lane][1] = sum;

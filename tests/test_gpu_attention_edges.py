@@ -228,3 +228,19 @@ def test_autograd_of_rows_that_start_anywhere(bd, at):
     assert torch.equal(o, bd.attention(q, k, v, window=(9, 0)))
     for a, b in zip(torch.autograd.grad(o, x, off(g)), want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=str)
+@pytest.mark.parametrize("nq,Lk", [(1, 600), (1, 65537), (150, 600), (150, 20001)])
+def test_many_keys_of_small_weights_behind_a_first_token(bd, nq, Lk, dtype):
+    """The first key's weight is 2^25.5 times each other's, which have all of the values: together they are 1 / 700 of the row
+    at 65537 keys.  In fp16 a weight is held to half a step of 2^-31 of the largest."""
+    q, k = torch.zeros(nq, 1, 64, dtype=dtype), torch.zeros(Lk, 1, 64, dtype=dtype)
+    v = torch.randn(Lk, 1, 64, generator=torch.Generator().manual_seed(3)).abs().to(dtype)
+    q[:], k[0], v[0] = 0.5, 17.6875 / 32, 0.0  # a score of 17.6875 (in bf16 17.75)
+    want = ref.attention(q, k, v, [(0, nq, 0, Lk)], 1.0, (-1, -1), 0)
+    if dtype == F16:
+        want["out"][1][:] -= (2.0 ** -25 - 2.0 ** -32) * v.double().sum(0)
+    out, lse = bd.maxsim_attn_fwd(*(t[None].to(DEV) for t in (q, k, v)), scale=1.0, with_lse=True)
+    ref.check(out, want["out"], "out")
+    ref.check(lse, want["lse"], "lse")
