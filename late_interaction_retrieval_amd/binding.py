@@ -1289,6 +1289,8 @@ def _rope(x, inv_freq, positions, offsets, layout, scale, inverse, out):
     _flat(inv_freq, "inv_freq", rotary // 2, torch.float64, dev)
     if positions is not None:
         _flat(positions, "positions", B * L, torch.int32, dev)
+        if positions.dim() != 1 and positions.shape != shape[:-2]:
+            raise ValueError("positions must be %s, got %s" % (tuple(shape[:-2]), tuple(positions.shape)))
     if offsets is not None:
         _flat(offsets, "offsets", B, torch.int32, dev)
     xv = _view(x, "x", shape, x.dtype, dev)
@@ -1524,6 +1526,8 @@ def _distill_sizes(scores, index, teacher):
     (N, V), K, dev = map(_size, scores.shape), _size(index.shape[1]), scores.device
     _flat(index, "index", N * K, torch.int32, dev)
     _flat(teacher, "teacher", N * K, torch.float32, dev)
+    if teacher.dim() != 1 and teacher.shape != index.shape:
+        raise ValueError("teacher must be %s as index, got %s" % (tuple(index.shape), tuple(teacher.shape)))
     return N, V, K, _code(scores.dtype, _FLOATS, "scores"), _rows(scores, "scores", scores.shape, scores.dtype, dev)
 
 

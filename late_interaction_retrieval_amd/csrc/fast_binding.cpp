@@ -338,7 +338,8 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     maxsim_view xv, yv;
     const int32_t *p, *o;
     if (!is_float(code) || !fits(B) || !fits(L) || !fits(H) || !fits(D) || !good(*f, at::kDouble, dev) || !fits(2 * f->numel()) ||
-        !int32s(pos, B * L, dev, &p) || !int32s(off, B, dev, &o) || !view_of(*x, x->sizes(), x->scalar_type(), dev, xv))
+        !int32s(pos, B * L, dev, &p) || (pos && pos->dim() != 1 && pos->sizes() != x->sizes().slice(0, x->dim() - 2)) ||
+        !int32s(off, B, dev, &o) || !view_of(*x, x->sizes(), x->scalar_type(), dev, xv))
         Py_RETURN_NONE;
     Tensor y = empty(x->sizes(), *x, x->scalar_type());
     view_of(y, x->sizes(), x->scalar_type(), dev, yv);
@@ -456,7 +457,8 @@ bool distill_of(const Tensor* z, const Tensor* index, const Tensor* teacher, PyO
         !z->is_contiguous() || !is_float(code_of(z->scalar_type())))
         return false;
     return good(*index, at::kInt, z->device()) && index->size(0) == z->size(0) && good(*teacher, at::kFloat, z->device()) &&
-           teacher->numel() == index->numel() && fits(z->size(0)) && fits(z->size(1)) && fits(index->size(1));
+           teacher->numel() == index->numel() && (teacher->dim() == 1 || teacher->sizes() == index->sizes()) &&
+           fits(z->size(0)) && fits(z->size(1)) && fits(index->size(1));
 }
 
 // (scores, index, teacher, temperature) -> (loss, stat)

@@ -47,3 +47,24 @@ def test_rows_that_no_tile_can_be_loaded_from_are_copied():
     for t in (whole.transpose(-1, -2), whole[:, :, :, 4:], whole[:, :, :, ::2]):
         u = bd._loadable(t)
         assert u.data_ptr() % 16 == 0 and u.is_contiguous() and torch.equal(u, t)
+
+
+def meta(*shape, dtype):
+    return torch.empty(shape, dtype=dtype, device="meta")
+
+
+def test_a_teacher_of_another_shape_is_refused():
+    """As many values in other rows: [K, N] for [N, K]; a flat list of all rows' is taken."""
+    raw = bd._distill_fwd.__wrapped__
+    z, i = meta(4, 9, dtype=torch.float32), meta(4, 2, dtype=torch.int32)
+    for bad in ((2, 4), (1, 8), (4, 2, 1)):
+        with pytest.raises(ValueError, match="teacher"):
+            raw(z, i, meta(*bad, dtype=torch.float32), 1.0, None, None, None)
+
+
+def test_positions_of_another_shape_are_refused():
+    """[L, B] for [B, L]; a flat list of all tokens' is taken."""
+    raw, x, f = bd._rope.__wrapped__, meta(2, 3, 4, 64, dtype=torch.bfloat16), meta(32, dtype=torch.float64)
+    for bad in ((3, 2), (1, 6), (2, 3, 1)):
+        with pytest.raises(ValueError, match="positions"):
+            raw(x, f, meta(*bad, dtype=torch.int32), None, "half", 1.0, False, None)
