@@ -64,7 +64,7 @@ int maxsim_rope(const maxsim_view* x, const maxsim_view* y, int32_t B, int32_t L
  *     S_ij = scale * sum_c q_ic k_jc;  P = softmax over the keys that i sees;  out_i = sum_j P_ij v_j
  * A query that sees no key gives zeros (lse -infinity, no gradient).
  *   q, out    [B, max_q, Hq, D], or, with cu_q, packed [rows_q, Hq, D] (batch step not used):
- *             sequence b is rows [cu_q[b], cu_q[b + 1])
+ *             sequence b is rows [cu_q[b], cu_q[b + 1]); starts may not decrease (else rows of the outputs are unspecified)
  *   k, v      [B, max_k, Hk, D], or, with cu_k, packed [rows_k, Hk, D]
  *   q_lens    [B] int32: Lq(b), without cu_q; NULL: max_q for all.  k_lens likewise.
  *   max_q, max_k  bounds of the lengths (longer ones are cut)

@@ -371,8 +371,25 @@ __device__ __forceinline__ void zero_rest(const maxsim_view& v, float* lse, int 
     zero_rows<T>(first<T>(v, cu != nullptr, b, row0, 0), v.token, v.head, lse ? lse + at * heads * lse_step : nullptr, lse_step,
                  (int64_t)len + part, all, parts, heads, D);
     if (!cu) return;
-    zero_rows<T>((T*)v.data, v.token, v.head, lse, lse_step, item, clamp64(((cint_ptr)cu)[0], 0, rows), items, heads, D);
-    zero_rows<T>((T*)v.data, v.token, v.head, lse, lse_step, clamp64(((cint_ptr)cu)[B], 0, rows) + item, rows, items, heads, D);
+    int64_t low = clamp64(((cint_ptr)cu)[0], 0, rows), high = clamp64(((cint_ptr)cu)[B], 0, rows);
+    if (low > 0 || high < rows) {  // should the starts not be in order, another workgroup's sequence may lie there: past all of them
+        int least = INT32_MAX, most = 0;
+        for (int i = threadIdx.x & 63; i < B; i += 64) {
+            const int from = cu[i], to = cu[i + 1];
+            if (from >= to) continue;
+            least = min(least, from);
+            most = max(most, to);
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            least = min(least, __shfl_xor(least, d));
+            most = max(most, __shfl_xor(most, d));
+        }
+        low = clamp64(least, 0, rows);  // (of no rows at all in any sequence, all)
+        high = max(clamp64(most, 0, rows), low);
+    }
+    zero_rows<T>((T*)v.data, v.token, v.head, lse, lse_step, item, low, items, heads, D);
+    zero_rows<T>((T*)v.data, v.token, v.head, lse, lse_step, high + item, rows, items, heads, D);
 }
 
 }  // namespace

@@ -244,3 +244,36 @@ def test_many_keys_of_small_weights_behind_a_first_token(bd, nq, Lk, dtype):
     out, lse = bd.maxsim_attn_fwd(*(t[None].to(DEV) for t in (q, k, v)), scale=1.0, with_lse=True)
     ref.check(out, want["out"], "out")
     ref.check(lse, want["lse"], "lse")
+
+
+def test_starts_out_of_order(bd):
+    """Starts that no caller should pass: rows that one sequence of them owns are that sequence's, though they lie past the
+    last start or before the first; rows past all of them are zeros."""
+    n = 90
+    q, k, v, g = (rand(n, 2, 64, dtype=F16, seed=i) for i in range(4))
+    for starts, a, b in (([20, 60, 40], 20, 60), ([50, 10, 40], 10, 40), ([70, 70, 5, 70], 5, 70)):
+        cu = torch.tensor(starts, dtype=torch.int32, device=DEV)
+        one = torch.tensor([a, b], dtype=torch.int32, device=DEV)
+        got, want = [], []
+        for to, c in ((got, cu), (want, one)):
+            how = dict(cu_q=c, cu_k=c, max_q=n, max_k=n, window=(9, 0))
+            out, lse = bd.maxsim_attn_fwd(q, k, v, with_lse=True, **how)
+            to += [out, lse, *bd.maxsim_attn_bwd(g, q, k, v, out, lse, **how)]
+        for x, y in zip(got, want):
+            assert torch.equal(x, y) and torch.all(x[:a] == 0) and torch.all(x[b:] == 0), starts
+
+
+@pytest.mark.parametrize("window", [(-1, 0), (30, 5)], ids=str)
+def test_many_short_sequences_in_fp16(bd, window):
+    """More key tiles than CUs at a width of 128: two workgroups of dK and dV to a CU."""
+    n = [1 + 13 * i % 120 for i in range(75)]
+    t = {m: torch.randn(sum(n), 4, 128, generator=torch.Generator().manual_seed(i)).to(F16) for i, m in enumerate("qkvg")}
+    cu = [0] + torch.tensor(n).cumsum(0).tolist()
+    want = ref.attention(t["q"], t["k"], t["v"], [(a, m, a, m) for a, m in zip(cu, n)], 128 ** -0.5, window, 0, t["g"])
+    d = {m: x.to(DEV) for m, x in t.items()}
+    starts = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    how = dict(window=window, cu_q=starts, cu_k=starts, max_q=max(n), max_k=max(n))
+    out, lse = bd.maxsim_attn_fwd(d["q"], d["k"], d["v"], with_lse=True, **how)
+    got = dict(out=out, lse=lse, **dict(zip(("dq", "dk", "dv"), bd.maxsim_attn_bwd(d["g"], d["q"], d["k"], d["v"], out, lse, **how))))
+    for m in got:
+        ref.check(got[m], want[m], m)
