@@ -23,10 +23,12 @@ namespace {
 constexpr int kMostEntries = 1024;
 constexpr size_t kLastCache = (size_t)256 << 20;  // bytes
 constexpr int kThreads = 256;
-// Columns that one wave takes by itself.  Forward (us with a wave to a row, and with four): 10393 x 2887 fp32 39, 46; 16384 x 1500
-// bf16 21, 47; 4096 x 4096 bf16 13, 17; 600 x 6000 bf16 7.7, 7.4; 16384 x 8192 bf16 91, 87.  Backward, whose four waves share the
-// entries: 10393 x 2887 fp32 53, 49; 512 x 2887 fp32 9.9, 6.6; 128 x 1500 fp32 6.7, 4.8; 16384 x 1500 bf16 28, 33.
-constexpr int kShortForward = 4096, kShortRow = 1024;
+// Columns that one wave takes by itself.  Forward (us with a wave to a row, and with four; 16 entries): many rows, up to 4096 columns:
+// 10393 x 2887 fp32 24, 36; 4096 x 4096 bf16 9.8, 15; 1024 x 4096 bf16 5.1, 5.9; 1024 x 512 fp32 3.6, 5.1 (but 600 x 6000 bf16 7.7,
+// 7.4; 16384 x 8192 bf16 91, 87).  Rows that leave a CU few waves (kFewRows), up to 2048: 256 x 512 fp32 3.6, 4.1; 16 x 1500 fp32 4.0, 4.1, with
+// 100 entries 4.4, 4.2; but 64 x 2887 fp32 4.8, 4.4; 256 x 4096 bf16 5.0, 4.4, with 100 entries 5.6, 4.5.  Backward, whose four waves share
+// the entries: 10393 x 2887 fp32 53, 49; 512 x 2887 fp32 9.9, 6.6; 128 x 1500 fp32 6.7, 4.8; 16384 x 1500 bf16 28, 33.
+constexpr int kShortForward = 4096, kShortFew = 2048, kFewRows = 512, kShortRow = 1024;
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -341,7 +343,7 @@ hipError_t fwd(const DistillArgs& a, hipStream_t stream) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         distill_finish_kernel<TT><<<(unsigned)a.N, 64, 0, stream>>>(a, d.splits);
-    } else if (a.V <= kShortForward) {
+    } else if (a.V <= (a.N < kFewRows ? kShortFew : kShortForward)) {
         distill_fwd_kernel<TT, 64><<<(unsigned)ceil_div(a.N, kThreads / 64), kThreads, 0, stream>>>(a);
     } else {
         distill_fwd_kernel<TT, kThreads><<<(unsigned)a.N, kThreads, 0, stream>>>(a);

@@ -3,6 +3,8 @@ pytest -m gpu."""
 import pytest
 import torch
 
+import layers_ref as ref
+
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
@@ -35,3 +37,16 @@ def test_arguments_of_as_many_values_in_other_rows(bd, general):
     assert torch.equal(bd.maxsim_rope(x, f, positions=at.flatten(), **how), want)
     with pytest.raises(ValueError, match="positions"):
         bd.maxsim_rope(x, f, positions=at.t().contiguous(), **how)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=str)
+@pytest.mark.parametrize("N,V,K", [(511, 2048, 5), (511, 2049, 70), (512, 2049, 70), (512, 4096, 3), (512, 4097, 3)])
+def test_rows_about_as_many_as_leave_a_wave_to_each(bd, N, V, K, dtype):
+    g = torch.Generator().manual_seed(N + V)
+    z, index = (3 * torch.randn(N, V, generator=g)).to(dtype), torch.randint(-1, V, (N, K), generator=g, dtype=torch.int32)
+    teacher, dloss = 3 * torch.randn(N, K, generator=g), torch.rand(N, generator=g) + 0.5
+    want = ref.distill(z, index, teacher, 0.8, dloss)
+    d = [t.to(DEV) for t in (z, index, teacher, dloss)]
+    loss, stat = bd.maxsim_distill_fwd(*d[:3], temperature=0.8)
+    ref.check(loss, want["loss"], "loss")
+    ref.check(bd.maxsim_distill_bwd(d[3], d[0], stat, *d[1:3], temperature=0.8), want["dscores"], "dscores")
