@@ -1482,7 +1482,8 @@ def _loadable(t):
 
 
 class AttentionFunction(torch.autograd.Function):
-    """Attention as an autograd op: of the forward only the output and a number for each row are kept."""
+    """Attention as an autograd op.  Kept for the backward beside q, k and v: the output, a number for each row and what rounding
+    left off the output, about twice the output's bytes in all."""
 
     @staticmethod
     def forward(ctx, q, k, v, cu_q, cu_k, q_lens, k_lens, how):

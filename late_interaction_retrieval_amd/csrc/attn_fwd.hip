@@ -318,7 +318,6 @@ __global__ __launch_bounds__(64 * kWaves, 1) void attn_fwd_few_kernel(AttnArgs p
     for (int i = 0; i < kWaves; ++i)
         total += joined[i][lane & 31][0] == -INFINITY ? 0.f : joined[i][lane & 31][1] * __builtin_amdgcn_exp2f(joined[i][lane & 31][0] - most);
     constexpr int BLOCK = 16 * 64 * 4;  // bytes of a block of 32 columns: register by register, 64 lanes each
-    static_assert(R::DB * BLOCK <= 2 * kWaves * BYTES, "a wave's part fits two arrays' share");
     // wave i's part in array i
     uint8_t* const mem = wave == 0 ? k_0 : wave == 1 ? v_0 : wave == 2 ? k_1 : v_1;
     static_assert(R::DB * BLOCK <= kWaves * BYTES, "a wave's part fits an array");

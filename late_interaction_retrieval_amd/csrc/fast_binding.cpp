@@ -306,13 +306,8 @@ bool int32s(const Tensor* t, int64_t n, at::Device dev, const int32_t** to) {
     *to = t->data_ptr<int32_t>();
     return true;
 }
-// An int that fits 32 bits; None where `none` is given.
-bool int_of(PyObject* o, int32_t& to, const int64_t* none = nullptr) {
-    if (none && o == Py_None) {
-        if (!fits(*none)) return false;
-        to = (int32_t)*none;
-        return true;
-    }
+// An int that fits 32 bits.
+bool int_of(PyObject* o, int32_t& to) {
     if (!PyLong_Check(o)) return false;
     const long v = PyLong_AsLong(o);
     if (v == -1 && PyErr_Occurred()) PyErr_Clear();
@@ -350,7 +345,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// The ten arguments that attention's two directions share (scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q,
+// The nine arguments that attention's two directions share (scale, window, sinks, q_lens, k_lens, cu_q, cu_k, max_q,
 // max_k from a[0] on) with q, k and v, as the library's struct.  False: not a plain call.
 bool attn_of(const Tensor& q, const Tensor& k, const Tensor& v, PyObject* const* a, maxsim_attn& s) {
     bool plain = PyTuple_Check(a[1]) && PyTuple_GET_SIZE(a[1]) == 2 && (a[0] == Py_None || PyFloat_Check(a[0]));
