@@ -46,8 +46,9 @@ enum { MAXSIM_ROPE_HALF = 0 /* (i, i + rotary/2) */, MAXSIM_ROPE_INTERLEAVED = 1
  *              the frequencies) are in these values and in `scale`.
  *   positions  [B, L] int32: each token's position; or NULL: offsets[b] + t, and t where that is
  *   offsets    [B] int32, or NULL.  (Not both.)
- * The angle is formed in fp64 and brought into one turn before it is rounded, so that far positions
- * lose nothing; sine and cosine are fp32.  Rows need the alignment of one element (16 bytes are fastest).
+ * The angle is formed in fp64 and brought into one turn before it is rounded to fp32 (off by pi 2^-24 at most), so that far
+ * positions lose nothing; sine, cosine and their products with scale are fp32, each rounded (an fp32 result is off by 5e-8 of
+ * its norm, one made with fp64 factors by 4e-8).  Rows need the alignment of one element (16 bytes are fastest).
  * Requires B, L >= 0, H >= 1, 1 <= D <= 1024, rotary even, 2 <= rotary <= D, B * L < 2^25 and scale finite.
  */
 int maxsim_rope(const maxsim_view* x, const maxsim_view* y, int32_t B, int32_t L, int32_t H, int32_t D, int32_t rotary,

@@ -1239,7 +1239,8 @@ def rope_frequencies(rotary, base=10000.0, stretch=1.0, kind="parts", length=409
     """(inv_freq [rotary / 2] fp64, scale) for rope: base^(-2 i / rotary), stretched for contexts `stretch` times as long as
     the `length` that the weights were trained on.  kind "linear": every frequency is divided by stretch; "base": the base
     grows so that the slowest is; "parts": pairs that make fewer than `slow` turns over `length` are divided, those
-    with more than `fast` stay, and those between are mixed, with scale 1 + 0.1 ln(stretch)."""
+    with more than `fast` stay, and those between are mixed, in the proportion of their turns (not of their index i), with scale
+    1 + 0.1 ln(stretch).  Any other frequencies and scale go to rope as they are."""
     if rotary < 2 or rotary % 2:
         raise ValueError("rotary must be even, got %d" % rotary)
     if kind not in ("linear", "base", "parts"):
