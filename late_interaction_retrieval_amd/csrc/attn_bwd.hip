@@ -12,12 +12,12 @@
 // type.  Each is held to half a step of T (fp16: brought into its range first, below), which averages out over many keys: the
 // gradients' error is 0.0024 of their norm in bf16 and 0.0003 in fp16, where their own rounding makes 0.0017 and 0.0002.
 //
-// Bound as the forward is.  Measured, the kernels alone (bf16):
-//     2 x 4096 tokens, 16 / 4 heads of 128, all pairs     dQ 375 us (1.10 PFLOP/s of its three products), dK and dV 550 + 14 (1.0 of four)
-//     2 x 4096 tokens, 32 heads of 64, all pairs          dQ 415, dK and dV 545
-//     16 documents of 700 to 1024 tokens, 16 / 4 heads of 128    dQ 190 - 197, dK and dV 237 - 248
-//     9 sequences of up to 601 tokens, 100 back and the first 3, 6 / 2 heads of 80, fp16    dQ 14.5, dK and dV 23.5 + 6: the way of a
-//                                                         few tiles through one wave
+// Bound as the forward is.  Measured, the kernels alone once the clocks have settled (bf16):
+//     2 x 4096 tokens, 16 / 4 heads of 128, all pairs     dQ 376 us (1.10 PFLOP/s of its three products), dK and dV 506 + 14 (1.09 of four)
+//     2 x 4096 tokens, 32 heads of 64, all pairs          dQ 415, dK and dV 535
+//     16 documents of 700 to 1024 tokens, 16 / 4 heads of 128    dQ 182, dK and dV 216 (matrix pipes 39 % and 47 % of their cycles)
+//     9 sequences of up to 601 tokens, 100 back and the first 3, 6 / 2 heads of 80, fp16    dQ 15.5, dK and dV 24.2 + 6.3: the way of a
+//                                                         few tiles through one wave (of it the largest dS of each block 1 and 1)
 // Tried and slower: 64 keys to a wave (its 512 registers move through the accumulator half: 340 us for 247); k's operands in
 // registers beside two waves to a SIMD (memory takes what does not fit, and waits for the next tile's loads: 494).
 #include <algorithm>

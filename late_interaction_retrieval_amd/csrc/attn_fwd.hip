@@ -10,15 +10,17 @@
 //
 // What bounds it: with many keys the matrix pipes and the exponentials together (a 64 x 32 tile at a width of 128 is
 // 1024 cycles of matrix instructions and about 900 of the vector unit, half of them exponentials at a quarter of its rate);
-// two waves to a SIMD overlap them to 52 % of the matrix pipes' cycles.  LDS has no bank conflicts.  A next
-// token is bound by the cache's bytes.  Measured, the kernels alone:
-//     8192 tokens, causal, 2048 back and the first 4, 32 / 8 heads of 128, bf16     260 us, 0.93 PFLOP/s of the pairs that see
-//                                                                            each other (library product of 8192^3: 1.2 - 1.4)
-//     2 x 4096 tokens, 16 / 4 heads of 128, all pairs                        275 us, 1.00 PFLOP/s
-//     2 x 4096 tokens, 32 heads of 64, all pairs                             313 us, 0.88 PFLOP/s
-//     64 packed documents of 32 to 1024 tokens, 128 to each side and the first, 16 heads of 64    84 - 89 us: the vector unit (79 %
-//                                              of a resident wave's share), 3616 workgroups in 3.5 rounds, 4576 that find nothing
-//     16 next tokens, caches of 8192 to 32768 keys, 8 key heads of 128       266 us + 6.6 the join, 1.45 GB at 5.4 TB/s
+// two waves to a SIMD overlap them to 52 % of the matrix pipes' cycles and 48 % of the vector unit's.  LDS has no bank conflicts.  A next
+// token is bound by the cache's bytes.  Measured, the kernels alone once the clocks have settled (the first 40 to 100 passes after other work
+// take 10 to 18 % longer; a library product of 8192^3 reaches 1.39 PFLOP/s then):
+//     8192 tokens, causal, 2048 back and the first 4, 32 / 8 heads of 128, bf16     251 - 258 us, 0.93 - 0.96 PFLOP/s of the pairs that
+//                                                                            see each other
+//     2 x 4096 tokens, 16 / 4 heads of 128, all pairs                        276 us, 1.00 PFLOP/s
+//     2 x 4096 tokens, 32 heads of 64, all pairs                             310 us, 0.89 PFLOP/s
+//     64 packed documents of 32 to 1024 tokens, 128 to each side and the first, 16 heads of 64    80 - 81 us: the vector unit (56 % of its
+//                                              cycles, the matrix pipes 20 %; 3 waves to a SIMD on average), 3616 workgroups in 3.5 rounds, 4576
+//                                              that find nothing
+//     16 next tokens, caches of 8192 to 32768 keys, 8 key heads of 128       267 us + 6.5 the join, 1.45 GB at 5.4 TB/s
 // Tried and slower: the next tile's scores made beside this one's softmax (through the branches between them the compiler
 // moves the accumulators to memory: 8 times the time); leaving out hidden blocks of 32 keys, or their exponentials, by
 // branches (89 -> 98 and 117 us); first tokens in blocks of 32 before the window's tiles (no difference).

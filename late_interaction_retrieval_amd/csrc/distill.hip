@@ -10,8 +10,8 @@
 // workgroups.  Differences z - max are formed before they are multiplied by 1 / T, and the backward gets
 // the maximum and the sum's logarithm apart, so that large scores at a low temperature lose nothing.
 //
-// Measured, the kernels alone: 8192 x 32768 bf16 forward 122 - 131 us (537 MB at 4.1 - 4.4 TB/s), backward 207 - 215 (1.07 GB at
-// 5.0 - 5.2); 10393 x 2887 fp32 36 and 48; 32 x 200003 fp32 forward 7.4 + 4.6 (the parts' join), backward 12.3; 64 x 64 4.8 and 5.4, a launch each.
+// Measured, the kernels alone: 8192 x 32768 bf16 forward 120 - 131 us (537 MB at 4.1 - 4.5 TB/s), backward 207 - 215 (1.07 GB at
+// 5.0 - 5.2); 10393 x 2887 fp32 36 and 48; 32 x 200003 fp32 forward 7.2 + 4.4 (the parts' join), backward 11.9; 64 x 64 4.4 and 5.5, a launch each.
 #include <algorithm>
 
 #include "encoder_dev.h"
@@ -23,7 +23,7 @@ namespace {
 constexpr int kMostEntries = 1024;
 constexpr size_t kLastCache = (size_t)256 << 20;  // bytes
 constexpr int kThreads = 256;
-// Columns that one wave takes by itself.  Forward (us with a wave to a row, and with four; 16 entries): many rows, up to 4096 columns:
+// Columns that one wave takes by itself.  Forward (us with a wave to a row, and with four; 16 entries, scores in the last cache): many rows, up to 4096 columns:
 // 10393 x 2887 fp32 24, 36; 4096 x 4096 bf16 9.8, 15; 1024 x 4096 bf16 5.1, 5.9; 1024 x 512 fp32 3.6, 5.1 (but 600 x 6000 bf16 7.7,
 // 7.4; 16384 x 8192 bf16 91, 87).  Rows that leave a CU few waves (kFewRows), up to 2048: 256 x 512 fp32 3.6, 4.1; 16 x 1500 fp32 4.0, 4.1, with
 // 100 entries 4.4, 4.2; but 64 x 2887 fp32 4.8, 4.4; 256 x 4096 bf16 5.0, 4.4, with 100 entries 5.6, 4.5.  Backward, whose four waves share
