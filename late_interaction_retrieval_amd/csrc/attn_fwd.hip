@@ -13,7 +13,7 @@
 // two waves to a SIMD overlap them to 52 % of the matrix pipes' cycles and 48 % of the vector unit's.  LDS has no bank conflicts.  A next
 // token is bound by the cache's bytes.  Measured, the kernels alone once the clocks have settled (the first 40 to 100 passes after other work
 // take 10 to 18 % longer; a library product of 8192^3 reaches 1.39 PFLOP/s then):
-//     8192 tokens, causal, 2048 back and the first 4, 32 / 8 heads of 128, bf16     251 - 258 us, 0.93 - 0.96 PFLOP/s of the pairs that
+//     8192 tokens, causal, 2048 back and the first 4, 32 / 8 heads of 128, bf16     251 - 271 us over cards, 0.89 - 0.96 PFLOP/s of the pairs that
 //                                                                            see each other
 //     2 x 4096 tokens, 16 / 4 heads of 128, all pairs                        276 us, 1.00 PFLOP/s
 //     2 x 4096 tokens, 32 heads of 64, all pairs                             310 us, 0.89 PFLOP/s
